@@ -57,10 +57,16 @@ enum {
 
 enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 };
 
+/* Activations of the linear's epilogue: silu z/(1+exp(-z)); gelu z Phi(z) (the normal
+ * distribution function); gelu_tanh z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_GELU_TANH = 3 };
+
 #define NVFP4_BLOCK_SIZE 16
 #define NVFP4_SCALE_TILE_K 128
 #define NVFP4_MAX_ROTATION_GROUP 128
 #define NVFP4_WORKSPACE_ALIGN 256
+#define NVFP4_CHECKPOINT_BLOCK 32
+#define NVFP4_NORM_MAX_K 16384
 #define NVFP4_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)   /* nvfp4_linear_noalloc's fixed device scratch */
 
 /* Alignment.  Every call checks its pointers and returns NVFP4_ERR_ARG for a misaligned
@@ -72,7 +78,10 @@ enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 };
  *   - bf16 outputs and biases of the linear and GEMM calls (out, bias): 2 bytes (the
  *     kernels take wide stores and loads only where the address allows them);
  *   - fp32 scalars (global scales, gsf_out, amax): 4 bytes;
- *   - workspaces: NVFP4_WORKSPACE_ALIGN.
+ *   - workspaces: NVFP4_WORKSPACE_ALIGN;
+ *   - every array of the RMS norm, checkpoint and gradient calls: 16 bytes, except fp32
+ *     scalars and the norm's grad_w (4), checkpoint scales (bytes: any address), and the
+ *     residual and preact of a linear's epilogue (2).
  * The scale-layout converters access bytes and need no alignment. */
 
 /* Bytes of a block-scale array for a [rows, k] tensor in the layout above. */
@@ -295,6 +304,130 @@ int nvfp4_linear_swiglu(const void* gate_dev, const void* up_dev, int64_t m, int
  */
 int nvfp4_dequantize(const uint8_t* packed_dev, const uint8_t* scale_dev, int64_t rows, int64_t k,
                      const float* global_sf_dev, void* out_dev, int out_dtype, void* stream);
+
+/*
+ * nvfp4_linear_epilogue: nvfp4_linear with an activation and a residual in the epilogue.
+ * With z the bf16 output of nvfp4_linear for the same arguments,
+ *     out = bf16(residual + act(z)),   act and the sum in fp32, one rounding.
+ * activation: NVFP4_ACT_*.  residual_dev: bf16 [m][out_features], NULL for none; it may be
+ * out_dev itself (the update in place of a residual stream), but not overlap it otherwise.
+ * preact_dev: NULL, or bf16 [m][out_features] that receives z (nvfp4_activation_backward
+ * takes it); it overlaps neither.  up_dev: NULL, or the input is the SwiGLU product of
+ * x_dev (gate) and up_dev as in nvfp4_linear_swiglu (rotation_group 0; z is then that
+ * call's output).  workspace: that of nvfp4_linear, or of nvfp4_linear_swiglu with up_dev.
+ */
+int nvfp4_linear_epilogue(const void* x_dev, const void* up_dev, int64_t m, int64_t k,
+                          const uint8_t* packed_dev, const uint8_t* inv_scale_dev, const float* global_sf_w_dev,
+                          const void* bias_dev, int64_t out_features, const float* global_sf_x_dev,
+                          int rotation_group, int activation, const void* residual_dev, void* preact_dev,
+                          void* out_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* nvfp4_gemm_epilogue: the same epilogue on nvfp4_gemm (z its bf16 output). */
+int nvfp4_gemm_epilogue(const uint8_t* x_codes_dev, const uint8_t* x_scale_dev, int64_t m, int64_t k,
+                        const uint8_t* packed_dev, const uint8_t* inv_scale_dev, int64_t n,
+                        const float* gsf_x_dev, const float* gsf_w_dev, const void* bias_dev, int activation,
+                        const void* residual_dev, void* preact_dev, void* out_dev, void* workspace_dev,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_rmsnorm: the RMS norm with the residual's addition.  Per row of k values
+ *     r = x + residual            (fp32, rounded to the residual's type; r = x without one)
+ *     s = fp32(1 / sqrt(sum(r^2) / k + eps))      (the sum in fp64: the same bits in any order)
+ *     y = bf16(fp32(fp32(r * s) * weight))
+ * x_dev [rows][k] of x_dtype, residual_dev NULL or [rows][k] of residual_dtype (fp32 when
+ * x is), weight_dev [k] of weight_dtype (each NVFP4_DTYPE_*).  residual_out_dev receives r
+ * in the residual's type; it may be residual_dev, or x_dev of that type (unused without a
+ * residual).  y_dev bf16 [rows][k].  ck_codes_dev / ck_scales_dev: both NULL, or y's 8-bit
+ * checkpoint (nvfp4_checkpoint_pack of y_dev, bit for bit).  k: a multiple of 16, at most
+ * NVFP4_NORM_MAX_K.  eps >= 0.
+ */
+int nvfp4_rmsnorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                  const void* weight_dev, int weight_dtype, int64_t rows, int64_t k, float eps,
+                  void* residual_out_dev, void* y_dev, uint8_t* ck_codes_dev, uint8_t* ck_scales_dev, void* stream);
+
+/*
+ * nvfp4_quantize_rmsnorm: nvfp4_quantize_activation (no rotation) of nvfp4_rmsnorm's y,
+ * which is never written: the same codes, scales and global scale, bit for bit.
+ * global_sf_dev NULL = dynamic scale, with a workspace of
+ * nvfp4_quantize_rmsnorm_workspace_bytes(rows); else the static scale it points to (no
+ * workspace).  gsf_out_dev: NULL, or receives the scale used.  Other arguments as above.
+ */
+size_t nvfp4_quantize_rmsnorm_workspace_bytes(int64_t rows);
+int nvfp4_quantize_rmsnorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                           const void* weight_dev, int weight_dtype, int64_t rows, int64_t k, float eps,
+                           const float* global_sf_dev, void* residual_out_dev, uint8_t* codes_dev,
+                           uint8_t* scales_dev, float* gsf_out_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * nvfp4_rmsnorm_backward: the gradient of the norm at r (x itself, or the sum that
+ * nvfp4_rmsnorm stored), the rounding of y taken as the identity.  With g = grad_y * weight
+ * and d = sum(g r) over the row,
+ *     grad_r = s g - r s^3 d / k + grad_residual,     grad_w = sum over rows of grad_y r s.
+ * grad_y_dev bf16; r_dev, grad_residual_dev (NULL = none: the gradient that reaches r by
+ * the residual stream) and grad_r_dev [rows][k] of r_dtype.  grad_r is the gradient of x
+ * and of the residual alike.  grad_w_dev: fp32 [k], or NULL (then no workspace).  The row
+ * partials of grad_w are added in a fixed order: results repeat bit for bit.
+ */
+size_t nvfp4_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t k);
+int nvfp4_rmsnorm_backward(const void* grad_y_dev, const void* r_dev, int r_dtype, const void* weight_dev,
+                           int weight_dtype, const void* grad_residual_dev, int64_t rows, int64_t k, float eps,
+                           void* grad_r_dev, float* grad_w_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * 8-bit activation checkpoints: what a training forward keeps of a bf16 [rows][k] tensor
+ * for its backward, in 8.25 bits a value.  codes [rows][k]: E4M3 (bias 7, finite max 448).
+ * scales [rows][ceil(k / 32)]: one byte s per 32 values of a row (the last block may hold
+ * 16); value = code * 2^(s - 127), exact in bf16.  2^(s - 127) is the smallest power of
+ * two, from 2^-110 to 2^120, that brings the block's largest finite magnitude to 448 or
+ * below; codes round to nearest even, so a value moves by at most 2^-4 of itself (or 2^-10
+ * of 2^(s - 127), if that is more).  Infinities and NaN become NaN.
+ * nvfp4_checkpoint_pack: x_dev bf16; rotation_group as for nvfp4_quantize_activation (the
+ * checkpoint holds the rotated, bf16-rounded values).  k: a multiple of 16.
+ * nvfp4_checkpoint_unpack: the values, to bf16 or fp32 [rows][k].
+ */
+size_t nvfp4_checkpoint_scale_bytes(int64_t rows, int64_t k);
+int nvfp4_checkpoint_pack(const void* x_dev, int64_t rows, int64_t k, int rotation_group, uint8_t* codes_dev,
+                          uint8_t* scales_dev, void* stream);
+int nvfp4_checkpoint_unpack(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t rows, int64_t k,
+                            void* out_dev, int out_dtype, void* stream);
+
+/* nvfp4_swiglu_checkpoint: nvfp4_swiglu, and the checkpoints of gate and up, in one pass. */
+int nvfp4_swiglu_checkpoint(const void* gate_dev, const void* up_dev, int64_t rows, int64_t k, void* x_dev,
+                            uint8_t* gate_codes_dev, uint8_t* gate_scales_dev, uint8_t* up_codes_dev,
+                            uint8_t* up_scales_dev, void* stream);
+
+/*
+ * nvfp4_swiglu_backward: with x = silu(g) u,
+ *     grad_gate = bf16(grad_x u silu'(g)),   grad_up = bf16(grad_x silu(g)),   fp32 inside.
+ * gate_dev / up_dev: checkpoint codes with their scales, or (both scales NULL) bf16.
+ */
+int nvfp4_swiglu_backward(const void* grad_x_dev, const void* gate_dev, const uint8_t* gate_scales_dev,
+                          const void* up_dev, const uint8_t* up_scales_dev, int64_t rows, int64_t k,
+                          void* grad_gate_dev, void* grad_up_dev, void* stream);
+
+/*
+ * nvfp4_activation_backward: grad_z = bf16(grad_y act'(z)), the gradient of a linear's
+ * epilogue.  z_dev: the preact of nvfp4_linear_epilogue (bf16 [rows][n], z_scales_dev
+ * NULL, any n), or its checkpoint (n a multiple of 16).
+ */
+int nvfp4_activation_backward(const void* grad_y_dev, const void* z_dev, const uint8_t* z_scales_dev, int64_t rows,
+                              int64_t n, int activation, void* grad_z_dev, void* stream);
+
+/*
+ * nvfp4_weight_grad: a linear's weight gradient from the checkpoint of its input,
+ *     grad_w[i][j] = sum over rows r of grad_y[r][i] * x[r][j]
+ * grad_y_dev bf16 [m][n], codes_dev / scales_dev a checkpoint of [m][k].  Products are
+ * exact, sums fp32.  grad_w_dev [n][k] of out_dtype.  m = 0 writes zeros.  workspace_dev:
+ * NULL, or 256-byte aligned; with nvfp4_weight_grad_workspace_bytes(m, n, k) bytes the rows
+ * are split across workgroups (joined in a fixed order) where n x k alone would not fill
+ * the GPU.  Depends on the compute-unit count of the current device.
+ */
+size_t nvfp4_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int nvfp4_weight_grad(const void* grad_y_dev, int64_t m, int64_t n, const uint8_t* codes_dev,
+                      const uint8_t* scales_dev, int64_t k, void* grad_w_dev, int out_dtype, void* workspace_dev,
+                      size_t workspace_bytes, void* stream);
 
 /* Scale-layout conversion: layout above <-> row-major [rows][k/16] bytes. */
 int nvfp4_scale_to_canonical(const uint8_t* layout_dev, uint8_t* canonical_dev,

@@ -19,12 +19,17 @@ NVFP4_ERR_WORKSPACE = -3
 NVFP4_ERR_HIP = -4
 NVFP4_DTYPE_BF16 = 0
 NVFP4_DTYPE_F32 = 1
+NVFP4_ACT_NONE = 0
+NVFP4_ACT_SILU = 1
+NVFP4_ACT_GELU = 2
+NVFP4_ACT_GELU_TANH = 3
 NVFP4_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes), in header order
 SIGNATURES = {
@@ -50,6 +55,24 @@ SIGNATURES = {
     "nvfp4_linear_noalloc": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _int, _vp, _vp]),
     "nvfp4_linear_segmented": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _int, _vp, _vp, _vp, _sz,
                                       _vp]),
+    "nvfp4_linear_epilogue": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _int, _int, _vp, _vp, _vp, _vp,
+                                     _sz, _vp]),
+    "nvfp4_gemm_epilogue": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _sz,
+                                   _vp]),
+    "nvfp4_rmsnorm": (_int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_quantize_rmsnorm_workspace_bytes": (_sz, [_i64]),
+    "nvfp4_quantize_rmsnorm": (_int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _sz, _vp]),
+    "nvfp4_rmsnorm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_rmsnorm_backward": (_int, [_vp, _vp, _int, _vp, _int, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_checkpoint_scale_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_checkpoint_pack": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp]),
+    "nvfp4_checkpoint_unpack": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _vp]),
+    "nvfp4_swiglu_checkpoint": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_swiglu_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "nvfp4_activation_backward": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp]),
+    "nvfp4_weight_grad_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_weight_grad": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _sz, _vp]),
     "nvfp4_scale_to_canonical": (_int, [_vp, _vp, _i64, _i64, _vp]),
     "nvfp4_scale_from_canonical": (_int, [_vp, _vp, _i64, _i64, _vp]),
     "nvfp4_last_error": (ctypes.c_char_p, []),

@@ -183,7 +183,8 @@ int check_segments(const char* fn, int64_t segments, int64_t seg_rows) {
 int linear_impl(const char* fn, const void* x, int64_t segments, int64_t seg_rows, int64_t k, const uint8_t* packed,
                 const uint8_t* inv_scale, const float* global_sf_w, const void* bias, int64_t out_features,
                 const float* global_sf_x, int rotation_group, void* out, float* gsf_out, void* workspace,
-                size_t workspace_bytes, hipStream_t s, const void* up = nullptr, bool split_k = true) {
+                size_t workspace_bytes, hipStream_t s, const void* up = nullptr, bool split_k = true,
+                const nvfp4::Epilogue& ep = {}) {
   // a dynamic scale over a SwiGLU product keeps the product after the linear workspace
   Range call(fn);
   const bool keep_product = up != nullptr && global_sf_x == nullptr;
@@ -217,7 +218,7 @@ int linear_impl(const char* fn, const void* x, int64_t segments, int64_t seg_row
     return hip_status(nvfp4::launch_linear_decode_fused(static_cast<const uint16_t*>(x), k, packed, inv_scale,
                                                         out_features, global_sf_x,
                                                         global_sf_x != nullptr ? gsf_out : gsf, global_sf_w,
-                                                        static_cast<const uint16_t*>(bias),
+                                                        static_cast<const uint16_t*>(bias), ep,
                                                         static_cast<uint16_t*>(out), ws.gemm, ws.gemm_bytes,
                                                         nvfp4::compute_units(), s),
                       fn);
@@ -234,11 +235,11 @@ int linear_impl(const char* fn, const void* x, int64_t segments, int64_t seg_row
   Range stage("nvfp4.gemm");
   if (a16)
     return hip_status(nvfp4::launch_gemm_decode_a16(ws.a16, m, k, packed, inv_scale, out_features, gsf, global_sf_w,
-                                                    static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(out),
+                                                    static_cast<const uint16_t*>(bias), ep, static_cast<uint16_t*>(out),
                                                     ws.gemm, ws.gemm_bytes, nvfp4::compute_units(), s),
                       fn);
   return hip_status(nvfp4::launch_gemm(ws.codes, ws.scales, m, k, packed, inv_scale, out_features, gsf, global_sf_w,
-                                       per_segment ? seg_rows : 0, static_cast<const uint16_t*>(bias),
+                                       per_segment ? seg_rows : 0, static_cast<const uint16_t*>(bias), ep,
                                        static_cast<uint16_t*>(out), ws.gemm, ws.gemm_bytes, s),
                     fn);
 }
@@ -269,6 +270,99 @@ int scratch_of_current_device(const char* fn, void** ptr) {
   }
   *ptr = g_scratch_dev[dev];
   return NVFP4_OK;
+}
+
+
+// Epilogue arguments of a linear or GEMM writing bf16 [m][n] to out.
+int check_activation(const char* fn, int activation) {
+  if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU_TANH)
+    return fail(NVFP4_ERR_ARG, "%s: unknown activation %d", fn, activation);
+  return NVFP4_OK;
+}
+int make_epilogue(const char* fn, int activation, const void* residual, void* preact, const void* out,
+                  nvfp4::Epilogue* ep) {
+  if (int rc = check_activation(fn, activation)) return rc;
+  if (int rc = check_align(fn, "residual", residual, 2)) return rc;
+  if (int rc = check_align(fn, "preact", preact, 2)) return rc;
+  if (preact != nullptr && (preact == out || preact == residual))
+    return fail(NVFP4_ERR_ARG, "%s: preact must not be out or residual", fn);
+  ep->residual = static_cast<const uint16_t*>(residual);
+  ep->preact = static_cast<uint16_t*>(preact);
+  ep->act = activation;
+  return NVFP4_OK;
+}
+
+bool is_dtype(int d) { return d == NVFP4_DTYPE_BF16 || d == NVFP4_DTYPE_F32; }
+
+// Shapes, types and pointers the RMS norm forms share; fills the common part of the
+// launcher's arguments.
+int check_norm(const char* fn, int64_t rows, int64_t k, float eps) {
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (k > nvfp4::kNormMaxK)
+    return fail(NVFP4_ERR_SHAPE, "%s: K must be at most %lld, got %lld", fn, (long long)nvfp4::kNormMaxK, (long long)k);
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(NVFP4_ERR_ARG, "%s: eps must be a finite number >= 0", fn);
+  return NVFP4_OK;
+}
+int norm_inputs(const char* fn, const void* x, int x_dtype, const void* residual, int residual_dtype,
+                const void* weight, int weight_dtype, int64_t rows, int64_t k, float eps, void* residual_out,
+                nvfp4::NormForward* a) {
+  if (int rc = check_norm(fn, rows, k, eps)) return rc;
+  if (!is_dtype(x_dtype) || !is_dtype(weight_dtype) || (residual != nullptr && !is_dtype(residual_dtype)))
+    return fail(NVFP4_ERR_ARG, "%s: dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if (residual != nullptr && x_dtype == NVFP4_DTYPE_F32 && residual_dtype != NVFP4_DTYPE_F32)
+    return fail(NVFP4_ERR_ARG, "%s: an fp32 x needs an fp32 residual", fn);
+  if (rows > 0 && (!x || !weight || (residual != nullptr && !residual_out)))
+    return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "x", x)) return rc;
+  if (int rc = check_aligned(fn, "residual", residual)) return rc;
+  if (int rc = check_aligned(fn, "weight", weight)) return rc;
+  if (int rc = check_aligned(fn, "residual_out", residual_out)) return rc;
+  *a = nvfp4::NormForward{};
+  a->x = x;
+  a->residual = residual;
+  a->w = weight;
+  a->r = residual != nullptr ? residual_out : nullptr;
+  a->rows = rows;
+  a->k = k;
+  a->eps = (double)eps;
+  a->x_f32 = x_dtype == NVFP4_DTYPE_F32;
+  a->stream_f32 = residual != nullptr ? residual_dtype == NVFP4_DTYPE_F32 : a->x_f32;
+  a->w_f32 = weight_dtype == NVFP4_DTYPE_F32;
+  return NVFP4_OK;
+}
+
+int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (need > 0 && (!workspace || bytes < need || ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN)))
+    return fail(NVFP4_ERR_WORKSPACE, "%s: need a %d-byte aligned workspace of %zu bytes, got %zu", fn,
+                NVFP4_WORKSPACE_ALIGN, need, bytes);
+  return NVFP4_OK;
+}
+
+// A saved operand: checkpoint codes with scales, or bf16 (scales NULL).
+int check_saved(const char* fn, const char* name, const void* saved) {
+  if (!saved) return fail(NVFP4_ERR_ARG, "%s: %s must not be NULL", fn, name);
+  return check_aligned(fn, name, saved);
+}
+
+int gemm_impl(const char* fn, const uint8_t* x_codes, const uint8_t* x_scale, int64_t m, int64_t k, const uint8_t* packed,
+              const uint8_t* inv_scale, int64_t n, const float* gsf_x, const float* gsf_w, const void* bias,
+              void* out, void* workspace, size_t workspace_bytes, void* stream, const nvfp4::Epilogue& ep = {}) {
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, m, k, true)) return rc;
+  if (n <= 0 || n >= kMaxDim) return fail(NVFP4_ERR_SHAPE, "%s: out_features must be in [1, 2^31), got %lld", fn, (long long)n);
+  if (m == 0) return NVFP4_OK;
+  if (!x_codes || !x_scale || !packed || !inv_scale || !gsf_x || !gsf_w || !out)
+    return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_nvfp4_operand(fn, "x_codes", x_codes, "x_scale", x_scale)) return rc;
+  if (int rc = check_nvfp4_operand(fn, "packed", packed, "inv_scale", inv_scale)) return rc;
+  if (int rc = check_epilogue(fn, out, bias, gsf_x, gsf_w)) return rc;
+  if (workspace != nullptr && ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN))
+    return fail(NVFP4_ERR_WORKSPACE, "%s: workspace must be %d-byte aligned", fn, NVFP4_WORKSPACE_ALIGN);
+  return hip_status(nvfp4::launch_gemm(x_codes, x_scale, m, k, packed, inv_scale, n, gsf_x, gsf_w, 0,
+                                       static_cast<const uint16_t*>(bias), ep, static_cast<uint16_t*>(out), workspace,
+                                       workspace != nullptr ? workspace_bytes : 0, static_cast<hipStream_t>(stream)),
+                    fn);
 }
 
 }  // namespace
@@ -503,23 +597,8 @@ int nvfp4_quantize_activation_segmented(const void* x, int64_t segments, int64_t
 int nvfp4_gemm(const uint8_t* x_codes, const uint8_t* x_scale, int64_t m, int64_t k, const uint8_t* packed,
                const uint8_t* inv_scale, int64_t n, const float* gsf_x, const float* gsf_w, const void* bias,
                void* out, void* workspace, size_t workspace_bytes, void* stream) {
-  const char* fn = "nvfp4_gemm";
-  Range call(fn);
-  g_err[0] = 0;
-  if (int rc = check_rows_k(fn, m, k, true)) return rc;
-  if (n <= 0 || n >= kMaxDim) return fail(NVFP4_ERR_SHAPE, "%s: out_features must be in [1, 2^31), got %lld", fn, (long long)n);
-  if (m == 0) return NVFP4_OK;
-  if (!x_codes || !x_scale || !packed || !inv_scale || !gsf_x || !gsf_w || !out)
-    return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
-  if (int rc = check_nvfp4_operand(fn, "x_codes", x_codes, "x_scale", x_scale)) return rc;
-  if (int rc = check_nvfp4_operand(fn, "packed", packed, "inv_scale", inv_scale)) return rc;
-  if (int rc = check_epilogue(fn, out, bias, gsf_x, gsf_w)) return rc;
-  if (workspace != nullptr && ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN))
-    return fail(NVFP4_ERR_WORKSPACE, "%s: workspace must be %d-byte aligned", fn, NVFP4_WORKSPACE_ALIGN);
-  return hip_status(nvfp4::launch_gemm(x_codes, x_scale, m, k, packed, inv_scale, n, gsf_x, gsf_w, 0,
-                                       static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(out), workspace,
-                                       workspace != nullptr ? workspace_bytes : 0, static_cast<hipStream_t>(stream)),
-                    fn);
+  return gemm_impl("nvfp4_gemm", x_codes, x_scale, m, k, packed, inv_scale, n, gsf_x, gsf_w, bias, out, workspace,
+                   workspace_bytes, stream);
 }
 
 int nvfp4_linear(const void* x, int64_t m, int64_t k, const uint8_t* packed, const uint8_t* inv_scale,
@@ -583,6 +662,258 @@ int nvfp4_scale_from_canonical(const uint8_t* canonical, uint8_t* layout, int64_
   if (rows == 0) return NVFP4_OK;
   if (!layout || !canonical) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
   return hip_status(nvfp4::launch_scale_layout(canonical, layout, rows, k, false, static_cast<hipStream_t>(stream)), fn);
+}
+
+int nvfp4_gemm_epilogue(const uint8_t* x_codes, const uint8_t* x_scale, int64_t m, int64_t k, const uint8_t* packed,
+                        const uint8_t* inv_scale, int64_t n, const float* gsf_x, const float* gsf_w, const void* bias,
+                        int activation, const void* residual, void* preact, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_gemm_epilogue";
+  g_err[0] = 0;
+  nvfp4::Epilogue ep;
+  if (int rc = make_epilogue(fn, activation, residual, preact, out, &ep)) return rc;
+  return gemm_impl(fn, x_codes, x_scale, m, k, packed, inv_scale, n, gsf_x, gsf_w, bias, out, workspace,
+                   workspace_bytes, stream, ep);
+}
+
+int nvfp4_linear_epilogue(const void* x, const void* up, int64_t m, int64_t k, const uint8_t* packed,
+                          const uint8_t* inv_scale, const float* global_sf_w, const void* bias, int64_t out_features,
+                          const float* global_sf_x, int rotation_group, int activation, const void* residual,
+                          void* preact, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_linear_epilogue";
+  g_err[0] = 0;
+  nvfp4::Epilogue ep;
+  if (int rc = make_epilogue(fn, activation, residual, preact, out, &ep)) return rc;
+  if (up != nullptr && rotation_group != 0)
+    return fail(NVFP4_ERR_ARG, "%s: a SwiGLU input takes no rotation group, got %d", fn, rotation_group);
+  if (int rc = check_aligned(fn, "up", up)) return rc;
+  return linear_impl(fn, x, 1, m, k, packed, inv_scale, global_sf_w, bias, out_features, global_sf_x, rotation_group,
+                     out, nullptr, workspace, workspace_bytes, static_cast<hipStream_t>(stream), up, true, ep);
+}
+
+int nvfp4_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                  int weight_dtype, int64_t rows, int64_t k, float eps, void* residual_out, void* y, uint8_t* ck_codes,
+                  uint8_t* ck_scales, void* stream) {
+  const char* fn = "nvfp4_rmsnorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = norm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, weight_dtype, rows, k, eps, residual_out,
+                           &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!y) return fail(NVFP4_ERR_ARG, "%s: y must not be NULL", fn);
+  if ((ck_codes == nullptr) != (ck_scales == nullptr))
+    return fail(NVFP4_ERR_ARG, "%s: checkpoint codes and scales go together", fn);
+  if (int rc = check_aligned(fn, "y", y)) return rc;
+  if (int rc = check_aligned(fn, "ck_codes", ck_codes)) return rc;
+  a.mode = nvfp4::kNormOut;
+  a.y = static_cast<uint16_t*>(y);
+  a.codes = ck_codes;
+  a.scales = ck_scales;
+  return hip_status(nvfp4::launch_rmsnorm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_quantize_rmsnorm_workspace_bytes(int64_t rows) {
+  if (rows < 0) return 0;
+  return align_up(sizeof(float) * nvfp4::kNormPartials) + align_up(sizeof(float) * (size_t)rows);
+}
+
+int nvfp4_quantize_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                           int weight_dtype, int64_t rows, int64_t k, float eps, const float* global_sf,
+                           void* residual_out, uint8_t* codes, uint8_t* scales, float* gsf_out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_quantize_rmsnorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = norm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, weight_dtype, rows, k, eps, residual_out,
+                           &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!codes || !scales) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_nvfp4_operand(fn, "codes", codes, "scales", scales)) return rc;
+  if (int rc = check_align(fn, "global_sf", global_sf, 4)) return rc;
+  if (int rc = check_align(fn, "gsf_out", gsf_out, 4)) return rc;
+  const size_t need = global_sf == nullptr ? nvfp4_quantize_rmsnorm_workspace_bytes(rows) : 0;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes, need)) return rc;
+  a.mode = global_sf != nullptr ? nvfp4::kNormStatic : nvfp4::kNormDynamic;
+  a.codes = codes;
+  a.scales = scales;
+  a.gsf = global_sf;
+  a.gsf_out = gsf_out;
+  if (global_sf == nullptr) {
+    a.partials = static_cast<float*>(workspace);
+    a.rstd = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(sizeof(float) * nvfp4::kNormPartials));
+  }
+  return hip_status(nvfp4::launch_rmsnorm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t k) {
+  if (rows < 0 || k <= 0 || k > nvfp4::kNormMaxK || k % NVFP4_BLOCK_SIZE) return 0;
+  return align_up(sizeof(float) * nvfp4::rmsnorm_backward_partial_floats(rows, k));
+}
+
+int nvfp4_rmsnorm_backward(const void* grad_y, const void* r, int r_dtype, const void* weight, int weight_dtype,
+                           const void* grad_residual, int64_t rows, int64_t k, float eps, void* grad_r, float* grad_w,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_rmsnorm_backward";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_norm(fn, rows, k, eps)) return rc;
+  if (!is_dtype(r_dtype) || !is_dtype(weight_dtype))
+    return fail(NVFP4_ERR_ARG, "%s: dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if (rows == 0 && grad_w == nullptr) return NVFP4_OK;
+  if (rows > 0 && (!grad_y || !r || !weight || !grad_r)) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "grad_y", grad_y)) return rc;
+  if (int rc = check_aligned(fn, "r", r)) return rc;
+  if (int rc = check_aligned(fn, "weight", weight)) return rc;
+  if (int rc = check_aligned(fn, "grad_residual", grad_residual)) return rc;
+  if (int rc = check_aligned(fn, "grad_r", grad_r)) return rc;
+  if (int rc = check_align(fn, "grad_w", grad_w, 4)) return rc;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes,
+                               grad_w != nullptr ? nvfp4_rmsnorm_backward_workspace_bytes(rows, k) : 0))
+    return rc;
+  nvfp4::NormBackward a{};
+  a.gy = static_cast<const uint16_t*>(grad_y);
+  a.r = r;
+  a.w = weight;
+  a.grad_residual = grad_residual;
+  a.rows = rows;
+  a.k = k;
+  a.eps = (double)eps;
+  a.stream_f32 = r_dtype == NVFP4_DTYPE_F32;
+  a.w_f32 = weight_dtype == NVFP4_DTYPE_F32;
+  a.grad_r = grad_r;
+  a.grad_w = grad_w;
+  a.partials = static_cast<float*>(workspace);
+  return hip_status(nvfp4::launch_rmsnorm_backward(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_checkpoint_scale_bytes(int64_t rows, int64_t k) {
+  if (rows <= 0 || k <= 0) return 0;
+  return (size_t)rows * (size_t)((k + NVFP4_CHECKPOINT_BLOCK - 1) / NVFP4_CHECKPOINT_BLOCK);
+}
+
+int nvfp4_checkpoint_pack(const void* x, int64_t rows, int64_t k, int rotation_group, uint8_t* codes, uint8_t* scales,
+                          void* stream) {
+  const char* fn = "nvfp4_checkpoint_pack";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (int rc = check_group(fn, rotation_group, k, true)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!x || !codes || !scales) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "x", x)) return rc;
+  if (int rc = check_aligned(fn, "codes", codes)) return rc;
+  return hip_status(nvfp4::launch_checkpoint_pack(static_cast<const uint16_t*>(x), rows, k, rotation_group,
+                                                  inv_sqrt(rotation_group), codes, scales,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k, void* out,
+                            int out_dtype, void* stream) {
+  const char* fn = "nvfp4_checkpoint_unpack";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (!is_dtype(out_dtype))
+    return fail(NVFP4_ERR_ARG, "%s: out_dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if (rows == 0) return NVFP4_OK;
+  if (!codes || !scales || !out) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "codes", codes)) return rc;
+  if (int rc = check_aligned(fn, "out", out)) return rc;
+  return hip_status(nvfp4::launch_checkpoint_unpack(codes, scales, rows, k, out, out_dtype == NVFP4_DTYPE_BF16,
+                                                    static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_swiglu_checkpoint(const void* gate, const void* up, int64_t rows, int64_t k, void* x, uint8_t* gate_codes,
+                            uint8_t* gate_scales, uint8_t* up_codes, uint8_t* up_scales, void* stream) {
+  const char* fn = "nvfp4_swiglu_checkpoint";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!gate || !up || !x || !gate_codes || !gate_scales || !up_codes || !up_scales)
+    return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (((uintptr_t)gate | (uintptr_t)up | (uintptr_t)x | (uintptr_t)gate_codes | (uintptr_t)up_codes) % 16)
+    return fail(NVFP4_ERR_ARG, "%s: tensors must be 16-byte aligned", fn);
+  return hip_status(nvfp4::launch_swiglu_checkpoint(static_cast<const uint16_t*>(gate),
+                                                    static_cast<const uint16_t*>(up), rows, k,
+                                                    static_cast<uint16_t*>(x), gate_codes, gate_scales, up_codes,
+                                                    up_scales, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_swiglu_backward(const void* grad_x, const void* gate, const uint8_t* gate_scales, const void* up,
+                          const uint8_t* up_scales, int64_t rows, int64_t k, void* grad_gate, void* grad_up,
+                          void* stream) {
+  const char* fn = "nvfp4_swiglu_backward";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (int rc = check_saved(fn, "grad_x", grad_x)) return rc;
+  if (int rc = check_saved(fn, "gate", gate)) return rc;
+  if (int rc = check_saved(fn, "up", up)) return rc;
+  if (int rc = check_saved(fn, "grad_gate", grad_gate)) return rc;
+  if (int rc = check_saved(fn, "grad_up", grad_up)) return rc;
+  if ((gate_scales == nullptr) != (up_scales == nullptr))
+    return fail(NVFP4_ERR_ARG, "%s: gate and up must be both checkpoints or both bf16", fn);
+  return hip_status(nvfp4::launch_swiglu_backward(static_cast<const uint16_t*>(grad_x), gate, gate_scales, up,
+                                                  up_scales, rows, k, static_cast<uint16_t*>(grad_gate),
+                                                  static_cast<uint16_t*>(grad_up), static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_activation_backward(const void* grad_y, const void* z, const uint8_t* z_scales, int64_t rows, int64_t n,
+                              int activation, void* grad_z, void* stream) {
+  const char* fn = "nvfp4_activation_backward";
+  Range call(fn);
+  g_err[0] = 0;
+  if (rows < 0 || rows >= kMaxDim || n <= 0 || n >= kMaxDim)
+    return fail(NVFP4_ERR_SHAPE, "%s: rows must be in [0, 2^31) and n in [1, 2^31), got %lld and %lld", fn,
+                (long long)rows, (long long)n);
+  if (z_scales != nullptr)
+    if (int rc = check_rows_k(fn, rows, n, true)) return rc;
+  if (int rc = check_activation(fn, activation)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (int rc = check_saved(fn, "grad_y", grad_y)) return rc;
+  if (int rc = check_saved(fn, "z", z)) return rc;
+  if (int rc = check_saved(fn, "grad_z", grad_z)) return rc;
+  return hip_status(nvfp4::launch_activation_backward(static_cast<const uint16_t*>(grad_y), z, z_scales, rows, n,
+                                                      activation, static_cast<uint16_t*>(grad_z),
+                                                      static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+size_t nvfp4_weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n <= 0 || k <= 0) return 0;
+  return align_up(nvfp4::weight_grad_workspace_bytes(m, n, k, nvfp4::compute_units()));
+}
+
+int nvfp4_weight_grad(const void* grad_y, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales, int64_t k,
+                      void* grad_w, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_weight_grad";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_rows_k(fn, m, k, true)) return rc;
+  if (n <= 0 || n >= kMaxDim) return fail(NVFP4_ERR_SHAPE, "%s: n must be in [1, 2^31), got %lld", fn, (long long)n);
+  if (!is_dtype(out_dtype))
+    return fail(NVFP4_ERR_ARG, "%s: out_dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if (!grad_w || (m > 0 && (!grad_y || !codes || !scales))) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "grad_y", grad_y)) return rc;
+  if (int rc = check_aligned(fn, "codes", codes)) return rc;
+  if (int rc = check_aligned(fn, "grad_w", grad_w)) return rc;
+  if (workspace != nullptr && ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN))
+    return fail(NVFP4_ERR_WORKSPACE, "%s: workspace must be %d-byte aligned", fn, NVFP4_WORKSPACE_ALIGN);
+  return hip_status(nvfp4::launch_weight_grad(static_cast<const uint16_t*>(grad_y), m, n, codes, scales, k, grad_w,
+                                              out_dtype == NVFP4_DTYPE_BF16, workspace,
+                                              workspace != nullptr ? workspace_bytes : 0, nvfp4::compute_units(),
+                                              static_cast<hipStream_t>(stream)),
+                    fn);
 }
 
 }  // extern "C"

@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias,
-    uint16_t* __restrict__ out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16) {
+    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi,
+    uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16) {
   using C = Cfg<WM, WN, TM, TN>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
 
   // Epilogue: y = bf16(alpha * acc) staged through LDS 32 rows at a time per wave,
   // then bf16(y + bias) written as 16-byte row segments.
-  uint8_t* epi = lds + wave * 32 * C::kEpiRowBytes;
+  uint8_t* staged = lds + wave * 32 * C::kEpiRowBytes;
   constexpr int kSegs = TN * 32 / 8;                 // 16-byte segments per staged row
   const int64_t wrow0 = row0 + wm * TM * 32;
   const int64_t wcol0 = col0 + wn * TN * 32;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
       for (int e = 0; e < 16; ++e) {
         const int r = 8 * (e >> 2) + 4 * kh + (e & 3);
         const float y = __fmul_rn(al[e], __fmul_rn(acc[i][j][e], kAccUnscale));
-        *reinterpret_cast<uint16_t*>(epi + r * C::kEpiRowBytes + (j * 32 + lr) * 2) = (uint16_t)f32_to_bf16(y);
+        *reinterpret_cast<uint16_t*>(staged + r * C::kEpiRowBytes + (j * 32 + lr) * 2) = (uint16_t)f32_to_bf16(y);
       }
     }
     __syncthreads();
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
       const int r = idx / kSegs, sg = idx % kSegs;
       const int64_t row = wrow0 + i * 32 + r;
       const int64_t col = wcol0 + sg * 8;
-      const uint4 v = *reinterpret_cast<const uint4*>(epi + r * C::kEpiRowBytes + sg * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(staged + r * C::kEpiRowBytes + sg * 16);
       if (row < m && col < n) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (bias != nullptr) {
@@ -265,6 +265,16 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
               w[h >> 1] = (w[h >> 1] & (0xFFFF0000u >> sh)) | (zb << sh);
             }
           }
+        }
+        if (epi) {
+#pragma unroll 1
+          for (int h = 0; h < 8 && col + h < n; ++h) {
+            const uint32_t sh = 16 * (h & 1);
+            const uint32_t z = finish_bf16((word(make_uint4(w[0], w[1], w[2], w[3]), h >> 1) >> sh) & 0xFFFFu, ep,
+                                           row * ldo + col + h);
+            out[row * ldo + col + h] = (uint16_t)z;
+          }
+          continue;
         }
         uint16_t* o = out + row * ldo + col;
         if (col + 8 <= n && ((uintptr_t)o & 15) == 0) {
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
 template <int WM, int WN, int TM, int TN>
 hipError_t launch_cfg(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
                       const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b, int64_t a_seg_rows,
-                      const uint16_t* bias,
+                      const uint16_t* bias, const Epilogue& ep,
                       uint16_t* out, int64_t b_srows, int64_t ldo, int aligned16, hipStream_t s) {
   using C = Cfg<WM, WN, TM, TN>;
   static bool attr_set[kMaxDevices] = {};
@@ -292,7 +302,7 @@ hipError_t launch_cfg(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m
   const int tiles_m = (int)((m + C::BM - 1) / C::BM);
   const int tiles_n = (int)((n + C::BN - 1) / C::BN);
   hipLaunchKernelGGL((gemm_kernel<WM, WN, TM, TN>), dim3(tiles_m * tiles_n), dim3(C::kThreads), C::kLds, s, a_codes,
-                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, b_srows, ldo, tiles_m,
+                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, b_srows, ldo, tiles_m,
                      tiles_n, aligned16);
   return hipGetLastError();
 }
@@ -301,16 +311,16 @@ hipError_t launch_cfg(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m
 // b_srows rows per K tile and whose output rows are ldo elements apart.
 hipError_t launch_generic(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                           const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                          const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
-                          int64_t b_srows, int64_t ldo, int cus, hipStream_t s) {
+                          const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep,
+                          uint16_t* out, int64_t b_srows, int64_t ldo, int cus, hipStream_t s) {
   const int aligned16 = ((k / 2) % 16 == 0) && (((uintptr_t)a_codes | (uintptr_t)b_codes) % 16 == 0);
   // Largest tile that still gives every compute unit a tile.
   const int64_t mid = ((m + 255) / 256) * ((n + 127) / 128);
   if (mid >= cus)
-    return launch_cfg<2, 2, 4, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
+    return launch_cfg<2, 2, 4, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
                                   b_srows, ldo,
                                   aligned16, s);
-  return launch_cfg<2, 2, 2, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
+  return launch_cfg<2, 2, 2, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
                                 b_srows, ldo,
                                 aligned16, s);
 }
@@ -361,15 +371,15 @@ size_t gemm_workspace_bytes(int64_t m, int64_t k, int64_t n) {
 hipError_t launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
                        const float* gsf_a, const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias,
-                       uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t s) {
+                       const Epilogue& ep, uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t s) {
   const int cus = compute_units();
   if (prefer_skinny(m, n) && gemm_skinny_supported(m, k, a_codes, a_scales, b_codes, b_scales))
-    return launch_gemm_skinny(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
+    return launch_gemm_skinny(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
                               workspace, workspace_bytes, cus, s);
   if (gemm_pipe_supported(m, k, n, a_codes, a_scales, b_codes, b_scales, cus))
-    return launch_gemm_pipe(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
+    return launch_gemm_pipe(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
                             workspace, workspace_bytes, cus, s);
-  return launch_generic(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, cus,
+  return launch_generic(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, cus,
                         s);
 }
 

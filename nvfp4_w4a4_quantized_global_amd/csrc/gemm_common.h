@@ -13,7 +13,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "activation_device.h"
 #include "nvfp4_device.h"
+#include "nvfp4_launch.h"
 
 namespace nvfp4 {
 namespace gemm {
@@ -88,6 +90,40 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 // bf16(y) + bias in fp32, rounded to bf16: the bias add after the GEMM output is rounded.
 __device__ __forceinline__ uint32_t add_bias_bf16(uint32_t y_bf16, uint16_t bias_bf16) {
   return f32_to_bf16(__fadd_rn(bf16_to_f32(y_bf16), bf16_to_f32(bias_bf16)));
+}
+
+// The epilogue past the bias for element idx: z is the plain linear's bf16 output.  Keeping
+// that rounding makes a fused call equal the linear followed by the activation and the sum,
+// and z the very value the activation's gradient is taken at.
+__device__ __forceinline__ uint32_t finish_bf16(uint32_t z, const Epilogue& ep, int64_t idx) {
+  if (ep.preact != nullptr) ep.preact[idx] = (uint16_t)z;
+  float v = activate(bf16_to_f32(z), ep.act);
+  if (ep.residual != nullptr) v = __fadd_rn(v, bf16_to_f32(ep.residual[idx]));
+  return pack_bf16x2(v, 0.0f);
+}
+
+// The same for eight consecutive elements packed in w (all inside the output, idx a
+// multiple of 8 on 16-byte aligned arrays).
+__device__ __forceinline__ void finish8_bf16(uint32_t (&w)[4], const Epilogue& ep, int64_t idx) {
+  if (ep.preact != nullptr) *reinterpret_cast<uint4*>(ep.preact + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (ep.residual != nullptr) r = *reinterpret_cast<const uint4*>(ep.residual + idx);
+  const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo = activate(__uint_as_float(w[i] << 16), ep.act);
+    float hi = activate(__uint_as_float(w[i] & 0xFFFF0000u), ep.act);
+    if (ep.residual != nullptr) {
+      lo = __fadd_rn(lo, __uint_as_float(rw[i] << 16));
+      hi = __fadd_rn(hi, __uint_as_float(rw[i] & 0xFFFF0000u));
+    }
+    w[i] = pack_bf16x2(lo, hi);
+  }
+}
+
+// Whether finish8_bf16's wide accesses are aligned for rows of ldo elements.
+__device__ __forceinline__ bool epilogue_wide(const Epilogue& ep, int64_t ldo) {
+  return (ldo & 7) == 0 && (((uintptr_t)ep.residual | (uintptr_t)ep.preact) & 15) == 0;
 }
 
 }  // namespace gemm

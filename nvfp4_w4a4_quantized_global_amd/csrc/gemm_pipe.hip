@@ -106,12 +106,14 @@ __device__ __forceinline__ void interleave() {
 // kTM: 32-row MFMA tiles per wave along M (4: 256 x 256 tiles, 2: 128 x 256).  With
 // sub = 2 (split launch of 128-row tiles only), tile indices count tiles twice as tall
 // (tiles_m of that grid), each cut into two 128-row halves: tile tile0 + u / 2, half u % 2.
-template <bool kSplit, int kTM>
+// kEpi: the epilogue past the bias (activation, residual; never with kSplit, whose reduce
+// applies it).
+template <bool kSplit, int kTM, bool kEpi>
 __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int64_t b_srows, int64_t ldo, int tiles_m,
+    const uint16_t* __restrict__ bias, const Epilogue ep, uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m,
     int tiles_n, int tile0, int splits, int sub,
     float* __restrict__ partial) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -347,7 +349,8 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
   // bias once, and stores them as one 16-byte segment when they are all inside the
   // output and the row starts are 16-byte aligned.
   const int64_t col = wcol0 + 8 * (lane & 15);
-  const bool vec_store = col + 8 <= n && (ldo & 7) == 0 && ((uintptr_t)out & 15) == 0;
+  const bool vec_store = col + 8 <= n && (ldo & 7) == 0 && ((uintptr_t)out & 15) == 0 &&
+                         (!kEpi || epilogue_wide(ep, ldo));
   uint32_t bw[4] = {0, 0, 0, 0};
   if (bias != nullptr) {
     if (col + 8 <= n && ((uintptr_t)(bias + col) & 15) == 0) {
@@ -397,6 +400,7 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
       }
       if (row < m) {
         uint16_t* o = out_i + 4 * p * ldo;
+        if (kEpi && vec_store) finish8_bf16(w, ep, (row_i + 4 * p) * ldo + col);
         if (vec_store) {
           typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
           __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(o));
@@ -404,7 +408,11 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
           const uint64_t lo = ((uint64_t)w[1] << 32) | w[0], hi = ((uint64_t)w[3] << 32) | w[2];
           const int cnt = n - col < 8 ? (int)(n - col) : 8;
 #pragma unroll 1
-          for (int h = 0; h < cnt; ++h) o[h] = (uint16_t)((h < 4 ? lo : hi) >> (16 * (h & 3)));
+          for (int h = 0; h < cnt; ++h) {
+            uint32_t z = (uint16_t)((h < 4 ? lo : hi) >> (16 * (h & 3)));
+            if (kEpi) z = finish_bf16(z, ep, (row_i + 4 * p) * ldo + col + h);
+            o[h] = (uint16_t)z;
+          }
         }
       }
     }
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
                                                       int tile0, int sub, int tiles_m, int64_t m, int64_t n,
                                                       const float* __restrict__ gsf_a, const float* __restrict__ gsf_b,
                                                       int64_t a_seg_rows, const uint16_t* __restrict__ bias,
-                                                      uint16_t* __restrict__ out, int64_t ldo) {
+                                                      const Epilogue ep, bool epi, uint16_t* out, int64_t ldo) {
   using G = Geo<kTM>;
   constexpr int kPerTile = G::kAcc * 256 / 8;     // threads per tile
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -474,6 +482,20 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
     uint32_t v = f32_to_bf16(__fmul_rn(alpha, __fmul_rn(acc[h], kAccUnscale)));
     if (bias != nullptr && col + h < n) v = add_bias_bf16(v, bias[col + h]);
     y[h] = (uint16_t)v;
+  }
+  if (epi) {
+    if (col + 8 <= n && epilogue_wide(ep, ldo)) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = y[2 * i] | ((uint32_t)y[2 * i + 1] << 16);
+      finish8_bf16(w, ep, row * ldo + col);
+#pragma unroll
+      for (int h = 0; h < 8; ++h) y[h] = (uint16_t)(w[h >> 1] >> (16 * (h & 1)));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (col + h < n) y[h] = (uint16_t)finish_bf16(y[h], ep, row * ldo + col + h);
+    }
   }
   uint16_t* o = out + row * ldo + col;
   if (col + 8 <= n && ((uintptr_t)o & 15) == 0) {
@@ -540,57 +562,57 @@ size_t plan_bytes(const PipePlan& p) {
 template <int kTM>
 hipError_t launch_split_tail(const PipePlan& p, int sub, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                              int64_t k, const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                             const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
+                             const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out,
                              float* partial, hipStream_t s) {
   constexpr int kLds = Geo<kTM>::kLds;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<true, kTM>), kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<true, kTM, false>), kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
   const int64_t units = p.rest * sub;
-  hipLaunchKernelGGL((gemm_pipe_kernel<true, kTM>), dim3((uint32_t)(units * p.splits)), dim3(256), kLds, s, a_codes,
-                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn,
+  hipLaunchKernelGGL((gemm_pipe_kernel<true, kTM, false>), dim3((uint32_t)(units * p.splits)), dim3(256), kLds, s, a_codes,
+                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn,
                      (int)p.full, p.splits, sub, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((split_k_reduce<kTM>), dim3((uint32_t)(units * Geo<kTM>::kAcc / 8)), dim3(256), 0, s, partial,
-                     p.splits, (int)units, (int)p.full, sub, tm, m, n, gsf_a, gsf_b, a_seg_rows, bias, out, n);
+                     p.splits, (int)units, (int)p.full, sub, tm, m, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, n);
   return hipGetLastError();
 }
 
-template <int kTM>
+template <int kTM, bool kEpi>
 hipError_t launch_plan(const PipePlan& p, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                       const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out, float* partial,
+                       const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, float* partial,
                        hipStream_t s) {
   constexpr int kLds = Geo<kTM>::kLds;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<false, kTM>), kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<false, kTM, kEpi>), kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
   if (p.full > 0) {
-    hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM>), dim3((uint32_t)p.full), dim3(256), kLds, s, a_codes, a_scales,
-                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn, 0, 1, 1,
+    hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM, kEpi>), dim3((uint32_t)p.full), dim3(256), kLds, s, a_codes, a_scales,
+                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn, 0, 1, 1,
                        (float*)nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (p.rest == 0) return hipSuccess;
   if (p.splits == 1) {
-    hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM>), dim3((uint32_t)p.rest), dim3(256), kLds, s, a_codes, a_scales,
-                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn, (int)p.full, 1,
+    hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM, kEpi>), dim3((uint32_t)p.rest), dim3(256), kLds, s, a_codes, a_scales,
+                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn, (int)p.full, 1,
                        1, (float*)nullptr);
     return hipGetLastError();
   }
   if (kTM == 4 && p.sub == 2)
     return launch_split_tail<2>(p, 2, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias,
-                                out, partial, s);
+                                ep, out, partial, s);
   return launch_split_tail<kTM>(p, 1, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias,
-                                out, partial, s);
+                                ep, out, partial, s);
 }
 
 }  // namespace
@@ -610,17 +632,17 @@ size_t gemm_pipe_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus) {
 
 hipError_t launch_gemm_pipe(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                             const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                            const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
+                            const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out,
                             void* workspace, size_t workspace_bytes, int cus, hipStream_t s) {
   PipePlan p = pipe_plan(m, k, n, cus);
   const size_t need = plan_bytes(p);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) p.splits = 1;
   float* partial = static_cast<float*>(workspace);
-  if (p.tm == 2)
-    return launch_plan<2>(p, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
-                          partial, s);
-  return launch_plan<4>(p, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out,
-                        partial, s);
+  using Fn = decltype(&launch_plan<4, false>);
+  static constexpr Fn f[2][2] = {{launch_plan<4, false>, launch_plan<4, true>},
+                                 {launch_plan<2, false>, launch_plan<2, true>}};
+  return f[p.tm == 2 ? 1 : 0][ep.active() ? 1 : 0](p, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b,
+                                                   a_seg_rows, bias, ep, out, partial, s);
 }
 
 }  // namespace nvfp4

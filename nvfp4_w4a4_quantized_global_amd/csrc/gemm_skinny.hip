@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int splits, float* __restrict__ partial) {
+    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi, uint16_t* out, int splits,
+    float* __restrict__ partial) {
   __shared__ float red[MT * 4][4][64];     // waves 1..3 hand their sums to wave 0, one at a time
 
   const int col_group = blockIdx.x / splits;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
           const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
           uint32_t y = f32_to_bf16(__fmul_rn(al, __fmul_rn(acc[i][j][e], kAccUnscale)));
           if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
+          if (epi) y = finish_bf16(y, ep, row * n + col);
           out[row * n + col] = (uint16_t)y;
         }
       }
@@ -200,7 +202,8 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
 __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restrict__ partial, int splits, int64_t m,
                                                           int64_t n, const float* __restrict__ gsf_a,
                                                           const float* __restrict__ gsf_b, int64_t a_seg_rows,
-                                                          const uint16_t* __restrict__ bias, uint16_t* __restrict__ out) {
+                                                          const uint16_t* __restrict__ bias, const Epilogue ep,
+                                                          bool epi, uint16_t* out) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= m * n) return;
   float acc = 0.0f;
@@ -208,6 +211,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restric
   const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, idx / n);
   uint32_t y = f32_to_bf16(__fmul_rn(alpha, __fmul_rn(acc, kAccUnscale)));
   if (bias != nullptr) y = add_bias_bf16(y, bias[idx % n]);
+  if (epi) y = finish_bf16(y, ep, idx);
   out[idx] = (uint16_t)y;
 }
 
@@ -304,7 +308,8 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* __restrict__ out, int splits, float* __restrict__ partial,
+    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi, uint16_t* out, int splits,
+    float* __restrict__ partial,
     const uint16_t* __restrict__ a16, float* __restrict__ gsf_dst) {
   // direct-load instructions per super tile and wave; bytes per slot and where the
   // weight's scale words sit in it
@@ -569,6 +574,7 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
       const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
       uint32_t y = f32_to_bf16(__fmul_rn(al, __fmul_rn(acc[e], kAccUnscale)));
       if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
+      if (epi) y = finish_bf16(y, ep, row * n + col);
       out[row * n + col] = (uint16_t)y;
     }
   }
@@ -599,16 +605,17 @@ DecodePlan decode_plan(int64_t k, int64_t n, int cus) {
 template <bool kA16, int kDW, bool kOne, int kFuse = 0>
 void launch_decode_t(dim3 grid, hipStream_t s, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                      int64_t k, const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                     const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out, int splits,
+                     const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, int splits,
                      float* partial, const uint16_t* x16, float* gsf_dst) {
   hipLaunchKernelGGL((gemm_decode_kernel<kA16, kDW, kOne, kFuse>), grid, dim3(64 * kDW), 0, s, a_codes, a_scales, m, k,
-                     b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits, partial, x16, gsf_dst);
+                     b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, splits, partial, x16,
+                     gsf_dst);
 }
 
 hipError_t launch_decode(bool a16, int fuse, int waves, uint32_t blocks, hipStream_t s, const uint8_t* a_codes,
                          const uint8_t* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
                          const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b,
-                         int64_t a_seg_rows, const uint16_t* bias, uint16_t* out, int splits, float* partial,
+                         int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, int splits, float* partial,
                          const uint16_t* x16, float* gsf_dst = nullptr) {
 #ifndef NVFP4_DECODE_ONE_ROW
 #define NVFP4_DECODE_ONE_ROW 1
@@ -626,7 +633,7 @@ hipError_t launch_decode(bool a16, int fuse, int waves, uint32_t blocks, hipStre
       {launch_decode_t<true, 4, true, kFuseDynamic>, launch_decode_t<true, 8, true, kFuseDynamic>}};
   const int w8 = waves == 8 ? 1 : 0;
   const Launch fn = fuse != 0 ? kFused[fuse == kFuseDynamic ? 1 : 0][w8] : kPlain[a16 ? 1 : 0][one ? 1 : 0][w8];
-  fn(dim3(blocks), s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits,
+  fn(dim3(blocks), s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, splits,
      partial, x16, gsf_dst);
   return hipGetLastError();
 }
@@ -634,10 +641,10 @@ hipError_t launch_decode(bool a16, int fuse, int waves, uint32_t blocks, hipStre
 template <int MT>
 hipError_t launch_mt(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
                      const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b, const uint16_t* bias,
-                     int64_t a_seg_rows, uint16_t* out, int splits, float* partial, hipStream_t s) {
+                     const Epilogue& ep, int64_t a_seg_rows, uint16_t* out, int splits, float* partial, hipStream_t s) {
   const int64_t groups = (n + kCols - 1) / kCols;
-  hipLaunchKernelGGL((gemm_skinny_kernel<MT>), dim3((uint32_t)(groups * splits)), dim3(256), 0, s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits,
-                     partial);
+  hipLaunchKernelGGL((gemm_skinny_kernel<MT>), dim3((uint32_t)(groups * splits)), dim3(256), 0, s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep,
+                     ep.active(), out, splits, partial);
   return hipGetLastError();
 }
 
@@ -657,8 +664,8 @@ size_t gemm_skinny_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus) {
 
 hipError_t launch_gemm_skinny(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                               const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                              const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
-                              void* workspace, size_t workspace_bytes, int cus, hipStream_t s) {
+                              const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep,
+                              uint16_t* out, void* workspace, size_t workspace_bytes, int cus, hipStream_t s) {
   const DecodePlan plan = decode_plan(k, n, cus);
   int splits = m <= 16 ? plan.splits : skinny_splits(k, n, cus);
   const size_t need = splits > 1 ? (size_t)splits * (size_t)m * (size_t)n * sizeof(float) : 0;
@@ -668,18 +675,18 @@ hipError_t launch_gemm_skinny(const uint8_t* a_codes, const uint8_t* a_scales, i
   if (m <= 16) {
     const int64_t tiles = (n + kDecRows - 1) / kDecRows;
     e = launch_decode(false, 0, plan.waves, (uint32_t)(tiles * splits), s, a_codes, a_scales, m, k, b_codes, b_scales,
-                      n, gsf_a, gsf_b, a_seg_rows, bias, out, splits, partial, nullptr);
+                      n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, splits, partial, nullptr);
   } else if (m <= 32) {
-    e = launch_mt<2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, a_seg_rows, out, splits, partial, s);
+    e = launch_mt<2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, ep, a_seg_rows, out, splits, partial, s);
   } else if (m <= 64) {
-    e = launch_mt<4>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, a_seg_rows, out, splits, partial, s);
+    e = launch_mt<4>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, ep, a_seg_rows, out, splits, partial, s);
   } else {
-    e = launch_mt<8>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, a_seg_rows, out, splits, partial, s);
+    e = launch_mt<8>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, ep, a_seg_rows, out, splits, partial, s);
   }
   if (e != hipSuccess || splits == 1) return e;
   const int64_t total = m * n;
   hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s, partial, splits, m,
-                     n, gsf_a, gsf_b, a_seg_rows, bias, out);
+                     n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out);
   return hipGetLastError();
 }
 
@@ -690,7 +697,7 @@ bool gemm_decode_a16_supported(int64_t m, int64_t k, const void* a16, const void
 
 hipError_t launch_gemm_decode_a16(const uint16_t* a16, int64_t m, int64_t k, const uint8_t* b_codes,
                                   const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b,
-                                  const uint16_t* bias, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                  const uint16_t* bias, const Epilogue& ep, uint16_t* out, void* workspace, size_t workspace_bytes,
                                   int cus, hipStream_t s) {
   const DecodePlan plan = decode_plan(k, n, cus);
   int splits = plan.splits;
@@ -699,11 +706,11 @@ hipError_t launch_gemm_decode_a16(const uint16_t* a16, int64_t m, int64_t k, con
   float* partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
   const int64_t tiles = (n + kDecRows - 1) / kDecRows;
   hipError_t e = launch_decode(true, 0, plan.waves, (uint32_t)(tiles * splits), s, nullptr, nullptr, m, k,
-                               b_codes, b_scales, n, gsf_a, gsf_b, 0, bias, out, splits, partial, a16);
+                               b_codes, b_scales, n, gsf_a, gsf_b, 0, bias, ep, out, splits, partial, a16);
   if (e != hipSuccess || splits == 1) return e;
   const int64_t total = m * n;
   hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s, partial, splits, m,
-                     n, gsf_a, gsf_b, (int64_t)0, bias, out);
+                     n, gsf_a, gsf_b, (int64_t)0, bias, ep, ep.active(), out);
   return hipGetLastError();
 }
 
@@ -737,7 +744,7 @@ bool linear_decode_fused_supported(int64_t m, int64_t k, int64_t n, bool dynamic
 
 hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_t* b_codes, const uint8_t* b_scales,
                                       int64_t n, const float* gsf_x, float* gsf_used, const float* gsf_w,
-                                      const uint16_t* bias, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                      const uint16_t* bias, const Epilogue& ep, uint16_t* out, void* workspace, size_t workspace_bytes,
                                       int cus, hipStream_t s) {
   if (gsf_x == nullptr && gsf_used == nullptr) return hipErrorInvalidValue;   // the reduce reads the scale there
   int waves;
@@ -745,10 +752,10 @@ hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_
   float* partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
   const int64_t tiles = (n + kDecRows - 1) / kDecRows;
   hipError_t e = launch_decode(true, gsf_x != nullptr ? kFuseStatic : kFuseDynamic, waves, (uint32_t)(tiles * splits), s, nullptr, nullptr, 1, k, b_codes,
-                               b_scales, n, gsf_x, gsf_w, 0, bias, out, splits, partial, x, gsf_used);
+                               b_scales, n, gsf_x, gsf_w, 0, bias, ep, out, splits, partial, x, gsf_used);
   if (e != hipSuccess || splits == 1) return e;
   hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, partial, splits,
-                     (int64_t)1, n, gsf_x != nullptr ? gsf_x : gsf_used, gsf_w, (int64_t)0, bias, out);
+                     (int64_t)1, n, gsf_x != nullptr ? gsf_x : gsf_used, gsf_w, (int64_t)0, bias, ep, ep.active(), out);
   return hipGetLastError();
 }
 

@@ -1,0 +1,439 @@
+// RMS norm with the residual's addition, on gfx950: its output as bf16 (with or without an
+// 8-bit checkpoint) or as NVFP4 codes and scales for the linear, and its gradient.
+//
+//   r = x + residual                      (rounded to the stream's type, stored)
+//   s = fp32(1 / sqrt(sum(r^2) / K + eps))
+//   y = bf16(fp32(fp32(r * s) * w))
+//
+// The squares of bf16 and fp32 values are exact in fp64 and so is, to far below fp32's
+// spacing, their sum in any order: s has the same bits whichever kernel computes it, so
+// the codes of y are the quantizer's bit for bit.  The fp64 additions (one per value)
+// stay hidden under the HBM traffic that bounds every form.
+//
+// A lane owns 16 consecutive values (one NVFP4 block, half a checkpoint block).  Rows of
+// at most 1024 values take a power-of-two group of lanes inside a wave, several rows per
+// workgroup; longer rows (to 16384) take a workgroup of their own with one chunk per lane.
+// Either way the row stays in registers between its sum and its output: one read, one write.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "checkpoint_device.h"
+#include "nvfp4_device.h"
+#include "nvfp4_launch.h"
+#include "quantize_device.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kGroupThreads = 256;   // workgroup of the several-rows form
+
+// Lanes per row and threads per workgroup for rows of k values.
+struct RowShape {
+  int lanes, threads;
+};
+RowShape row_shape(int64_t k) {
+  const int chunks = (int)(k / kBlock);
+  if (chunks <= 64) {
+    int l = 8;
+    while (l < chunks) l *= 2;
+    return {l, kGroupThreads};
+  }
+  const int t = (chunks + 63) / 64 * 64;
+  return {t, t};
+}
+
+// 16 weights as loaded (8 words of bf16 pairs or 16 of fp32), expanded where used.
+template <bool kF32>
+struct Weight16 {
+  uint4 raw[kF32 ? 4 : 2];
+  __device__ __forceinline__ void load(const void* w, int64_t off) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + off * (kF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (kF32 ? 4 : 2); ++i) raw[i] = p[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (kF32 ? 4 : 2); ++i) raw[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const uint4& q = raw[kF32 ? i / 4 : i / 8];
+    const int e = kF32 ? i & 3 : (i >> 1) & 3;
+    const uint32_t u = e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w;
+    return kF32 ? __uint_as_float(u) : __uint_as_float((i & 1) ? u & 0xFFFF0000u : u << 16);
+  }
+};
+
+template <bool kF32>
+__device__ __forceinline__ void load_stream16(const void* p, int64_t off, float (&v)[16]) {
+  if constexpr (kF32) load16_f32(static_cast<const float*>(p) + off, v);
+  else load16_bf16(static_cast<const uint16_t*>(p) + off, v);
+}
+
+__device__ __forceinline__ void round_bf16(float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = gemm::pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    v[2 * i] = __uint_as_float(w << 16);
+    v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+}
+
+// v already rounded to the stream's type.
+template <bool kF32>
+__device__ __forceinline__ void store_stream16(void* p, int64_t off, const float (&v)[16]) {
+  if constexpr (kF32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    store16_bf16(static_cast<uint16_t*>(p) + off, v);
+  }
+}
+
+__device__ __forceinline__ double sum_squares(const float (&v)[16]) {
+  double a = 0.0, b = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    a = fma((double)v[i], (double)v[i], a);
+    b = fma((double)v[i + 1], (double)v[i + 1], b);
+  }
+  return a + b;
+}
+
+__device__ __forceinline__ float row_scale(double sum, int64_t k, double eps) {
+  return (float)(1.0 / sqrt(sum / (double)k + eps));
+}
+
+// Sum over the `lanes` lanes of a row (a power of two within a wave).
+template <typename T>
+__device__ __forceinline__ T group_sum(T v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// y = bf16((r * s) * w), over r.
+template <bool kWF32>
+__device__ __forceinline__ void normalize16(float (&v)[16], float s, const Weight16<kWF32>& w) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], s), w.get(i));
+  round_bf16(v);
+}
+
+// kRes: no residual, one in bf16, one in fp32 (the stream's type is the residual's, or
+// x's without one).  What becomes of y is a.mode: bf16 with an optional checkpoint,
+// codes under a static scale, codes of a single row under its own dynamic scale, or
+// (first pass of a dynamic scale over many rows) only s and the abs-max of y.
+template <bool kXF32, int kRes, bool kWF32>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormForward a) {
+  constexpr bool kSF32 = kRes == 0 ? kXF32 : kRes == 2;
+  __shared__ double part[16];
+  __shared__ float pmax[16];
+  const int t = threadIdx.x;
+  const int rows_here = blockDim.x / a.lanes;
+  const int sub = rows_here == 1 ? 0 : t / a.lanes;
+  const int c = t - sub * a.lanes;
+  const int64_t k = a.k;
+  const bool in_k = c < k / kBlock;
+  Weight16<kWF32> w;
+  if (in_k) w.load(a.w, (int64_t)c * kBlock);
+  else w.zero();
+  const float gsf_static = a.mode == kNormStatic ? *a.gsf : 0.0f;
+  if (a.mode == kNormStatic && a.gsf_out != nullptr && blockIdx.x == 0 && t == 0) *a.gsf_out = gsf_static;
+  float mx = 0.0f;
+
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_here) {
+    const int64_t row = row0 + sub;
+    const bool valid = row < a.rows && in_k;
+    const int64_t off = row * k + (int64_t)c * kBlock;
+    float v[16];
+    if (valid) {
+      load_stream16<kXF32>(a.x, off, v);
+      if constexpr (kRes != 0) {
+        float q[16];
+        load_stream16<kRes == 2>(a.residual, off, q);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], q[i]);
+        if constexpr (!kSF32) round_bf16(v);
+        store_stream16<kSF32>(a.r, off, v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+    double ss = group_sum(sum_squares(v), a.lanes < 64 ? a.lanes : 64);
+    if (a.lanes > 64) {
+      if ((t & 63) == 0) part[t >> 6] = ss;
+      __syncthreads();
+      ss = 0.0;
+      for (int i = 0; i < (int)(blockDim.x >> 6); ++i) ss += part[i];
+      __syncthreads();
+    }
+    const float s = row_scale(ss, k, a.eps);
+    normalize16<kWF32>(v, s, w);
+
+    if (a.mode == kNormOut) {
+      if (valid) store16_bf16(a.y + off, v);
+      if (a.codes != nullptr) {
+        uint32_t sb;
+        const uint4 code = ck_pack16(v, sb);
+        if (valid) {
+          *reinterpret_cast<uint4*>(a.codes + off) = code;
+          if ((c & 1) == 0) a.scales[row * ((k + kCkBlock - 1) / kCkBlock) + (c >> 1)] = (uint8_t)sb;
+        }
+      }
+      continue;
+    }
+    float gsf = gsf_static;
+    if (a.mode != kNormStatic) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      if (a.mode == kNormStats) {
+        if (c == 0 && row < a.rows) a.rstd[row] = s;
+        continue;
+      }
+      // the one row: its abs-max over the workgroup (rows beyond it are zeros)
+      mx = wave_max(mx);
+      if ((t & 63) == 0) pmax[t >> 6] = mx;
+      __syncthreads();
+      for (int i = 0; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
+      gsf = global_scale_from_amax(mx);
+      if (t == 0 && a.gsf_out != nullptr) *a.gsf_out = gsf;
+    }
+    // lanes past the row's last 128-wide tile hold no unit of this row
+    const int64_t urow = c < (k + kScaleTileK - 1) / kScaleTileK * 8 ? row : a.rows;
+    quantize_unit<false>(v, urow, c >> 3, c & 7, a.rows, k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
+  }
+  if (a.mode == kNormStats) {
+    mx = wave_max(mx);
+    if ((t & 63) == 0) pmax[t >> 6] = mx;
+    __syncthreads();
+    if (t == 0) {
+      for (int i = 1; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
+      a.partials[blockIdx.x] = mx;
+    }
+  }
+}
+
+// Second pass of a dynamic scale: y again from r and s (r is in the memory-side cache, and
+// storing y in the first pass would cost more than forming it twice), then its codes.
+// Units and lanes as in the quantizer's own pass.
+constexpr int kQThreads = 256;
+template <bool kSF32, bool kWF32>
+__global__ void __launch_bounds__(kQThreads) rmsnorm_quantize_kernel(const NormForward a, int n_partials) {
+  __shared__ float lds[kQThreads / 64];
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < n_partials; i += kQThreads) m = fmaxf(m, a.partials[i]);
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQThreads / 64; ++i) m = fmaxf(m, lds[i]);
+  const float gsf = global_scale_from_amax(m);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.gsf_out != nullptr) *a.gsf_out = gsf;
+
+  const int64_t kt_count = (a.k + kScaleTileK - 1) / kScaleTileK;
+  const int64_t units = a.rows * kt_count;
+  const int j = threadIdx.x & 7;
+  const void* r = a.r != nullptr ? a.r : a.x;
+  for (int64_t u0 = (int64_t)blockIdx.x * (kQThreads / 8); u0 < units; u0 += (int64_t)gridDim.x * (kQThreads / 8)) {
+    const int64_t unit = u0 + (threadIdx.x >> 3);
+    const int64_t row = unit / kt_count, kt = unit - row * kt_count;
+    const int64_t blk = kt * 8 + j;
+    float v[16];
+    Weight16<kWF32> w;
+    float s = 0.0f;
+    if (row < a.rows && blk < a.k / kBlock) {
+      load_stream16<kSF32>(r, row * a.k + blk * kBlock, v);
+      w.load(a.w, blk * kBlock);
+      s = a.rstd[row];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      w.zero();
+    }
+    normalize16<kWF32>(v, s, w);
+    quantize_unit<false>(v, row, kt, j, a.rows, a.k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
+  }
+}
+
+// Gradient.  With n = r s, g = gy w and d = sum(g r) over the row:
+//   grad_r = s g - r (s^3 d / K) + grad_residual,   grad_w = sum over rows of gy n
+// (the rounding of y taken as the identity).  Each workgroup walks its rows with its
+// lanes' 16 columns of grad_w in registers and writes one partial row of them;
+// rmsnorm_weight_grad_kernel adds the partials in a fixed order.
+template <bool kSF32, bool kWF32, bool kRes>
+__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackward a) {
+  __shared__ double part_ss[16];
+  __shared__ float part_d[16];
+  __shared__ float colsum[kGroupThreads * 16];
+  const int t = threadIdx.x;
+  const int rows_here = blockDim.x / a.lanes;
+  const int sub = rows_here == 1 ? 0 : t / a.lanes;
+  const int c = t - sub * a.lanes;
+  const int64_t k = a.k;
+  const bool in_k = c < k / kBlock;
+  Weight16<kWF32> w;
+  if (in_k) w.load(a.w, (int64_t)c * kBlock);
+  else w.zero();
+  float gw[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) gw[i] = 0.0f;
+
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_here) {
+    const int64_t row = row0 + sub;
+    const bool valid = row < a.rows && in_k;
+    const int64_t off = row * k + (int64_t)c * kBlock;
+    float r[16], g[16], q[16];
+    if (valid) {
+      load_stream16<kSF32>(a.r, off, r);
+      load16_bf16(a.gy + off, g);
+      if constexpr (kRes) load_stream16<kSF32>(a.grad_residual, off, q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = g[i] = q[i] = 0.0f;
+    }
+    double ss = sum_squares(r);
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) d = fmaf(g[i] * w.get(i), r[i], d);
+    const int lanes = a.lanes < 64 ? a.lanes : 64;
+    ss = group_sum(ss, lanes);
+    d = group_sum(d, lanes);
+    if (a.lanes > 64) {
+      if ((t & 63) == 0) {
+        part_ss[t >> 6] = ss;
+        part_d[t >> 6] = d;
+      }
+      __syncthreads();
+      ss = 0.0;
+      d = 0.0f;
+      for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
+        ss += part_ss[i];
+        d += part_d[i];
+      }
+      __syncthreads();
+    }
+    const float s = row_scale(ss, k, a.eps);
+    const float f = s * s * (d / (float)k);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float n = r[i] * s;
+      gw[i] = fmaf(g[i], n, gw[i]);
+      const float x = fmaf(s, g[i] * w.get(i), -(n * f));
+      r[i] = kRes ? x + q[i] : x;
+    }
+    if (valid) {
+      if constexpr (!kSF32) round_bf16(r);
+      store_stream16<kSF32>(a.grad_r, off, r);
+    }
+  }
+  if (a.grad_w == nullptr) return;
+  if (rows_here == 1) {
+    if (in_k) store_stream16<true>(a.partials, (int64_t)blockIdx.x * k + (int64_t)c * kBlock, gw);
+    return;
+  }
+  // the workgroup's rows side by side in LDS, added in row order
+#pragma unroll
+  for (int i = 0; i < 16; ++i) colsum[t * 16 + i] = gw[i];
+  __syncthreads();
+  if (sub == 0 && in_k) {
+    for (int s = 1; s < rows_here; ++s)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) gw[i] += colsum[(s * a.lanes + c) * 16 + i];
+    store_stream16<true>(a.partials, (int64_t)blockIdx.x * k + (int64_t)c * kBlock, gw);
+  }
+}
+
+// grad_w[j] = sum of n partial rows, 32 columns and 8 interleaved row sets per workgroup.
+__global__ void __launch_bounds__(256) rmsnorm_weight_grad_kernel(const float* __restrict__ partials, int n, int64_t k,
+                                                                  float* __restrict__ grad_w) {
+  __shared__ float lds[8][32];
+  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int set = threadIdx.x >> 5;
+  float a = 0.0f;
+  if (col < k) {
+#pragma unroll 8
+    for (int i = set; i < n; i += 8) a += partials[(int64_t)i * k + col];
+  }
+  lds[set][threadIdx.x & 31] = a;
+  __syncthreads();
+  if (set == 0 && col < k) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) a += lds[i][threadIdx.x];
+    grad_w[col] = a;
+  }
+}
+
+using ForwardFn = void (*)(const NormForward);
+
+ForwardFn forward_kernel(const NormForward& a) {
+  const int w = a.w_f32 ? 1 : 0;
+  if (a.residual == nullptr) {
+    static constexpr ForwardFn f[2][2] = {{rmsnorm_kernel<false, 0, false>, rmsnorm_kernel<false, 0, true>},
+                                          {rmsnorm_kernel<true, 0, false>, rmsnorm_kernel<true, 0, true>}};
+    return f[a.x_f32 ? 1 : 0][w];
+  }
+  static constexpr ForwardFn f[3][2] = {{rmsnorm_kernel<false, 1, false>, rmsnorm_kernel<false, 1, true>},
+                                        {rmsnorm_kernel<false, 2, false>, rmsnorm_kernel<false, 2, true>},
+                                        {rmsnorm_kernel<true, 2, false>, rmsnorm_kernel<true, 2, true>}};
+  return f[!a.stream_f32 ? 0 : !a.x_f32 ? 1 : 2][w];
+}
+
+// Workgroups of the row-walking kernels whose per-workgroup results are joined afterwards.
+int64_t walking_blocks(int64_t rows, const RowShape& s) {
+  const int64_t per = s.threads / s.lanes;
+  return std::min<int64_t>((rows + per - 1) / per, kNormPartials);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(NormForward a, hipStream_t s) {
+  const RowShape shape = row_shape(a.k);
+  a.lanes = shape.lanes;
+  const int64_t per = shape.threads / shape.lanes;
+  int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, 1 << 20);   // the rest by the row loop
+  if (a.mode == kNormDynamic) {
+    // one row needs no second pass: its workgroup knows the whole abs-max
+    a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
+    blocks = walking_blocks(a.rows, shape);
+  }
+  hipLaunchKernelGGL(forward_kernel(a), dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.mode != kNormStats) return e;
+  using QuantFn = void (*)(const NormForward, int);
+  static constexpr QuantFn q[2][2] = {{rmsnorm_quantize_kernel<false, false>, rmsnorm_quantize_kernel<false, true>},
+                                      {rmsnorm_quantize_kernel<true, false>, rmsnorm_quantize_kernel<true, true>}};
+  const int64_t units = a.rows * ((a.k + kScaleTileK - 1) / kScaleTileK);
+  const int64_t grid = std::min<int64_t>((units + kQThreads / 8 - 1) / (kQThreads / 8), 4096);
+  const bool sf32 = a.residual != nullptr ? a.stream_f32 : a.x_f32;
+  hipLaunchKernelGGL(q[sf32 ? 1 : 0][a.w_f32 ? 1 : 0], dim3((uint32_t)grid), dim3(kQThreads), 0, s, a, (int)blocks);
+  return hipGetLastError();
+}
+
+size_t rmsnorm_backward_partial_floats(int64_t rows, int64_t k) {
+  return (size_t)walking_blocks(rows, row_shape(k)) * (size_t)k;
+}
+
+hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s) {
+  const RowShape shape = row_shape(a.k);
+  a.lanes = shape.lanes;
+  const int64_t blocks = walking_blocks(a.rows, shape);
+  using Fn = void (*)(const NormBackward);
+  static constexpr Fn f[2][2][2] = {
+      {{rmsnorm_backward_kernel<false, false, false>, rmsnorm_backward_kernel<false, false, true>},
+       {rmsnorm_backward_kernel<false, true, false>, rmsnorm_backward_kernel<false, true, true>}},
+      {{rmsnorm_backward_kernel<true, false, false>, rmsnorm_backward_kernel<true, false, true>},
+       {rmsnorm_backward_kernel<true, true, false>, rmsnorm_backward_kernel<true, true, true>}}};
+  if (blocks > 0)
+    hipLaunchKernelGGL(f[a.stream_f32 ? 1 : 0][a.w_f32 ? 1 : 0][a.grad_residual != nullptr ? 1 : 0],
+                       dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.grad_w == nullptr) return e;
+  hipLaunchKernelGGL(rmsnorm_weight_grad_kernel, dim3((uint32_t)((a.k + 31) / 32)), dim3(256), 0, s, a.partials,
+                     (int)blocks, a.k, a.grad_w);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

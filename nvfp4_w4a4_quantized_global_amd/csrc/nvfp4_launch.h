@@ -15,6 +15,17 @@ constexpr int kMaxDevices = 64;
 // (`done` is the caller's per-kernel record); a no-op after the first call there.
 hipError_t set_dynamic_lds_once(const void* kernel, int bytes, bool (&done)[kMaxDevices]);
 
+// What a linear's output goes through after its bias: z = the bf16 output of the plain
+// linear, stored to preact [m][n] when not NULL, then out = bf16(residual + act(z)) with
+// act (NVFP4_ACT_*) and the sum in fp32.  residual [m][n] bf16, NULL, or out itself: every
+// element is read by the thread that writes it, just before.
+struct Epilogue {
+  const uint16_t* residual = nullptr;
+  uint16_t* preact = nullptr;
+  int act = 0;
+  bool active() const { return residual != nullptr || preact != nullptr || act != 0; }
+};
+
 // Upper bound on the number of per-block partial maxima of the amax pass, and on the
 // number of segments (row blocks with their own scale) of one call.
 constexpr int kMaxAmaxPartials = 8192;
@@ -71,7 +82,7 @@ hipError_t launch_scale_layout(const uint8_t* src, uint8_t* dst, int64_t rows, i
 hipError_t launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
                        const float* gsf_a, const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias,
-                       uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t s);
+                       const Epilogue& ep, uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t s);
 
 // Compute units of the current device (cached per device).
 int compute_units();
@@ -85,8 +96,8 @@ bool gemm_pipe_supported(int64_t m, int64_t k, int64_t n, const void* a_codes, c
 size_t gemm_pipe_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus);
 hipError_t launch_gemm_pipe(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                             const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                            const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
-                            void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
+                            const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep,
+                            uint16_t* out, void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
 
 // The decode GEMM for m <= kDecodeA16Rows activation rows given as the fp16 operand
 // form a16 [m][k] (launch_quantize's a16 output) instead of codes and scales, so the
@@ -96,8 +107,8 @@ constexpr int kDecodeA16Rows = 4;
 bool gemm_decode_a16_supported(int64_t m, int64_t k, const void* a16, const void* b_codes, const void* b_scales);
 hipError_t launch_gemm_decode_a16(const uint16_t* a16, int64_t m, int64_t k, const uint8_t* b_codes,
                                   const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b,
-                                  const uint16_t* bias, uint16_t* out, void* workspace, size_t workspace_bytes,
-                                  int cus, hipStream_t s);
+                                  const uint16_t* bias, const Epilogue& ep, uint16_t* out, void* workspace,
+                                  size_t workspace_bytes, int cus, hipStream_t s);
 
 // The weight-streaming GEMM for m <= 128 (gemm_skinny.hip): K a multiple of 32, code
 // pointers 16-byte and scale pointers 4-byte aligned.  Splits K across blocks when the
@@ -107,8 +118,8 @@ bool gemm_skinny_supported(int64_t m, int64_t k, const void* a_codes, const void
 size_t gemm_skinny_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus);
 hipError_t launch_gemm_skinny(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                               const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                              const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, uint16_t* out,
-                              void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
+                              const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep,
+                              uint16_t* out, void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
 
 // The whole linear for up to 16 activation rows with a static scale, in the
 // weight-streaming kernel: each block quantizes its K range of the bf16 rows x [m][k]
@@ -124,8 +135,71 @@ bool linear_decode_fused_supported(int64_t m, int64_t k, int64_t n, bool dynamic
                                    const void* b_codes, const void* b_scales, size_t workspace_bytes, int cus);
 hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_t* b_codes, const uint8_t* b_scales,
                                       int64_t n, const float* gsf_x, float* gsf_used, const float* gsf_w,
-                                      const uint16_t* bias, uint16_t* out, void* workspace, size_t workspace_bytes,
-                                      int cus, hipStream_t s);
+                                      const uint16_t* bias, const Epilogue& ep, uint16_t* out, void* workspace,
+                                      size_t workspace_bytes, int cus, hipStream_t s);
+
+// RMS norm (norm.hip), k a multiple of 16 up to kNormMaxK.  x is bf16 or (x_f32) fp32;
+// with a residual (bf16, or fp32 with stream_f32; an fp32 x takes an fp32 one) r receives
+// the rounded sum.  kNormOut writes y (bf16) and, with codes not NULL, its checkpoint;
+// kNormStatic and kNormDynamic write NVFP4 codes and scales under *gsf or the dynamic
+// scale (gsf_out: the scale used); dynamic takes rstd [rows] and partials [kNormPartials].
+constexpr int64_t kNormMaxK = 16384;
+constexpr int kNormPartials = 1024;
+enum NormMode { kNormOut, kNormStatic, kNormDynamic, kNormOneRow, kNormStats };   // the last two: internal
+struct NormForward {
+  const void* x;
+  const void* residual;
+  const void* w;
+  void* r;
+  int64_t rows, k;
+  double eps;
+  bool x_f32, stream_f32, w_f32;
+  int mode;
+  uint16_t* y;
+  uint8_t *codes, *scales;
+  const float* gsf;
+  float *gsf_out, *rstd, *partials;
+  int lanes;   // set by the launcher
+};
+hipError_t launch_rmsnorm(NormForward a, hipStream_t s);
+
+// Its gradient: grad_r [rows][k] (the stream's type; grad_residual, of that type, is added
+// when not NULL) and, when not NULL, grad_w [k] fp32 through partials.
+struct NormBackward {
+  const uint16_t* gy;
+  const void *r, *w, *grad_residual;
+  int64_t rows, k;
+  double eps;
+  bool stream_f32, w_f32;
+  void* grad_r;
+  float *grad_w, *partials;
+  int lanes;   // set by the launcher
+};
+size_t rmsnorm_backward_partial_floats(int64_t rows, int64_t k);
+hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s);
+
+// 8-bit checkpoints (checkpoint.hip): codes [rows][k], scales [rows][ceil(k / 32)].
+hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t rows, int64_t k, int group, float inv_sqrt_g,
+                                  uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k, void* out,
+                                    bool out_bf16, hipStream_t s);
+hipError_t launch_swiglu_checkpoint(const uint16_t* gate, const uint16_t* up, int64_t rows, int64_t k, uint16_t* x,
+                                    uint8_t* gate_codes, uint8_t* gate_scales, uint8_t* up_codes, uint8_t* up_scales,
+                                    hipStream_t s);
+// Saved operands are checkpoint codes, or bf16 where their scales are NULL.
+hipError_t launch_swiglu_backward(const uint16_t* gy, const void* gate, const uint8_t* gate_scales, const void* up,
+                                  const uint8_t* up_scales, int64_t rows, int64_t k, uint16_t* grad_gate,
+                                  uint16_t* grad_up, hipStream_t s);
+hipError_t launch_activation_backward(const uint16_t* gy, const void* z, const uint8_t* z_scales, int64_t rows,
+                                      int64_t k, int act, uint16_t* grad_z, hipStream_t s);
+
+// grad_w [n][k] (fp32, or bf16) = sum over rows of gy [rows][n] x checkpoint [rows][k]
+// (weight_grad.hip).  partial: fp32 split sums, weight_grad_workspace_bytes of them, or
+// NULL (unsplit).
+size_t weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int cus);
+hipError_t launch_weight_grad(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales,
+                              int64_t k, void* grad_w, bool out_bf16, void* workspace, size_t workspace_bytes,
+                              int cus, hipStream_t s);
 
 // Workspace the GEMM dispatcher can use for an [m, k] x [n, k] product (0 if none).
 size_t gemm_workspace_bytes(int64_t m, int64_t k, int64_t n);

@@ -1,0 +1,310 @@
+// Weight gradient from an 8-bit checkpoint on gfx950 matrix cores:
+//
+//   grad_w[n][k] = sum over rows m of gy[m][n] * x[m][k],   x = E4M3 code * 2^(s - 127)
+//
+// gy is bf16 as it arrives; a code times its power of two is exact in bf16, so the bf16
+// MFMA multiplies the checkpoint's values exactly and accumulates in fp32: nothing is
+// rounded before the sum.
+//
+// Both operands have the contraction (rows) as their slow dimension, while an MFMA lane
+// needs consecutive contraction values of one column.  The transposition costs nothing:
+// LDS holds the tiles as they are in memory, [64 rows][256 columns] of bf16, and
+// ds_read_b64_tr_b16 hands each lane four rows of its column.
+//
+// One 256-thread workgroup per 256 x 256 tile of grad_w, one wave per SIMD, each wave
+// 128 x 128 (4 x 4 tiles of v_mfma_f32_32x32x16_bf16), rows in steps of 64 through two
+// LDS stages:
+//   * gy goes global -> LDS directly, 16 bytes a lane;
+//   * codes go through registers: loaded a step ahead, expanded by the hardware's scaled
+//     conversion (one instruction per two values), written to LDS as bf16;
+//   * a 512-byte row holds 32 chunks of 16 bytes, chunk c at position c ^ 4 (row % 4): the
+//     four rows that one transposed read gathers then lie in different banks;
+//   * rows and columns past the end read a zero chunk, so they add nothing even where gy
+//     holds infinities.
+// Few tiles (a narrow projection) leave compute units idle, so the rows are split across
+// workgroups into fp32 partials that weight_grad_reduce adds in split order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "checkpoint_device.h"
+#include "gemm_common.h"
+#include "nvfp4_device.h"
+#include "nvfp4_launch.h"
+
+namespace nvfp4 {
+namespace {
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef short short8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kTile = 256;                  // columns of gy, and of x, per workgroup
+constexpr int kStep = 64;                   // rows per LDS stage
+constexpr int kRowBytes = kTile * 2;
+constexpr int kPanel = kStep * kRowBytes;   // one operand of one stage, 32 KB
+constexpr int kLds = 4 * kPanel;
+constexpr int kBand = 4;                    // tile rows per band of the tile order
+
+__device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {};
+
+// Position of chunk c in row r.
+__device__ __forceinline__ int swz(int r, int c) { return c ^ ((r & 3) << 2); }
+
+// One 16-byte global -> LDS copy per lane; the address is a wave-uniform LDS base plus
+// 16 bytes a lane.  Inline asm so that the compiler does not hold LDS reads back for it:
+// step_barrier waits for it.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
+  asm volatile("global_load_lds_dwordx4 %1, off" :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(src) : "memory");
+}
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Four rows of one column (see the lane layout at the reads below).
+__device__ __forceinline__ short4_t read_tr(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4_t*)p);
+}
+
+// 16 codes -> 32 bytes of bf16.
+__device__ __forceinline__ void expand16(const uint4& c, float scale, uint4 (&o)[2]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false));
+    r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true));
+  }
+  o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// kAligned: rows of gy start on 16-byte boundaries (N a multiple of 8) and take the direct
+// copies; otherwise they are gathered value by value.
+template <bool kAligned, bool kOutBf16>
+__global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __restrict__ gy, int64_t m, int64_t n,
+                                                             const uint8_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, int64_t k,
+                                                             void* __restrict__ out, int tiles_n, int tiles_k,
+                                                             int splits, float* __restrict__ partial) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  // Workgroups are dealt round-robin to the 8 XCDs: each XCD gets a contiguous run of
+  // tiles, ordered in bands of kBand tile rows, so the tiles resident on one XCD share
+  // operand columns in its L2.  With splits, the splits of a tile follow each other.
+  const int nblk = gridDim.x;
+  int bid = blockIdx.x;
+  if ((nblk & 7) == 0) bid = (bid & 7) * (nblk >> 3) + (bid >> 3);
+  const int split = bid % splits;
+  bid /= splits;
+  const int band = bid / (kBand * tiles_k);
+  const int band_rows = min(tiles_n - band * kBand, kBand);
+  const int in_band = bid - band * kBand * tiles_k;
+  const int64_t n0 = (int64_t)(band * kBand + in_band % band_rows) * kTile;
+  const int64_t k0 = (int64_t)(in_band / band_rows) * kTile;
+
+  const int t = threadIdx.x;
+  const int lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wn = wave >> 1, wk = wave & 1;
+  const int64_t steps = (m + kStep - 1) / kStep;
+  const int64_t s_begin = steps * split / splits, s_end = steps * (split + 1) / splits;
+  const int64_t kb = (k + kCkBlock - 1) / kCkBlock;
+
+  auto panel_a = [&](int64_t s) { return lds + (int)(s & 1) * 2 * kPanel; };
+  auto panel_b = [&](int64_t s) { return lds + (int)(s & 1) * 2 * kPanel + kPanel; };
+
+  // gy: instruction i of wave w fills rows 16 w + 2 i and + 1 of the panel
+  auto stage_gy = [&](int64_t s) {
+    uint8_t* dst = panel_a(s);
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 16 * wave + 2 * i + (lane >> 5);
+        const int64_t row = s * kStep + r;
+        const int64_t col = n0 + 8 * swz(r, lane & 31);
+        const uint8_t* src = row < m && col < n ? reinterpret_cast<const uint8_t*>(gy + row * n + col) : kZeros;
+        copy16_to_lds(src, dst + (16 * wave + 2 * i) * kRowBytes);
+      }
+    } else {
+      for (int i = t; i < kStep * 32; i += 256) {
+        const int r = i >> 5, c = i & 31;
+        const int64_t row = s * kStep + r;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (row < m) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int64_t col = n0 + 8 * c + e;
+            if (col < n) w[e >> 1] |= (uint32_t)gy[row * n + col] << (16 * (e & 1));
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+  // codes: thread t takes 16-value chunk t % 16 of rows t / 16 + 16 i
+  const int64_t xcol = k0 + 16 * (t & 15);
+  const bool xcol_in = xcol < k;
+  uint4 xc[4];
+  uint32_t xs[4];
+  auto load_x = [&](int64_t s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = s * kStep + (t >> 4) + 16 * i;
+      const bool in = s < s_end && row < m && xcol_in;
+      xc[i] = in ? *reinterpret_cast<const uint4*>(codes + row * k + xcol) : make_uint4(0, 0, 0, 0);
+      xs[i] = in ? scales[row * kb + (xcol >> 5)] : 127u;
+    }
+  };
+  auto store_x = [&](int64_t s) {
+    uint8_t* dst = panel_b(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (t >> 4) + 16 * i;
+      uint4 o[2];
+      expand16(xc[i], pow2f((int)xs[i] - 127), o);
+      uint4* d = reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, 2 * (t & 15)) * 16);
+      d[0] = o[0];
+      d[1] = o[1];
+    }
+  };
+
+  // Fragment reads.  The 16 lanes of a group together address four rows of 16 columns (lane
+  // j: row j / 4, columns 4 (j % 4) ..) and receive one column each: lane j column j, the
+  // four rows in order.  An MFMA lane l holds column l % 32 and rows 8 (l / 32) .. + 7 of
+  // the 16-row sub-step: two reads.  Row % 4 is (l % 16) / 4 for every read of a lane.
+  const int q = (lane & 15) >> 2;
+  const int lrow = 8 * (lane >> 5) + q;
+  const int lbyte = lrow * kRowBytes + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+  auto fragment = [&](const uint8_t* panel, int half, int i, int sub) {
+    const uint8_t* p = panel + lbyte + half * 256 + ((i ^ q) << 6) + sub * 16 * kRowBytes;
+    const short4_t lo = read_tr(p), hi = read_tr(p + 4 * kRowBytes);
+    return __builtin_bit_cast(bf16x8_t, (short8_t){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  };
+
+  float16_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  if (s_begin < s_end) {
+    stage_gy(s_begin);
+    load_x(s_begin);
+    store_x(s_begin);
+    load_x(s_begin + 1);
+  }
+  step_barrier();
+  for (int64_t s = s_begin; s < s_end; ++s) {
+    if (s + 1 < s_end) {
+      stage_gy(s + 1);
+      store_x(s + 1);
+      load_x(s + 2);
+    }
+    const uint8_t *pa = panel_a(s), *pb = panel_b(s);
+#pragma unroll
+    for (int sub = 0; sub < kStep / 16; ++sub) {
+      bf16x8_t fa[4], fb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i] = fragment(pa, wn, i, sub);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[j] = fragment(pb, wk, j, sub);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+    step_barrier();
+  }
+
+  // Entry e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32 of the block.
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t col = k0 + wk * 128 + 32 * j + (lane & 31);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t row = n0 + wn * 128 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        if (row < n && col < k) {
+          if (splits > 1) partial[((int64_t)split * n + row) * k + col] = acc[i][j][e];
+          else if (kOutBf16) static_cast<uint16_t*>(out)[row * k + col] = (uint16_t)gemm::pack_bf16x2(acc[i][j][e], 0.0f);
+          else static_cast<float*>(out)[row * k + col] = acc[i][j][e];
+        }
+      }
+    }
+  }
+}
+
+// Adds the partials [splits][count] in split order, four values per thread (k is a
+// multiple of 16, so count is one of 4).
+template <bool kOutBf16>
+__global__ void __launch_bounds__(256) weight_grad_reduce(const float* __restrict__ partial, int splits, int64_t count,
+                                                          void* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  float4 a = *reinterpret_cast<const float4*>(partial + i);
+  for (int s = 1; s < splits; ++s) {
+    const float4 b = *reinterpret_cast<const float4*>(partial + s * count + i);
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  }
+  if (kOutBf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) =
+        make_uint2(gemm::pack_bf16x2(a.x, a.y), gemm::pack_bf16x2(a.z, a.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = a;
+}
+
+// Row splits: as many as fill the compute units once, each at least four steps long.
+int row_splits(int64_t m, int64_t n, int64_t k, int cus) {
+  const int64_t tiles = ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
+  const int64_t steps = (m + kStep - 1) / kStep;
+  int64_t sp = std::min<int64_t>(cus / tiles, steps / 4);
+  return (int)std::max<int64_t>(sp, 1);
+}
+
+template <bool kAligned, bool kOutBf16>
+hipError_t launch_t(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales, int64_t k,
+                    void* grad_w, int splits, float* partial, hipStream_t s) {
+  static bool attr_set[kMaxDevices] = {};
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&weight_grad_kernel<kAligned, kOutBf16>), kLds,
+                                          attr_set);
+      e != hipSuccess)
+    return e;
+  const int tn = (int)((n + kTile - 1) / kTile), tk = (int)((k + kTile - 1) / kTile);
+  hipLaunchKernelGGL((weight_grad_kernel<kAligned, kOutBf16>), dim3((uint32_t)((int64_t)tn * tk * splits)), dim3(256),
+                     kLds, s, gy, m, n, codes, scales, k, grad_w, tn, tk, splits, partial);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t count = n * k;
+  hipLaunchKernelGGL((weight_grad_reduce<kOutBf16>), dim3((uint32_t)((count / 4 + 255) / 256)), dim3(256), 0, s,
+                     partial, splits, count, grad_w);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int cus) {
+  const int sp = row_splits(m, n, k, cus);
+  return sp > 1 ? (size_t)sp * (size_t)n * (size_t)k * sizeof(float) : 0;
+}
+
+hipError_t launch_weight_grad(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales,
+                              int64_t k, void* grad_w, bool out_bf16, void* workspace, size_t workspace_bytes,
+                              int cus, hipStream_t s) {
+  int splits = row_splits(m, n, k, cus);
+  if (splits > 1 && (workspace == nullptr || workspace_bytes < weight_grad_workspace_bytes(m, n, k, cus))) splits = 1;
+  float* partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  using Fn = decltype(&launch_t<false, false>);
+  static constexpr Fn f[2][2] = {{launch_t<false, false>, launch_t<false, true>},
+                                 {launch_t<true, false>, launch_t<true, true>}};
+  return f[n % 8 == 0 ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, splits, partial, s);
+}
+
+}  // namespace nvfp4

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -20,6 +21,9 @@ from ._lib import check, lib
 NVFP4_BLOCK_SIZE = 16
 SCALE_TILE_K = 128
 MAX_ROTATION_GROUP = 128
+ACTIVATIONS = {None: _lib.NVFP4_ACT_NONE, "silu": _lib.NVFP4_ACT_SILU, "gelu": _lib.NVFP4_ACT_GELU,
+               "gelu_tanh": _lib.NVFP4_ACT_GELU_TANH}
+DTYPE_CODES = {torch.bfloat16: _lib.NVFP4_DTYPE_BF16, torch.float32: _lib.NVFP4_DTYPE_F32}
 
 
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p | None:
@@ -43,6 +47,58 @@ def _require_cuda(name: str, t: torch.Tensor, dtype: torch.dtype | None = None, 
         raise ValueError(f"{name} must be contiguous")
     if t.data_ptr() % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _activation_code(activation: str | None) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}; the activations are {tuple(ACTIVATIONS)}")
+    return ACTIVATIONS[activation]
+
+
+def _require_device(device: torch.device, **tensors: torch.Tensor | None) -> None:
+    """Every given tensor lives on ``device``."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _on_device(fn):
+    """Runs ``fn`` with its first tensor's device current: the library launches on, sizes its
+    workspaces for and keeps kernel attributes of the current device."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else next(iter(kwargs.values()), None)
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
+    return call
+
+
+def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, out) -> torch.Tensor | None:
+    """Checks a linear's epilogue arguments; returns the residual as a contiguous [m, n]."""
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.dtype != torch.bfloat16 or residual.numel() != m * n \
+                or residual.shape[-1:] != (n,):
+            raise ValueError(f"residual must be bf16 with {m} rows of {n}, got "
+                             f"{getattr(residual, 'dtype', None)} {list(getattr(residual, 'shape', []))}")
+        _require_device(device, residual=residual)
+        residual = residual.reshape(m, n)
+        if not residual.is_contiguous():
+            residual = residual.contiguous()
+    for name, t in (("preact", preact), ("out", out)):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or t.shape != (m, n) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 [{m}, {n}] tensor")
+        _require_device(device, **{name: t})
+    named = [(name, t.data_ptr()) for name, t in (("out", out), ("residual", residual), ("preact", preact))
+             if t is not None]
+    for i, (a, pa) in enumerate(named):
+        for b, pb in named[i + 1:]:
+            if abs(pa - pb) < 2 * m * n and not (pa == pb and (a, b) == ("out", "residual")):
+                raise ValueError(f"{a} and {b} must not overlap (residual may be out itself)")
+    return residual
 
 
 def scale_bytes(rows: int, k: int) -> int:
@@ -125,12 +181,14 @@ def quantize_activation(x: torch.Tensor, global_sf_x=None, rotation_group: int =
     return codes, scales[: scale_bytes(m, k)], gsf
 
 
+@_on_device
 def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
                global_sf_x, global_sf_w, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
-               workspace: torch.Tensor | None = None, split_k: bool = True) -> torch.Tensor:
+               workspace: torch.Tensor | None = None, split_k: bool = True, activation: str | None = None,
+               residual: torch.Tensor | None = None, preact: torch.Tensor | None = None) -> torch.Tensor:
     """Block-scaled GEMM on already quantized activations; bf16 [M, N].
 
-    With ``split_k`` (default) a workspace of gemm_workspace_bytes is used (allocated
+    ``activation``, ``residual`` and ``preact``: the epilogue of :func:`nvfp4_linear`.  With ``split_k`` (default) a workspace of gemm_workspace_bytes is used (allocated
     here if not given) so the last partial round of tiles is split along K."""
     _require_cuda("x_codes", x_codes, torch.uint8, 2)
     _require_cuda("packed", packed, torch.uint8, 2)
@@ -159,18 +217,34 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         ws_bytes = 0 if workspace is None else workspace.numel()
     else:
         workspace = None
+    act = _activation_code(activation)
+    if act or residual is not None or preact is not None:
+        _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias)
+        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, out)
+        check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
+                                        _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
+                                        _ptr(workspace), ws_bytes, _stream(x_codes.device)))
+        return out
     check(lib().nvfp4_gemm(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx), _ptr(gw),
                            _ptr(bias), _ptr(out), _ptr(workspace), ws_bytes, _stream(x_codes.device)))
     return out
 
 
+@_on_device
 def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor, global_sf_w: torch.Tensor,
                  bias: torch.Tensor | None, out_features: int, global_sf_x=None, rotation_group: int = 0,
-                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 activation: str | None = None, residual: torch.Tensor | None = None,
+                 preact: torch.Tensor | None = None) -> torch.Tensor:
     """The NVFP4 W4A4 linear: (rotate,) global scale, quantize, block-scaled GEMM, alpha, bias.
 
     ``global_sf_x=None`` computes the activation scale dynamically from the
     call's 2-D input.  Leading dimensions of x are flattened and restored.
+
+    With ``activation`` ("silu", "gelu" or "gelu_tanh") or ``residual`` (bf16, the output's
+    shape) the epilogue goes on: from the plain linear's bf16 output z it forms
+    ``bf16(residual + act(z))``, the activation and the sum in fp32.  ``residual`` may be
+    ``out`` itself.  ``preact`` (contiguous bf16 [rows, out_features]) receives z.
     """
     if x.dtype != torch.bfloat16:
         raise ValueError(f"x must be bf16, got {x.dtype}")
@@ -199,6 +273,15 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
+    act = _activation_code(activation)
+    if act or residual is not None or preact is not None:
+        _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias)
+        residual = _epilogue_tensors(m, out_features, x.device, residual, preact, out)
+        check(lib().nvfp4_linear_epilogue(_ptr(x2d), None, m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
+                                          out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
+                                          _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
+                                          _stream(x.device)))
+        return out.reshape(*orig[:-1], out_features)
     check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
                              _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
                              _stream(x.device)))
@@ -298,11 +381,14 @@ def quantize_swiglu(gate: torch.Tensor, up: torch.Tensor, global_sf_x=None
     return codes, scales[: scale_bytes(m, k)], gsf
 
 
+@_on_device
 def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
                         global_sf_w: torch.Tensor, bias: torch.Tensor | None, out_features: int, global_sf_x=None,
-                        workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+                        workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        activation: str | None = None, residual: torch.Tensor | None = None,
+                        preact: torch.Tensor | None = None) -> torch.Tensor:
     """down_proj on silu(gate) * up, the product never written (same result as
-    nvfp4_linear(swiglu(gate, up), ...))."""
+    nvfp4_linear(swiglu(gate, up), ...), with the same epilogue arguments)."""
     g2, u2 = _gate_up(gate, up)
     m, k = g2.shape
     _require_cuda("packed", packed, torch.uint8, 2)
@@ -323,6 +409,14 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
         workspace = torch.empty((need,), dtype=torch.uint8, device=gate.device)
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=gate.device)
+    act = _activation_code(activation)
+    if act or residual is not None or preact is not None:
+        _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias)
+        residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, out)
+        check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
+                                          out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
+                                          _ptr(workspace), workspace.numel(), _stream(gate.device)))
+        return out.reshape(*gate.shape[:-1], out_features)
     check(lib().nvfp4_linear_swiglu(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                     out_features, _ptr(gx), _ptr(out), _ptr(workspace), workspace.numel(),
                                     _stream(gate.device)))
@@ -455,51 +549,104 @@ class _NVFP4STEFn(torch.autograd.Function):
     so the rotation is its own transpose), grad_W = grad_y^T rotate(x), grad_b = sum of
     grad_y over rows; the products accumulate in fp32 and grad_x is rounded to bf16 once,
     after its rotation.  The two products are plain library GEMMs (hipBLASLt through
-    torch.matmul): the backward is not part of the inference path."""
+    torch.matmul): the backward is not part of the inference path.
+
+    With ``saved`` the input is kept as its 8-bit checkpoint (already rotated) instead of
+    bf16, and grad_W comes from :func:`weight_grad` on it: the library's own product on
+    E4M3 values, fp32 sums.  With an activation the forward also keeps the epilogue's z
+    (in 8 bits when the input is), and the gradient passes act'(z) first; the residual's
+    gradient is grad_y itself."""
 
     @staticmethod
-    def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias, global_sf_x, group: int):
+    def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias, global_sf_x, group: int, saved=None,
+                activation=None, residual=None):
+        from . import checkpoint as ck
+        n = weight.shape[0]
         packed, inv_scale, gsf_w = quantize_weight(weight.detach().to(torch.bfloat16).contiguous())
         b = None if bias is None else bias.detach().to(torch.bfloat16).contiguous()
-        ctx.save_for_backward(x, weight)
+        z = None
+        if activation is not None:
+            z = torch.empty((x.numel() // x.shape[-1], n), dtype=torch.bfloat16, device=x.device)
+        y = nvfp4_linear(x, packed, inv_scale, gsf_w, b, n, global_sf_x, group, activation=activation,
+                         residual=None if residual is None else residual.detach(), preact=z)
+        ctx.x_shape, ctx.x_dtype = x.shape, x.dtype
+        x_scales = z_scales = None
+        if z is not None and saved is not None and n % NVFP4_BLOCK_SIZE == 0:
+            z, z_scales, _ = ck.checkpoint_pack(z)
+        if saved is not None:
+            x, x_scales = saved
+        ctx.save_for_backward(x, weight, z, x_scales, z_scales)
         ctx.group = group
+        ctx.activation = activation
         ctx.has_bias = bias is not None
         ctx.bias_dtype = None if bias is None else bias.dtype
-        return nvfp4_linear(x, packed, inv_scale, gsf_w, b, weight.shape[0], global_sf_x, group)
+        return y
 
     @staticmethod
     def backward(ctx, grad_y: torch.Tensor):
-        x, weight = ctx.saved_tensors
+        from . import checkpoint as ck
+        x, weight, z, x_scales, z_scales = ctx.saved_tensors
+        packed_input = x_scales is not None
         n, k = weight.shape
         g = ctx.group
-        gy = grad_y.reshape(-1, n).float()
+        grad_r = grad_y if ctx.needs_input_grad[7] else None
+        gy2 = grad_y.reshape(-1, n)
+        if z is not None:
+            saved_z = z if z_scales is None else ck.Checkpoint(z, z_scales)
+            gy2 = ck.activation_backward(gy2, saved_z, ctx.activation)
+        gy = None
+        if ctx.needs_input_grad[0] or not packed_input or ctx.has_bias:
+            gy = gy2.float()
         grad_x = grad_w = grad_b = None
         if ctx.needs_input_grad[0]:
             gxr = gy @ weight.float()
-            grad_x = (rotate_activation(gxr.contiguous(), g, out_dtype=x.dtype) if g else gxr.to(x.dtype))
-            grad_x = grad_x.reshape(x.shape)
+            grad_x = (rotate_activation(gxr.contiguous(), g, out_dtype=ctx.x_dtype) if g else gxr.to(ctx.x_dtype))
+            grad_x = grad_x.reshape(ctx.x_shape)
         if ctx.needs_input_grad[1]:
-            x2 = x.reshape(-1, k)
-            xr = rotate_activation(x2.contiguous(), g) if g else x2
-            grad_w = (gy.t() @ xr.float()).to(weight.dtype)
+            if packed_input:
+                dtype = weight.dtype if weight.dtype in DTYPE_CODES else torch.float32
+                grad_w = ck.weight_grad(gy2, ck.Checkpoint(x, x_scales, g), dtype).to(weight.dtype)
+            else:
+                x2 = x.reshape(-1, k)
+                xr = rotate_activation(x2.contiguous(), g) if g else x2
+                grad_w = (gy.t() @ xr.float()).to(weight.dtype)
         if ctx.has_bias and ctx.needs_input_grad[2]:
             grad_b = gy.sum(0).to(ctx.bias_dtype)
-        return grad_x, grad_w, grad_b, None, None
+        return grad_x, grad_w, grad_b, None, None, None, None, grad_r
 
 
 def nvfp4_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, global_sf_x=None,
-                       rotation_group: int = 0) -> torch.Tensor:
+                       rotation_group: int = 0, checkpoint=None, activation: str | None = None,
+                       residual: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable NVFP4 linear for training (straight-through estimator).
 
     ``weight`` is the full-precision master [out, in] (already rotated along ``in`` when
     ``rotation_group`` is set, as from_weight's fold leaves it); ``x`` is cast to bf16.
     The forward equals :func:`nvfp4_linear` on the packed master weight; gradients flow
-    to ``x``, ``weight`` and ``bias`` as through the full-precision linear."""
+    to ``x``, ``weight`` and ``bias`` as through the full-precision linear.
+
+    ``checkpoint``: None keeps ``x`` in bf16 for the backward; True keeps it as an 8-bit
+    checkpoint packed here; a :class:`Checkpoint` of ``x`` (from :func:`rmsnorm_train` or
+    :func:`checkpoint_pack` with this rotation group) is shared, so several linears on one
+    input keep it once.  grad_W is then taken at the checkpoint's values.  ``activation``
+    and ``residual`` (bf16, gets its gradient too): the epilogue of :func:`nvfp4_linear`."""
+    from . import checkpoint as ck
     x = x.to(torch.bfloat16)
     if x.dim() < 1 or not x.is_contiguous():
         x = x.contiguous()
     gx = None if global_sf_x is None else _scalar_f32(global_sf_x, x.device)
-    return _NVFP4STEFn.apply(x, weight, bias, gx, int(rotation_group or 0))
+    group = int(rotation_group or 0)
+    _activation_code(activation)
+    saved = None
+    if checkpoint is not None and checkpoint is not False:
+        held = ck.checkpoint_pack(x.detach(), group) if checkpoint is True else checkpoint
+        if not isinstance(held, ck.Checkpoint):
+            raise TypeError("checkpoint must be None, True or a Checkpoint")
+        if held.rotation_group != group or held.codes.numel() != x.numel() or held.codes.shape[-1] != x.shape[-1]:
+            raise ValueError(f"checkpoint holds {list(held.codes.shape)} under rotation group {held.rotation_group}; "
+                             f"the linear's input is {list(x.shape)} under {group}")
+        saved = (held.codes.reshape(-1, x.shape[-1]), held.scales.reshape(-1, held.scales.shape[-1]))
+    return _NVFP4STEFn.apply(x, weight, bias, gx, group, saved, activation, residual)
 
 
 def _check_layer_geometry(packed: torch.Tensor, in_features: int, rotation_group: int | None) -> None:
@@ -595,7 +742,9 @@ class NVFP4Linear:
         """Switch to a static scale from a recorded abs-max (a float or an fp32 device scalar)."""
         self.act_scale, self.input_amax, self.margin, self._gsf_x = "static", input_amax, float(margin), None
 
-    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor, activation: str | None = None,
+                 residual: torch.Tensor | None = None) -> torch.Tensor:
+        """The linear on ``x``; ``activation`` and ``residual`` as in :func:`nvfp4_linear`."""
         x = x.to(torch.bfloat16)
         g = self.rotation_group or 0
         if self._record is not None:
@@ -604,7 +753,8 @@ class NVFP4Linear:
             gsf = None
         else:
             gsf = self.activation_global_sf()
-        return nvfp4_linear(x, self.packed, self.inv_scale, self.global_sf_w, self.bias, self.out_features, gsf, g)
+        return nvfp4_linear(x, self.packed, self.inv_scale, self.global_sf_w, self.bias, self.out_features, gsf, g,
+                            activation=activation, residual=residual)
 
     def dequantized_weight(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The packed weight expanded back to ``dtype`` (the W4A16 fallback's weight)."""

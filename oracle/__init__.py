@@ -6,3 +6,4 @@ binding) never imports, calls or links it, and the two share no code.
 """
 from .nvfp4 import *  # noqa: F401,F403
 from .nvfp4 import __all__  # noqa: F401
+from .operators import *  # noqa: F401,F403
