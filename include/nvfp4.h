@@ -307,14 +307,15 @@ int nvfp4_dequantize(const uint8_t* packed_dev, const uint8_t* scale_dev, int64_
 
 /*
  * nvfp4_linear_epilogue: nvfp4_linear with an activation and a residual in the epilogue.
- * With z the bf16 output of nvfp4_linear for the same arguments,
- *     out = bf16(residual + act(z)),   act and the sum in fp32, one rounding.
+ * With acc the fp32 product of nvfp4_linear,
+ *     z = alpha * acc + bias,     out = bf16(act(z) + residual),
+ * all in fp32 with that one rounding (nvfp4_linear itself rounds the product to bf16 and
+ * the sum with the bias again).
  * activation: NVFP4_ACT_*.  residual_dev: bf16 [m][out_features], NULL for none; it may be
  * out_dev itself (the update in place of a residual stream), but not overlap it otherwise.
- * preact_dev: NULL, or bf16 [m][out_features] that receives z (nvfp4_activation_backward
- * takes it); it overlaps neither.  up_dev: NULL, or the input is the SwiGLU product of
- * x_dev (gate) and up_dev as in nvfp4_linear_swiglu (rotation_group 0; z is then that
- * call's output).  workspace: that of nvfp4_linear, or of nvfp4_linear_swiglu with up_dev.
+ * preact_dev: NULL, or bf16 [m][out_features] that receives bf16(z) (where
+ * nvfp4_activation_backward takes the derivative); it overlaps neither.  up_dev: NULL, or the input is the SwiGLU product of
+ * x_dev (gate) and up_dev as in nvfp4_linear_swiglu (rotation_group 0).  workspace: that of nvfp4_linear, or of nvfp4_linear_swiglu with up_dev.
  */
 int nvfp4_linear_epilogue(const void* x_dev, const void* up_dev, int64_t m, int64_t k,
                           const uint8_t* packed_dev, const uint8_t* inv_scale_dev, const float* global_sf_w_dev,
@@ -322,7 +323,7 @@ int nvfp4_linear_epilogue(const void* x_dev, const void* up_dev, int64_t m, int6
                           int rotation_group, int activation, const void* residual_dev, void* preact_dev,
                           void* out_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
 
-/* nvfp4_gemm_epilogue: the same epilogue on nvfp4_gemm (z its bf16 output). */
+/* nvfp4_gemm_epilogue: the same epilogue on nvfp4_gemm. */
 int nvfp4_gemm_epilogue(const uint8_t* x_codes_dev, const uint8_t* x_scale_dev, int64_t m, int64_t k,
                         const uint8_t* packed_dev, const uint8_t* inv_scale_dev, int64_t n,
                         const float* gsf_x_dev, const float* gsf_w_dev, const void* bias_dev, int activation,

@@ -12,8 +12,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import check, lib
-from .nvfp4 import (DTYPE_CODES, _activation_code, _gate_up, _on_device, _ptr, _require_cuda,
-                    _require_device, _stream)
+from .nvfp4 import (DTYPE_CODES, _activation_code, _gate_up, _on_device, _ptr, _require_device, _stream)
 
 CHECKPOINT_BLOCK = 32
 
@@ -35,33 +34,35 @@ def _scale_columns(k: int) -> int:
     return (k + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
 
 
-def _rows2d(name: str, t: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
-    """``t`` as contiguous 16-byte aligned rows [.., K] (copied where its strides or address
-    differ)."""
+def _rows(name: str, t: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> tuple[torch.Tensor, int, int]:
+    """``t`` [..., K] as contiguous 16-byte aligned rows on a GPU (copied where its strides or
+    address differ), with the number of rows and K."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() < 1:
-        raise ValueError(f"{name} must have at least one dimension")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
     k = t.shape[-1]
-    t2 = t.reshape(t.numel() // k if k else 0, k).contiguous()
-    if t2.data_ptr() % 16:
-        t2 = t2.clone()
-    _require_cuda(name, t2, dtype, 2)
-    return t2
+    rows = t.numel() // k if k else 0
+    if not t.is_contiguous():
+        t = t.contiguous()
+    if t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t, rows, k
 
 
-def _saved2d(name: str, ck: Checkpoint) -> tuple[torch.Tensor, torch.Tensor]:
-    """A checkpoint's codes [rows, K] and scales [rows, ceil(K/32)], checked."""
-    codes = _rows2d(f"{name}.codes", ck.codes, torch.uint8)
-    rows, k = codes.shape
-    scales = ck.scales
-    if scales.dtype != torch.uint8 or scales.device != codes.device or scales.numel() != rows * _scale_columns(k) \
-            or scales.shape[-1:] != (_scale_columns(k),):
-        raise ValueError(f"{name}.scales must be uint8 with {rows} rows of {_scale_columns(k)} on {codes.device}, got "
+def _saved(name: str, ck: Checkpoint) -> tuple[torch.Tensor, torch.Tensor, int, int]:
+    """A checkpoint's codes and scales as contiguous rows, checked, with the rows and K."""
+    codes, rows, k = _rows(f"{name}.codes", ck.codes, torch.uint8)
+    scales, cols = ck.scales, _scale_columns(k)
+    if scales.dtype != torch.uint8 or scales.device != codes.device or scales.numel() != rows * cols \
+            or scales.shape[-1:] != (cols,):
+        raise ValueError(f"{name}.scales must be uint8 with {rows} rows of {cols} on {codes.device}, got "
                          f"{scales.dtype} {list(scales.shape)} on {scales.device}")
-    return codes, scales.reshape(rows, _scale_columns(k)).contiguous()
+    return codes, scales if scales.is_contiguous() else scales.contiguous(), rows, k
 
 
 def _empty_checkpoint(shape, device, rotation_group: int = 0) -> Checkpoint:
@@ -74,10 +75,10 @@ def _empty_checkpoint(shape, device, rotation_group: int = 0) -> Checkpoint:
 def checkpoint_pack(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
     """bf16 [..., K] (K a multiple of 16) to its 8-bit checkpoint, after the optional block
     rotation.  A value moves by at most 2^-4 of itself; infinities and NaN become NaN."""
-    x2 = _rows2d("x", x)
+    x2, rows, k = _rows("x", x)
     ck = _empty_checkpoint(x.shape, x.device, int(rotation_group))
-    check(lib().nvfp4_checkpoint_pack(_ptr(x2), x2.shape[0], x2.shape[1], int(rotation_group), _ptr(ck.codes),
-                                      _ptr(ck.scales), _stream(x.device)))
+    check(lib().nvfp4_checkpoint_pack(_ptr(x2), rows, k, int(rotation_group), _ptr(ck.codes), _ptr(ck.scales),
+                                      _stream(x.device)))
     return ck
 
 
@@ -90,10 +91,10 @@ def checkpoint_unpack(ck: Checkpoint, dtype: torch.dtype = torch.bfloat16) -> to
 def _unpack(_device_of: torch.Tensor, ck: Checkpoint, dtype: torch.dtype) -> torch.Tensor:
     if dtype not in DTYPE_CODES:
         raise ValueError(f"checkpoint_unpack supports bf16 and fp32 outputs, got {dtype}")
-    codes, scales = _saved2d("checkpoint", ck)
+    codes, scales, rows, k = _saved("checkpoint", ck)
     out = torch.empty(ck.codes.shape, dtype=dtype, device=codes.device)
-    check(lib().nvfp4_checkpoint_unpack(_ptr(codes), _ptr(scales), codes.shape[0], codes.shape[1], _ptr(out),
-                                        DTYPE_CODES[dtype], _stream(codes.device)))
+    check(lib().nvfp4_checkpoint_unpack(_ptr(codes), _ptr(scales), rows, k, _ptr(out), DTYPE_CODES[dtype],
+                                        _stream(codes.device)))
     return out
 
 
@@ -102,14 +103,13 @@ def weight_grad(grad_y: torch.Tensor, ck: Checkpoint, dtype: torch.dtype = torch
     """The weight gradient of a linear from the checkpoint of its input: grad_y^T x, [N, K],
     for grad_y bf16 [..., N] and x [..., K].  Products are exact, sums fp32; ``dtype`` is the
     result's (fp32 or bf16).  The same inputs give the same bits."""
-    gy = _rows2d("grad_y", grad_y)
+    gy, m, n = _rows("grad_y", grad_y)
     if dtype not in DTYPE_CODES:
         raise ValueError(f"weight_grad supports fp32 and bf16 results, got {dtype}")
-    codes, scales = _saved2d("checkpoint", ck)
+    codes, scales, rows, k = _saved("checkpoint", ck)
     _require_device(gy.device, checkpoint=codes)
-    (m, n), k = gy.shape, codes.shape[1]
-    if codes.shape[0] != m:
-        raise ValueError(f"grad_y has {m} rows, the checkpoint {codes.shape[0]}")
+    if rows != m:
+        raise ValueError(f"grad_y has {m} rows, the checkpoint {rows}")
     out = torch.empty((n, k), dtype=dtype, device=gy.device)
     need = int(lib().nvfp4_weight_grad_workspace_bytes(m, n, k))
     ws = torch.empty((need,), dtype=torch.uint8, device=gy.device) if need else None
@@ -134,23 +134,25 @@ def swiglu_checkpoint(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tenso
 def swiglu_backward(grad_x: torch.Tensor, gate, up) -> tuple[torch.Tensor, torch.Tensor]:
     """Gradients (bf16) of :func:`swiglu` at ``gate`` and ``up``: both Checkpoints, or both
     bf16 tensors, of grad_x's shape."""
-    gx = _rows2d("grad_x", grad_x)
+    gx, rows, k = _rows("grad_x", grad_x)
     packed = isinstance(gate, Checkpoint)
     if packed != isinstance(up, Checkpoint):
         raise ValueError("gate and up must be both checkpoints or both bf16 tensors")
     if packed:
-        (g, gs), (u, us) = _saved2d("gate", gate), _saved2d("up", up)
         if gate.rotation_group or up.rotation_group:
             raise ValueError("gate and up must be packed without a rotation")
+        (g, gs, *gm), (u, us, *um) = _saved("gate", gate), _saved("up", up)
     else:
-        (g, gs), (u, us) = (_rows2d("gate", gate), None), (_rows2d("up", up), None)
+        gs = us = None
+        (g, *gm), (u, *um) = _rows("gate", gate), _rows("up", up)
     _require_device(gx.device, gate=g, up=u)
-    if g.shape != gx.shape or u.shape != gx.shape:
+    if gm != [rows, k] or um != [rows, k]:
         raise ValueError(f"grad_x, gate and up must have the same shape, got {list(gx.shape)}, {list(g.shape)} and "
                          f"{list(u.shape)}")
-    dg, du = (torch.empty(grad_x.shape, dtype=torch.bfloat16, device=gx.device) for _ in range(2))
-    check(lib().nvfp4_swiglu_backward(_ptr(gx), _ptr(g), _ptr(gs), _ptr(u), _ptr(us), gx.shape[0], gx.shape[1], _ptr(dg),
-                                      _ptr(du), _stream(gx.device)))
+    dg = torch.empty(grad_x.shape, dtype=torch.bfloat16, device=gx.device)
+    du = torch.empty_like(dg)
+    check(lib().nvfp4_swiglu_backward(_ptr(gx), _ptr(g), _ptr(gs), _ptr(u), _ptr(us), rows, k, _ptr(dg), _ptr(du),
+                                      _stream(gx.device)))
     return dg, du
 
 
@@ -158,20 +160,20 @@ def swiglu_backward(grad_x: torch.Tensor, gate, up) -> tuple[torch.Tensor, torch
 def activation_backward(grad_y: torch.Tensor, z, activation: str | None) -> torch.Tensor:
     """bf16(grad_y act'(z)): the gradient before the activation of a linear's epilogue.  ``z``:
     its ``preact`` (bf16, any width), or that tensor's Checkpoint."""
-    gy = _rows2d("grad_y", grad_y)
+    gy, rows, n = _rows("grad_y", grad_y)
     act = _activation_code(activation)
     if isinstance(z, Checkpoint):
         if z.rotation_group:
             raise ValueError("z must be packed without a rotation")
-        z2, zs = _saved2d("z", z)
+        z2, zs, *zm = _saved("z", z)
     else:
-        z2, zs = _rows2d("z", z), None
+        zs = None
+        z2, *zm = _rows("z", z)
     _require_device(gy.device, z=z2)
-    if z2.shape != gy.shape:
+    if zm != [rows, n]:
         raise ValueError(f"grad_y and z must have the same shape, got {list(gy.shape)} and {list(z2.shape)}")
     out = torch.empty(grad_y.shape, dtype=torch.bfloat16, device=gy.device)
-    check(lib().nvfp4_activation_backward(_ptr(gy), _ptr(z2), _ptr(zs), gy.shape[0], gy.shape[1], act, _ptr(out),
-                                          _stream(gy.device)))
+    check(lib().nvfp4_activation_backward(_ptr(gy), _ptr(z2), _ptr(zs), rows, n, act, _ptr(out), _stream(gy.device)))
     return out
 
 

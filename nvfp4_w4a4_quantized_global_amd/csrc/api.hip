@@ -715,7 +715,7 @@ int nvfp4_rmsnorm(const void* x, int x_dtype, const void* residual, int residual
 }
 
 size_t nvfp4_quantize_rmsnorm_workspace_bytes(int64_t rows) {
-  if (rows < 0) return 0;
+  if (rows <= 1) return 0;   // one row is one workgroup's: nothing to hand over
   return align_up(sizeof(float) * nvfp4::kNormPartials) + align_up(sizeof(float) * (size_t)rows);
 }
 
@@ -742,7 +742,7 @@ int nvfp4_quantize_rmsnorm(const void* x, int x_dtype, const void* residual, int
   a.scales = scales;
   a.gsf = global_sf;
   a.gsf_out = gsf_out;
-  if (global_sf == nullptr) {
+  if (need > 0) {
     a.partials = static_cast<float*>(workspace);
     a.rstd = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(sizeof(float) * nvfp4::kNormPartials));
   }

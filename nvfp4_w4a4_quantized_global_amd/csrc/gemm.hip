@@ -107,14 +107,17 @@ struct Cfg {
   static constexpr int kEpiRowBytes = TN * 32 * 2 + 16;
   static constexpr int kEpiLds = WM * WN * 32 * kEpiRowBytes;
   static constexpr int kLds = kLoopLds > kEpiLds ? kLoopLds : kEpiLds;
+  static constexpr int kEpiF32RowBytes = TN * 32 * 4 + 16;   // the fp32 epilogue's staging
+  static_assert(WM * WN * 32 * kEpiF32RowBytes <= kLds, "fits");
 };
 
-template <int WM, int WN, int TM, int TN>
+// kEpi: the epilogue with activation and residual.
+template <int WM, int WN, int TM, int TN, bool kEpi>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi,
+    const uint16_t* __restrict__ bias, const Epilogue ep,
     uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16) {
   using C = Cfg<WM, WN, TM, TN>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -237,6 +240,27 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
   for (int i = 0; i < TM; ++i) {
     float al[16];
     group_alphas(gsf_a, gsf_b, a_seg_rows, wrow0 + i * 32, kh, m, al);
+    if constexpr (kEpi) {
+      // in fp32 through the wave's LDS region, then element by element
+      float* f32 = reinterpret_cast<float*>(lds + wave * 32 * C::kEpiF32RowBytes);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          f32[(8 * (e >> 2) + 4 * kh + (e & 3)) * (C::kEpiF32RowBytes / 4) + j * 32 + lr] =
+              __fmul_rn(al[e], __fmul_rn(acc[i][j][e], kAccUnscale));
+      __syncthreads();
+#pragma unroll 1
+      for (int idx = lane; idx < 32 * TN * 32; idx += 64) {
+        const int r = idx / (TN * 32), c = idx % (TN * 32);
+        const int64_t row = wrow0 + i * 32 + r, col = wcol0 + c;
+        if (row < m && col < n)
+          out[row * ldo + col] =
+              (uint16_t)finish_bf16(f32[r * (C::kEpiF32RowBytes / 4) + c], bias, col, ep, row * ldo + col);
+      }
+      __syncthreads();
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
 #pragma unroll
@@ -266,16 +290,6 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
             }
           }
         }
-        if (epi) {
-#pragma unroll 1
-          for (int h = 0; h < 8 && col + h < n; ++h) {
-            const uint32_t sh = 16 * (h & 1);
-            const uint32_t z = finish_bf16((word(make_uint4(w[0], w[1], w[2], w[3]), h >> 1) >> sh) & 0xFFFFu, ep,
-                                           row * ldo + col + h);
-            out[row * ldo + col + h] = (uint16_t)z;
-          }
-          continue;
-        }
         uint16_t* o = out + row * ldo + col;
         if (col + 8 <= n && ((uintptr_t)o & 15) == 0) {
           *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -288,21 +302,21 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
   }
 }
 
-template <int WM, int WN, int TM, int TN>
+template <int WM, int WN, int TM, int TN, bool kEpi>
 hipError_t launch_cfg(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
                       const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b, int64_t a_seg_rows,
                       const uint16_t* bias, const Epilogue& ep,
                       uint16_t* out, int64_t b_srows, int64_t ldo, int aligned16, hipStream_t s) {
   using C = Cfg<WM, WN, TM, TN>;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_kernel<WM, WN, TM, TN>), C::kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_kernel<WM, WN, TM, TN, kEpi>), C::kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tiles_m = (int)((m + C::BM - 1) / C::BM);
   const int tiles_n = (int)((n + C::BN - 1) / C::BN);
-  hipLaunchKernelGGL((gemm_kernel<WM, WN, TM, TN>), dim3(tiles_m * tiles_n), dim3(C::kThreads), C::kLds, s, a_codes,
-                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, b_srows, ldo, tiles_m,
+  hipLaunchKernelGGL((gemm_kernel<WM, WN, TM, TN, kEpi>), dim3(tiles_m * tiles_n), dim3(C::kThreads), C::kLds, s, a_codes,
+                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, b_srows, ldo, tiles_m,
                      tiles_n, aligned16);
   return hipGetLastError();
 }
@@ -316,13 +330,11 @@ hipError_t launch_generic(const uint8_t* a_codes, const uint8_t* a_scales, int64
   const int aligned16 = ((k / 2) % 16 == 0) && (((uintptr_t)a_codes | (uintptr_t)b_codes) % 16 == 0);
   // Largest tile that still gives every compute unit a tile.
   const int64_t mid = ((m + 255) / 256) * ((n + 127) / 128);
-  if (mid >= cus)
-    return launch_cfg<2, 2, 4, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
-                                  b_srows, ldo,
-                                  aligned16, s);
-  return launch_cfg<2, 2, 2, 2>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,
-                                b_srows, ldo,
-                                aligned16, s);
+  using Fn = decltype(&launch_cfg<2, 2, 4, 2, false>);
+  static constexpr Fn f[2][2] = {{launch_cfg<2, 2, 2, 2, false>, launch_cfg<2, 2, 2, 2, true>},
+                                 {launch_cfg<2, 2, 4, 2, false>, launch_cfg<2, 2, 4, 2, true>}};
+  return f[mid >= cus ? 1 : 0][ep.active() ? 1 : 0](a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b,
+                                                    a_seg_rows, bias, ep, out, b_srows, ldo, aligned16, s);
 }
 
 }  // namespace

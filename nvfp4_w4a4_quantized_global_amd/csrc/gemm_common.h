@@ -92,38 +92,45 @@ __device__ __forceinline__ uint32_t add_bias_bf16(uint32_t y_bf16, uint16_t bias
   return f32_to_bf16(__fadd_rn(bf16_to_f32(y_bf16), bf16_to_f32(bias_bf16)));
 }
 
-// The epilogue past the bias for element idx: z is the plain linear's bf16 output.  Keeping
-// that rounding makes a fused call equal the linear followed by the activation and the sum,
-// and z the very value the activation's gradient is taken at.
-__device__ __forceinline__ uint32_t finish_bf16(uint32_t z, const Epilogue& ep, int64_t idx) {
-  if (ep.preact != nullptr) ep.preact[idx] = (uint16_t)z;
-  float v = activate(bf16_to_f32(z), ep.act);
+// The epilogue with activation and residual, in fp32 from the product to one rounding:
+// z = y + bias (y = alpha times the accumulator), preact = bf16(z), out = bf16(act(z) +
+// residual).  One element, at idx of the row-major output; returns its bf16 bits.
+__device__ __forceinline__ uint32_t finish_bf16(float y, const uint16_t* bias, int64_t col, const Epilogue& ep,
+                                                int64_t idx) {
+  const float z = bias != nullptr ? __fadd_rn(y, bf16_to_f32(bias[col])) : y;
+  if (ep.preact != nullptr) ep.preact[idx] = (uint16_t)pack_bf16x2(z, 0.0f);
+  float v = activate(z, ep.act);
   if (ep.residual != nullptr) v = __fadd_rn(v, bf16_to_f32(ep.residual[idx]));
   return pack_bf16x2(v, 0.0f);
 }
 
-// The same for eight consecutive elements packed in w (all inside the output, idx a
-// multiple of 8 on 16-byte aligned arrays).
-__device__ __forceinline__ void finish8_bf16(uint32_t (&w)[4], const Epilogue& ep, int64_t idx) {
-  if (ep.preact != nullptr) *reinterpret_cast<uint4*>(ep.preact + idx) = make_uint4(w[0], w[1], w[2], w[3]);
-  uint4 r = make_uint4(0, 0, 0, 0);
-  if (ep.residual != nullptr) r = *reinterpret_cast<const uint4*>(ep.residual + idx);
-  const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+// Eight consecutive elements of a row, z already with its bias, packed to bf16.  Wide
+// accesses: the caller has checked epilogue_wide and that all eight are in the row.
+template <int kAct>
+__device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const Epilogue& ep, int64_t idx) {
+  if (ep.preact != nullptr)
+    *reinterpret_cast<uint4*>(ep.preact + idx) = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
+                                                            pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo = activate(__uint_as_float(w[i] << 16), ep.act);
-    float hi = activate(__uint_as_float(w[i] & 0xFFFF0000u), ep.act);
-    if (ep.residual != nullptr) {
-      lo = __fadd_rn(lo, __uint_as_float(rw[i] << 16));
-      hi = __fadd_rn(hi, __uint_as_float(rw[i] & 0xFFFF0000u));
+  for (int i = 0; i < 8; ++i) v[i] = activate_t<kAct>(z[i]);
+  if (ep.residual != nullptr) {
+    const uint4 r = *reinterpret_cast<const uint4*>(ep.residual + idx);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __fadd_rn(v[2 * i], __uint_as_float(w[i] << 16));
+      v[2 * i + 1] = __fadd_rn(v[2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    w[i] = pack_bf16x2(lo, hi);
   }
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
-// Whether finish8_bf16's wide accesses are aligned for rows of ldo elements.
-__device__ __forceinline__ bool epilogue_wide(const Epilogue& ep, int64_t ldo) {
-  return (ldo & 7) == 0 && (((uintptr_t)ep.residual | (uintptr_t)ep.preact) & 15) == 0;
+// Whether finish8_bf16's wide accesses, and such a store to out, are aligned for rows of
+// ldo elements.
+__device__ __forceinline__ bool epilogue_wide(const Epilogue& ep, const uint16_t* out, int64_t ldo) {
+  return (ldo & 7) == 0 && (((uintptr_t)ep.residual | (uintptr_t)ep.preact | (uintptr_t)out) & 15) == 0;
 }
 
 }  // namespace gemm

@@ -31,6 +31,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gemm_common.h"
 #include "nvfp4_device.h"
 #include "nvfp4_launch.h"
@@ -42,6 +44,8 @@ using namespace gemm;
 
 constexpr int kRows = 256;                       // rows of B (output columns) per tile
 constexpr int kEpiRowBytes = 128 * 2 + 16;
+constexpr int kEpiF32RowBytes = 128 * 4 + 16;
+constexpr int kEpiF32Lds = 4 * 32 * kEpiF32RowBytes;   // four waves' staging of the fp32 epilogue
 
 // Tile geometry for kTM 32-row MFMA tiles per wave along M (2 x 2 waves): A rows per
 // tile 64 * kTM (256, or 128 for few activation rows), B rows 256.  One LDS stage holds
@@ -106,9 +110,10 @@ __device__ __forceinline__ void interleave() {
 // kTM: 32-row MFMA tiles per wave along M (4: 256 x 256 tiles, 2: 128 x 256).  With
 // sub = 2 (split launch of 128-row tiles only), tile indices count tiles twice as tall
 // (tiles_m of that grid), each cut into two 128-row halves: tile tile0 + u / 2, half u % 2.
-// kEpi: the epilogue past the bias (activation, residual; never with kSplit, whose reduce
-// applies it).
-template <bool kSplit, int kTM, bool kEpi>
+// kEpi: kPlain, or the epilogue with this activation and a residual (never with kSplit,
+// whose reduce applies it).
+constexpr int kPlain = -1;
+template <bool kSplit, int kTM, int kEpi>
 __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
@@ -336,6 +341,60 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     return;
   }
 
+  if constexpr (kEpi != kPlain) {
+    // Epilogue in fp32: alpha * acc staged through LDS as fp32, 32 rows per wave at a time
+    // (16-byte writes of 4 consecutive columns; a row stride of 132 words keeps eight rows
+    // in different banks), read back as 8 consecutive columns of a row per lane.  Each wave
+    // uses its own LDS region, as in the plain epilogue below.
+    uint8_t* st = lds + wave * 32 * kEpiF32RowBytes;
+    const int64_t er0 = row0 + wm * (32 * kTM);
+    const int64_t ec = col0 + wn * 128 + 8 * (lane & 15);
+    const bool wide = ec + 8 <= n && epilogue_wide(ep, out, ldo);
+    float bv[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && ec + h < n ? bf16_to_f32(bias[ec + h]) : 0.0f;
+    const float alpha = a_seg_rows > 0 ? 0.0f : alpha_for(gsf_a, gsf_b, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, min(er0 + i * 32 + lr, m - 1)) : alpha;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y[4];
+#pragma unroll
+          for (int s4 = 0; s4 < 4; ++s4) y[s4] = __fmul_rn(al, __fmul_rn(acc[i][j][4 * q + s4], kAccUnscale));
+          *reinterpret_cast<float4*>(st + lr * kEpiF32RowBytes + (32 * j + 8 * q + 4 * kh) * 4) =
+              make_float4(y[0], y[1], y[2], y[3]);
+        }
+      lds_order();
+#pragma unroll 1
+      for (int p = 0; p < 8; ++p) {
+        const int r = 4 * p + (lane >> 4);
+        const int64_t row = er0 + i * 32 + r;
+        const float4* f = reinterpret_cast<const float4*>(st + r * kEpiF32RowBytes + (lane & 15) * 32);
+        const float4 f0 = f[0], f1 = f[1];
+        const float z[8] = {__fadd_rn(f0.x, bv[0]), __fadd_rn(f0.y, bv[1]), __fadd_rn(f0.z, bv[2]),
+                            __fadd_rn(f0.w, bv[3]), __fadd_rn(f1.x, bv[4]), __fadd_rn(f1.y, bv[5]),
+                            __fadd_rn(f1.z, bv[6]), __fadd_rn(f1.w, bv[7])};
+        if (row >= m) continue;
+        const int64_t idx = row * ldo + ec;
+        if (wide) {
+          const uint4 o = finish8_bf16<kEpi>(z, ep, idx);
+          typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+          __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(out + idx));
+        } else {
+          const float y[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            if (ec + h < n) out[idx + h] = (uint16_t)finish_bf16(y[h], bias, ec + h, ep, idx + h);
+        }
+      }
+      lds_order();
+    }
+    return;
+  }
+
   // Epilogue: bf16(alpha * acc) staged through LDS 32 rows per wave at a time (8-byte
   // writes of 4 consecutive columns), then bf16(y + bias), written as 16-byte row
   // segments.  Each wave stages its own rows in its own LDS region, so only the wave's
@@ -349,8 +408,7 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
   // bias once, and stores them as one 16-byte segment when they are all inside the
   // output and the row starts are 16-byte aligned.
   const int64_t col = wcol0 + 8 * (lane & 15);
-  const bool vec_store = col + 8 <= n && (ldo & 7) == 0 && ((uintptr_t)out & 15) == 0 &&
-                         (!kEpi || epilogue_wide(ep, ldo));
+  const bool vec_store = col + 8 <= n && (ldo & 7) == 0 && ((uintptr_t)out & 15) == 0;
   uint32_t bw[4] = {0, 0, 0, 0};
   if (bias != nullptr) {
     if (col + 8 <= n && ((uintptr_t)(bias + col) & 15) == 0) {
@@ -400,7 +458,6 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
       }
       if (row < m) {
         uint16_t* o = out_i + 4 * p * ldo;
-        if (kEpi && vec_store) finish8_bf16(w, ep, (row_i + 4 * p) * ldo + col);
         if (vec_store) {
           typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
           __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(o));
@@ -408,11 +465,7 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
           const uint64_t lo = ((uint64_t)w[1] << 32) | w[0], hi = ((uint64_t)w[3] << 32) | w[2];
           const int cnt = n - col < 8 ? (int)(n - col) : 8;
 #pragma unroll 1
-          for (int h = 0; h < cnt; ++h) {
-            uint32_t z = (uint16_t)((h < 4 ? lo : hi) >> (16 * (h & 3)));
-            if (kEpi) z = finish_bf16(z, ep, (row_i + 4 * p) * ldo + col + h);
-            o[h] = (uint16_t)z;
-          }
+          for (int h = 0; h < cnt; ++h) o[h] = (uint16_t)((h < 4 ? lo : hi) >> (16 * (h & 3)));
         }
       }
     }
@@ -476,26 +529,36 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
   const int64_t col = (int64_t)tn * kRows + (wave & 1) * 128 + j * 32 + 8 * qq;
   if (row >= m || col >= n) return;
   const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, row);
+  if (epi) {
+    float z[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) z[h] = __fmul_rn(alpha, __fmul_rn(acc[h], kAccUnscale));
+    const int64_t idx = row * ldo + col;
+    if (col + 8 <= n && epilogue_wide(ep, out, ldo)) {
+      if (bias != nullptr)
+#pragma unroll
+        for (int h = 0; h < 8; ++h) z[h] = __fadd_rn(z[h], bf16_to_f32(bias[col + h]));
+      uint4 o;
+      switch (ep.act) {
+        case NVFP4_ACT_SILU: o = finish8_bf16<NVFP4_ACT_SILU>(z, ep, idx); break;
+        case NVFP4_ACT_GELU: o = finish8_bf16<NVFP4_ACT_GELU>(z, ep, idx); break;
+        case NVFP4_ACT_GELU_TANH: o = finish8_bf16<NVFP4_ACT_GELU_TANH>(z, ep, idx); break;
+        default: o = finish8_bf16<NVFP4_ACT_NONE>(z, ep, idx);
+      }
+      *reinterpret_cast<uint4*>(out + idx) = o;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (col + h < n) out[idx + h] = (uint16_t)finish_bf16(z[h], bias, col + h, ep, idx + h);
+    }
+    return;
+  }
   uint16_t y[8];
 #pragma unroll
   for (int h = 0; h < 8; ++h) {
     uint32_t v = f32_to_bf16(__fmul_rn(alpha, __fmul_rn(acc[h], kAccUnscale)));
     if (bias != nullptr && col + h < n) v = add_bias_bf16(v, bias[col + h]);
     y[h] = (uint16_t)v;
-  }
-  if (epi) {
-    if (col + 8 <= n && epilogue_wide(ep, ldo)) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = y[2 * i] | ((uint32_t)y[2 * i + 1] << 16);
-      finish8_bf16(w, ep, row * ldo + col);
-#pragma unroll
-      for (int h = 0; h < 8; ++h) y[h] = (uint16_t)(w[h >> 1] >> (16 * (h & 1)));
-    } else {
-#pragma unroll
-      for (int h = 0; h < 8; ++h)
-        if (col + h < n) y[h] = (uint16_t)finish_bf16(y[h], ep, row * ldo + col + h);
-    }
   }
   uint16_t* o = out + row * ldo + col;
   if (col + 8 <= n && ((uintptr_t)o & 15) == 0) {
@@ -566,13 +629,13 @@ hipError_t launch_split_tail(const PipePlan& p, int sub, const uint8_t* a_codes,
                              float* partial, hipStream_t s) {
   constexpr int kLds = Geo<kTM>::kLds;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<true, kTM, false>), kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<true, kTM, kPlain>), kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
   const int64_t units = p.rest * sub;
-  hipLaunchKernelGGL((gemm_pipe_kernel<true, kTM, false>), dim3((uint32_t)(units * p.splits)), dim3(256), kLds, s, a_codes,
+  hipLaunchKernelGGL((gemm_pipe_kernel<true, kTM, kPlain>), dim3((uint32_t)(units * p.splits)), dim3(256), kLds, s, a_codes,
                      a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn,
                      (int)p.full, p.splits, sub, partial);
   hipError_t e = hipGetLastError();
@@ -582,12 +645,12 @@ hipError_t launch_split_tail(const PipePlan& p, int sub, const uint8_t* a_codes,
   return hipGetLastError();
 }
 
-template <int kTM, bool kEpi>
+template <int kTM, int kEpi>
 hipError_t launch_plan(const PipePlan& p, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
                        const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, float* partial,
                        hipStream_t s) {
-  constexpr int kLds = Geo<kTM>::kLds;
+  constexpr int kLds = kEpi == kPlain ? Geo<kTM>::kLds : std::max(Geo<kTM>::kLds, kEpiF32Lds);
   static bool attr_set[kMaxDevices] = {};
   if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&gemm_pipe_kernel<false, kTM, kEpi>), kLds,
                                           attr_set);
@@ -638,11 +701,15 @@ hipError_t launch_gemm_pipe(const uint8_t* a_codes, const uint8_t* a_scales, int
   const size_t need = plan_bytes(p);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) p.splits = 1;
   float* partial = static_cast<float*>(workspace);
-  using Fn = decltype(&launch_plan<4, false>);
-  static constexpr Fn f[2][2] = {{launch_plan<4, false>, launch_plan<4, true>},
-                                 {launch_plan<2, false>, launch_plan<2, true>}};
-  return f[p.tm == 2 ? 1 : 0][ep.active() ? 1 : 0](p, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b,
-                                                   a_seg_rows, bias, ep, out, partial, s);
+  using Fn = decltype(&launch_plan<4, kPlain>);
+  static constexpr Fn f[2][5] = {
+      {launch_plan<4, kPlain>, launch_plan<4, NVFP4_ACT_NONE>, launch_plan<4, NVFP4_ACT_SILU>,
+       launch_plan<4, NVFP4_ACT_GELU>, launch_plan<4, NVFP4_ACT_GELU_TANH>},
+      {launch_plan<2, kPlain>, launch_plan<2, NVFP4_ACT_NONE>, launch_plan<2, NVFP4_ACT_SILU>,
+       launch_plan<2, NVFP4_ACT_GELU>, launch_plan<2, NVFP4_ACT_GELU_TANH>}};
+  static_assert(NVFP4_ACT_NONE == 0 && NVFP4_ACT_SILU == 1 && NVFP4_ACT_GELU == 2 && NVFP4_ACT_GELU_TANH == 3, "");
+  return f[p.tm == 2 ? 1 : 0][ep.active() ? 1 + ep.act : 0](p, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a,
+                                                            gsf_b, a_seg_rows, bias, ep, out, partial, s);
 }
 
 }  // namespace nvfp4

@@ -188,9 +188,10 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
           partial[((int64_t)split * m + row) * n + col] = acc[i][j][e];
         } else {
           const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
-          uint32_t y = f32_to_bf16(__fmul_rn(al, __fmul_rn(acc[i][j][e], kAccUnscale)));
-          if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
-          if (epi) y = finish_bf16(y, ep, row * n + col);
+          const float v = __fmul_rn(al, __fmul_rn(acc[i][j][e], kAccUnscale));
+          uint32_t y = f32_to_bf16(v);
+          if (epi) y = finish_bf16(v, bias, col, ep, row * n + col);
+          else if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
           out[row * n + col] = (uint16_t)y;
         }
       }
@@ -209,9 +210,10 @@ __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restric
   float acc = 0.0f;
   for (int sp = 0; sp < splits; ++sp) acc += partial[sp * m * n + idx];
   const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, idx / n);
-  uint32_t y = f32_to_bf16(__fmul_rn(alpha, __fmul_rn(acc, kAccUnscale)));
-  if (bias != nullptr) y = add_bias_bf16(y, bias[idx % n]);
-  if (epi) y = finish_bf16(y, ep, idx);
+  const float v = __fmul_rn(alpha, __fmul_rn(acc, kAccUnscale));
+  uint32_t y = f32_to_bf16(v);
+  if (epi) y = finish_bf16(v, bias, idx % n, ep, idx);
+  else if (bias != nullptr) y = add_bias_bf16(y, bias[idx % n]);
   out[idx] = (uint16_t)y;
 }
 
@@ -572,9 +574,10 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
       partial[((int64_t)split * m + row) * n + col] = acc[e];
     } else {
       const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
-      uint32_t y = f32_to_bf16(__fmul_rn(al, __fmul_rn(acc[e], kAccUnscale)));
-      if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
-      if (epi) y = finish_bf16(y, ep, row * n + col);
+      const float v = __fmul_rn(al, __fmul_rn(acc[e], kAccUnscale));
+      uint32_t y = f32_to_bf16(v);
+      if (epi) y = finish_bf16(v, bias, col, ep, row * n + col);
+      else if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
       out[row * n + col] = (uint16_t)y;
     }
   }

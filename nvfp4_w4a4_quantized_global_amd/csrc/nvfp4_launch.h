@@ -15,10 +15,10 @@ constexpr int kMaxDevices = 64;
 // (`done` is the caller's per-kernel record); a no-op after the first call there.
 hipError_t set_dynamic_lds_once(const void* kernel, int bytes, bool (&done)[kMaxDevices]);
 
-// What a linear's output goes through after its bias: z = the bf16 output of the plain
-// linear, stored to preact [m][n] when not NULL, then out = bf16(residual + act(z)) with
-// act (NVFP4_ACT_*) and the sum in fp32.  residual [m][n] bf16, NULL, or out itself: every
-// element is read by the thread that writes it, just before.
+// A linear's epilogue with activation and residual: from z = alpha * acc + bias in fp32,
+// preact [m][n] = bf16(z) when not NULL and out = bf16(act(z) + residual), act one of
+// NVFP4_ACT_*: nothing is rounded in between.  residual [m][n] bf16, NULL, or out itself:
+// every element is read by the thread that writes it, just before.
 struct Epilogue {
   const uint16_t* residual = nullptr;
   uint16_t* preact = nullptr;

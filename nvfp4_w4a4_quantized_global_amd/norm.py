@@ -5,30 +5,25 @@ from __future__ import annotations
 import torch
 
 from ._lib import check, lib
-from .checkpoint import Checkpoint, _empty_checkpoint, _rows2d
-from .nvfp4 import DTYPE_CODES, _on_device, _ptr, _require_cuda, _require_device, _scalar_f32, _stream, scale_bytes
+from .checkpoint import Checkpoint, _empty_checkpoint, _rows
+from .nvfp4 import DTYPE_CODES, _on_device, _ptr, _require_device, _scalar_f32, _stream, scale_bytes
 
 NORM_MAX_K = 16384
 
 
-def _stream_rows(name: str, t: torch.Tensor) -> torch.Tensor:
+def _stream_rows(name: str, t: torch.Tensor) -> tuple[torch.Tensor, int, int]:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in DTYPE_CODES:
         raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    return _rows2d(name, t, t.dtype)
+    return _rows(name, t, t.dtype)
 
 
 def _weight(weight: torch.Tensor, k: int, device: torch.device) -> torch.Tensor:
-    if not isinstance(weight, torch.Tensor):
-        raise TypeError("weight must be a torch.Tensor")
-    if weight.dtype not in DTYPE_CODES or weight.shape != (k,):
+    w, rows, n = _stream_rows("weight", weight)
+    if n != k or rows != 1 or w.dim() != 1:
         raise ValueError(f"weight must be bf16 or fp32 [{k}], got {weight.dtype} {list(weight.shape)}")
-    _require_device(device, weight=weight)
-    w = weight.detach().contiguous()
-    if w.data_ptr() % 16:
-        w = w.clone()
-    _require_cuda("weight", w)
+    _require_device(device, weight=w)
     return w
 
 
@@ -36,19 +31,18 @@ class _Inputs:
     """The checked inputs of one norm call, in the order of the C calls' first arguments."""
 
     def __init__(self, x, weight, eps, residual):
-        self.x = _stream_rows("x", x)
-        self.rows, self.k = self.x.shape
+        self.x, self.rows, self.k = _stream_rows("x", x)
         self.w = _weight(weight, self.k, x.device)
         self.res = self.out = None
         if residual is not None:
-            self.res = _stream_rows("residual", residual)
+            self.res, _, _ = _stream_rows("residual", residual)
             _require_device(x.device, residual=residual)
             if residual.shape != x.shape:
                 raise ValueError(f"x and residual must have the same shape, got {list(x.shape)} and "
                                  f"{list(residual.shape)}")
             if x.dtype == torch.float32 and residual.dtype != torch.float32:
                 raise ValueError("an fp32 x needs an fp32 residual")
-            self.out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+            self.out = torch.empty_like(self.res)
         self.args = (_ptr(self.x), DTYPE_CODES[x.dtype], _ptr(self.res),
                      DTYPE_CODES[x.dtype if self.res is None else self.res.dtype], _ptr(self.w),
                      DTYPE_CODES[self.w.dtype], self.rows, self.k, float(eps))
@@ -90,16 +84,15 @@ def quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     a = _Inputs(x, weight, eps, residual)
     dev = x.device
     codes = torch.empty((a.rows, a.k // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((max(scale_bytes(a.rows, a.k), 1),), dtype=torch.uint8, device=dev)
+    scales = torch.empty((scale_bytes(a.rows, a.k),), dtype=torch.uint8, device=dev)
     gsf = torch.empty((), dtype=torch.float32, device=dev)
     g = None if global_sf_x is None else _scalar_f32(global_sf_x, dev)
     _require_device(dev, global_sf_x=g)
-    need = int(lib().nvfp4_quantize_rmsnorm_workspace_bytes(a.rows)) if g is None else 0
+    need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(a.rows) if g is None else 0
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     check(lib().nvfp4_quantize_rmsnorm(*a.args, _ptr(g), _ptr(a.out), _ptr(codes), _ptr(scales), _ptr(gsf), _ptr(ws),
                                        need, _stream(dev)))
-    out = (codes, scales[: scale_bytes(a.rows, a.k)], gsf)
-    return out if residual is None else (*out, a.out)
+    return (codes, scales, gsf) if residual is None else (codes, scales, gsf, a.out)
 
 
 @_on_device
@@ -108,22 +101,21 @@ def rmsnorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor
     """Gradient of the norm at r (x, or the sum rmsnorm returned): (grad_r in r's dtype, the
     gradient of x and of the residual alike; grad_weight fp32 [K]).  ``grad_residual``: the
     gradient that reaches r along the residual stream, of r's dtype, added to grad_r."""
-    gy = _rows2d("grad_y", grad_y)
-    r2 = _stream_rows("r", r)
-    rows, k = r2.shape
+    gy, *gm = _rows("grad_y", grad_y)
+    r2, rows, k = _stream_rows("r", r)
     _require_device(gy.device, r=r, grad_residual=grad_residual)
-    if gy.shape != r2.shape:
+    if gm != [rows, k]:
         raise ValueError(f"grad_y and r must have the same shape, got {list(grad_y.shape)} and {list(r.shape)}")
     w = _weight(weight, k, gy.device)
     gr = None
     if grad_residual is not None:
-        gr = _rows2d("grad_residual", grad_residual, r.dtype)
-        if gr.shape != r2.shape:
+        gr, *rm = _rows("grad_residual", grad_residual, r.dtype)
+        if rm != [rows, k]:
             raise ValueError(f"grad_residual and r must have the same shape, got {list(grad_residual.shape)} and "
                              f"{list(r.shape)}")
     grad_r = torch.empty(r.shape, dtype=r.dtype, device=r.device)
     grad_w = torch.empty((k,), dtype=torch.float32, device=r.device)
-    need = int(lib().nvfp4_rmsnorm_backward_workspace_bytes(rows, k))
+    need = lib().nvfp4_rmsnorm_backward_workspace_bytes(rows, k)
     ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=r.device)
     check(lib().nvfp4_rmsnorm_backward(_ptr(gy), _ptr(r2), DTYPE_CODES[r.dtype], _ptr(w), DTYPE_CODES[w.dtype], _ptr(gr),
                                        rows, k, float(eps), _ptr(grad_r), _ptr(grad_w), _ptr(ws), ws.numel(),

@@ -10,7 +10,6 @@ the "minimax_h3_nvfp4_decoder" page: ``rotate_activation``,
 from __future__ import annotations
 
 import contextlib
-import ctypes
 import functools
 
 import torch
@@ -26,12 +25,14 @@ ACTIVATIONS = {None: _lib.NVFP4_ACT_NONE, "silu": _lib.NVFP4_ACT_SILU, "gelu": _
 DTYPE_CODES = {torch.bfloat16: _lib.NVFP4_DTYPE_BF16, torch.float32: _lib.NVFP4_DTYPE_F32}
 
 
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p | None:
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# Addresses and streams go to ctypes as plain integers (the argument types are c_void_p):
+# wrapping them, and building a torch Stream object for its handle, costs microseconds a call.
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _require_cuda(name: str, t: torch.Tensor, dtype: torch.dtype | None = None, dim: int | None = None) -> None:
@@ -83,7 +84,6 @@ def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, ou
             raise ValueError(f"residual must be bf16 with {m} rows of {n}, got "
                              f"{getattr(residual, 'dtype', None)} {list(getattr(residual, 'shape', []))}")
         _require_device(device, residual=residual)
-        residual = residual.reshape(m, n)
         if not residual.is_contiguous():
             residual = residual.contiguous()
     for name, t in (("preact", preact), ("out", out)):
@@ -241,10 +241,10 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     ``global_sf_x=None`` computes the activation scale dynamically from the
     call's 2-D input.  Leading dimensions of x are flattened and restored.
 
-    With ``activation`` ("silu", "gelu" or "gelu_tanh") or ``residual`` (bf16, the output's
-    shape) the epilogue goes on: from the plain linear's bf16 output z it forms
-    ``bf16(residual + act(z))``, the activation and the sum in fp32.  ``residual`` may be
-    ``out`` itself.  ``preact`` (contiguous bf16 [rows, out_features]) receives z.
+    With ``activation`` ("silu", "gelu" or "gelu_tanh"), ``residual`` (bf16, the output's
+    shape) or ``preact`` the epilogue is ``bf16(act(z) + residual)`` from z = product + bias,
+    in fp32 with that one rounding.  ``residual`` may be ``out`` itself; ``preact``
+    (contiguous bf16 [rows, out_features]) receives bf16(z).
     """
     if x.dtype != torch.bfloat16:
         raise ValueError(f"x must be bf16, got {x.dtype}")
