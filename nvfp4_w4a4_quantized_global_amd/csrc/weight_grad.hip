@@ -17,10 +17,12 @@
 //   * gy goes global -> LDS directly, 16 bytes a lane;
 //   * codes go through registers: loaded a step ahead, expanded by the hardware's scaled
 //     conversion (one instruction per two values), written to LDS as bf16;
-//   * a 512-byte row holds 32 chunks of 16 bytes, chunk c at position c ^ 4 (row % 4): the
-//     four rows that one transposed read gathers then lie in different banks;
-//   * rows and columns past the end read a zero chunk, so they add nothing even where gy
-//     holds infinities.
+//   * both come by buffer loads, whose range check supplies zeros for rows and columns past
+//     the end: they add nothing even where gy holds infinities, and the loop carries no
+//     per-lane address arithmetic;
+//   * a 512-byte row holds 32 chunks of 16 bytes, chunk c at position c ^ 4 (row % 4) (the
+//     four rows that one transposed read gathers lie in different banks), for x with bit 0
+//     also flipped by bit 3 of c (so that the 32-byte writes of neighbouring lanes do).
 // Few tiles (a narrow projection) leave compute units idle, so the rows are split across
 // workgroups into fp32 partials that weight_grad_reduce adds in split order.
 #include <hip/hip_runtime.h>
@@ -48,19 +50,45 @@ constexpr int kPanel = kStep * kRowBytes;   // one operand of one stage, 32 KB
 constexpr int kLds = 4 * kPanel;
 constexpr int kBand = 4;                    // tile rows per band of the tile order
 
-__device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {};
-
 // Position of chunk c in row r.
 __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r & 3) << 2); }
+__device__ __forceinline__ int swz_x(int r, int c) { return swz(r, c) ^ ((c >> 3) & 1); }
+
+// A buffer of `bytes` bytes from p (wave-uniform): loads past them return zero.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4_t buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer here
+constexpr int64_t kBufferWidth = 1 << 24;    // columns up to which a step's rows fit 31-bit offsets
 
 // One 16-byte global -> LDS copy per lane; the address is a wave-uniform LDS base plus
 // 16 bytes a lane.  Inline asm so that the compiler does not hold LDS reads back for it:
 // step_barrier waits for it.
-__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
-  asm volatile("global_load_lds_dwordx4 %1, off" :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(src) : "memory");
+__device__ __forceinline__ void copy16_to_lds(u32x4_t rsrc, uint32_t offset, uint8_t* dst) {
+  asm volatile("buffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(offset), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
 __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Scheduling of one sub-step: kN times an MFMA, an access of kind kMem and some vector work.
+template <int kMem, int kN>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int g = 0; g < kN; ++g) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kMem, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Four rows of one column (see the lane layout at the reads below).
@@ -69,8 +97,7 @@ __device__ __forceinline__ short4_t read_tr(const uint8_t* p) {
 }
 
 // 16 codes -> 32 bytes of bf16.
-__device__ __forceinline__ void expand16(const uint4& c, float scale, uint4 (&o)[2]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+__device__ __forceinline__ void expand16(const u32x4_t& w, float scale, uint4 (&o)[2]) {
   uint32_t r[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -81,8 +108,8 @@ __device__ __forceinline__ void expand16(const uint4& c, float scale, uint4 (&o)
   o[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// kAligned: rows of gy start on 16-byte boundaries (N a multiple of 8) and take the direct
-// copies; otherwise they are gathered value by value.
+// kAligned: rows of gy start on 16-byte boundaries (N a multiple of 8) and a step's rows fit
+// 31-bit offsets; otherwise gy is gathered value by value and addresses are 64-bit.
 template <bool kAligned, bool kOutBf16>
 __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __restrict__ gy, int64_t m, int64_t n,
                                                              const uint8_t* __restrict__ codes,
@@ -115,24 +142,31 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   auto panel_a = [&](int64_t s) { return lds + (int)(s & 1) * 2 * kPanel; };
   auto panel_b = [&](int64_t s) { return lds + (int)(s & 1) * 2 * kPanel + kPanel; };
 
+  // bytes of the rows of step s in an array of `width` bytes a row
+  auto step_bytes = [&](int64_t s, int64_t width) {
+    const int64_t rows = s < s_end ? min(m - s * kStep, (int64_t)kStep) : 0;
+    return (uint32_t)(rows * width);
+  };
   // gy: instruction i of wave w fills rows 16 w + 2 i and + 1 of the panel
+  uint32_t goff[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 16 * wave + 2 * i + (lane >> 5);
+    const int64_t col = n0 + 8 * swz(r, lane & 31);
+    goff[i] = col < n ? (uint32_t)((r * n + col) * 2) : kOutside;
+  }
   auto stage_gy = [&](int64_t s) {
     uint8_t* dst = panel_a(s);
     if constexpr (kAligned) {
+      const u32x4_t rs = buffer_of(gy + s * kStep * n, step_bytes(s, 2 * n));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * wave + 2 * i + (lane >> 5);
-        const int64_t row = s * kStep + r;
-        const int64_t col = n0 + 8 * swz(r, lane & 31);
-        const uint8_t* src = row < m && col < n ? reinterpret_cast<const uint8_t*>(gy + row * n + col) : kZeros;
-        copy16_to_lds(src, dst + (16 * wave + 2 * i) * kRowBytes);
-      }
+      for (int i = 0; i < 8; ++i) copy16_to_lds(rs, goff[i], dst + (16 * wave + 2 * i) * kRowBytes);
     } else {
       for (int i = t; i < kStep * 32; i += 256) {
         const int r = i >> 5, c = i & 31;
         const int64_t row = s * kStep + r;
         uint32_t w[4] = {0, 0, 0, 0};
-        if (row < m) {
+        if (s < s_end && row < m) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int64_t col = n0 + 8 * c + e;
@@ -145,16 +179,32 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   };
   // codes: thread t takes 16-value chunk t % 16 of rows t / 16 + 16 i
   const int64_t xcol = k0 + 16 * (t & 15);
-  const bool xcol_in = xcol < k;
-  uint4 xc[4];
+  uint32_t xoff[4], soff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (t >> 4) + 16 * i;
+    xoff[i] = xcol < k ? (uint32_t)(r * k + xcol) : kOutside;
+    soff[i] = xcol < k ? (uint32_t)(r * kb + (xcol >> 5)) : kOutside;
+  }
+  u32x4_t xc[4];
   uint32_t xs[4];
   auto load_x = [&](int64_t s) {
+    if constexpr (kAligned) {
+      const auto rc = rsrc_of(codes + s * kStep * k, step_bytes(s, k));
+      const auto rs = rsrc_of(scales + s * kStep * kb, step_bytes(s, kb));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = s * kStep + (t >> 4) + 16 * i;
-      const bool in = s < s_end && row < m && xcol_in;
-      xc[i] = in ? *reinterpret_cast<const uint4*>(codes + row * k + xcol) : make_uint4(0, 0, 0, 0);
-      xs[i] = in ? scales[row * kb + (xcol >> 5)] : 127u;
+      for (int i = 0; i < 4; ++i) {
+        xc[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)xoff[i], 0, 0);
+        xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)soff[i], 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = s * kStep + (t >> 4) + 16 * i;
+        const bool in = s < s_end && row < m && xcol < k;
+        xc[i] = in ? *reinterpret_cast<const u32x4_t*>(codes + row * k + xcol) : u32x4_t{0, 0, 0, 0};
+        xs[i] = in ? scales[row * kb + (xcol >> 5)] : 0u;
+      }
     }
   };
   auto store_x = [&](int64_t s) {
@@ -164,9 +214,9 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
       const int r = (t >> 4) + 16 * i;
       uint4 o[2];
       expand16(xc[i], pow2f((int)xs[i] - 127), o);
-      uint4* d = reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, 2 * (t & 15)) * 16);
-      d[0] = o[0];
-      d[1] = o[1];
+      const int c = 2 * (t & 15);
+      *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c) * 16) = o[0];
+      *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c + 1) * 16) = o[1];
     }
   };
 
@@ -177,8 +227,9 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   const int q = (lane & 15) >> 2;
   const int lrow = 8 * (lane >> 5) + q;
   const int lbyte = lrow * kRowBytes + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-  auto fragment = [&](const uint8_t* panel, int half, int i, int sub) {
-    const uint8_t* p = panel + lbyte + half * 256 + ((i ^ q) << 6) + sub * 16 * kRowBytes;
+  // flip: chunk c = 16 half + 4 i + ... of x sits one off where bit 3 of c, bit 1 of i, is set
+  auto fragment = [&](const uint8_t* panel, int half, int i, int sub, int flip) {
+    const uint8_t* p = panel + (lbyte ^ (flip << 4)) + half * 256 + ((i ^ q) << 6) + sub * 16 * kRowBytes;
     const short4_t lo = read_tr(p), hi = read_tr(p + 4 * kRowBytes);
     return __builtin_bit_cast(bf16x8_t, (short8_t){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
   };
@@ -191,51 +242,94 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  if (s_begin < s_end) {
-    stage_gy(s_begin);
-    load_x(s_begin);
-    store_x(s_begin);
-    load_x(s_begin + 1);
-  }
-  step_barrier();
-  for (int64_t s = s_begin; s < s_end; ++s) {
-    if (s + 1 < s_end) {
-      stage_gy(s + 1);
-      store_x(s + 1);
-      load_x(s + 2);
-    }
-    const uint8_t *pa = panel_a(s), *pb = panel_b(s);
+  auto load_fragments = [&](int64_t s, int sub, bf16x8_t (&fa)[4], bf16x8_t (&fb)[4]) {
 #pragma unroll
-    for (int sub = 0; sub < kStep / 16; ++sub) {
-      bf16x8_t fa[4], fb[4];
+    for (int i = 0; i < 4; ++i) fa[i] = fragment(panel_a(s), wn, i, sub, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i] = fragment(pa, wn, i, sub);
+    for (int j = 0; j < 4; ++j) fb[j] = fragment(panel_b(s), wk, j, sub, j >> 1);
+  };
+  auto multiply = [&](const bf16x8_t (&fa)[4], const bf16x8_t (&fb)[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = fragment(pb, wk, j, sub);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-    step_barrier();
-  }
+      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+  };
 
-  // Entry e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32 of the block.
+  // Four sub-steps of 16 rows per step; each reads the fragments of the next while its own
+  // MFMAs run.  The barrier stands before the last: by then this step's panels are read
+  // (their last fragments are in registers) and the next step's are complete, so the loads
+  // of the step after that start into the freed panels.
+  bf16x8_t fa[2][4], fb[2][4];
+  stage_gy(s_begin);
+  load_x(s_begin);
+  store_x(s_begin);
+  stage_gy(s_begin + 1);
+  load_x(s_begin + 1);
+  step_barrier();
+  load_fragments(s_begin, 0, fa[0], fb[0]);
+#pragma clang loop unroll(disable)
+  for (int64_t s = s_begin; s < s_end; ++s) {
+    load_fragments(s, 1, fa[1], fb[1]);
+    multiply(fa[0], fb[0]);
+    interleave<0x100, 16>();
+    load_fragments(s, 2, fa[0], fb[0]);
+    store_x(s + 1);
+    multiply(fa[1], fb[1]);
+    interleave<0x100, 16>();
+    load_fragments(s, 3, fa[1], fb[1]);
+    multiply(fa[0], fb[0]);
+    interleave<0x100, 16>();
+    step_barrier();
+    stage_gy(s + 2);
+    load_x(s + 2);
+    load_fragments(s + 1, 0, fa[0], fb[0]);
+    multiply(fa[1], fb[1]);
+    interleave<0x100, 16>();
+  }
+  step_barrier();   // no copy still landing in LDS
+
+  // The product is computed transposed (x as the first operand): entry e of lane l is
+  // column 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32, so a lane holds runs of four
+  // columns.  32 rows at a time pass through the wave's own LDS region (a row stride of 132
+  // words keeps eight rows in different banks) and leave as whole 512-byte rows.
+  constexpr int kStageRow = 132;
+  float* st = reinterpret_cast<float*>(lds) + wave * 32 * kStageRow;
+  static_assert(4 * 32 * kStageRow * 4 <= kLds, "staging fits");
+  const int64_t orow0 = n0 + wn * 128, ocol0 = k0 + wk * 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t col = k0 + wk * 128 + 32 * j + (lane & 31);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t row = n0 + wn * 128 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (row < n && col < k) {
-          if (splits > 1) partial[((int64_t)split * n + row) * k + col] = acc[i][j][e];
-          else if (kOutBf16) static_cast<uint16_t*>(out)[row * k + col] = (uint16_t)gemm::pack_bf16x2(acc[i][j][e], 0.0f);
-          else static_cast<float*>(out)[row * k + col] = acc[i][j][e];
-        }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4*>(st + (lane & 31) * kStageRow + 32 * j + 8 * e + 4 * (lane >> 5)) =
+            make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (kOutBf16 && splits == 1) {
+      const int64_t col = ocol0 + 8 * (lane & 15);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int r = 4 * p + (lane >> 4);
+        const float4* f = reinterpret_cast<const float4*>(st + r * kStageRow + 8 * (lane & 15));
+        const float4 a = f[0], b = f[1];
+        const int64_t row = orow0 + 32 * i + r;
+        if (row < n && col < k)
+          __builtin_nontemporal_store(u32x4_t{gemm::pack_bf16x2(a.x, a.y), gemm::pack_bf16x2(a.z, a.w),
+                                              gemm::pack_bf16x2(b.x, b.y), gemm::pack_bf16x2(b.z, b.w)},
+                                      reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + row * k + col));
+      }
+    } else {
+      float* dst = splits > 1 ? partial + (int64_t)split * n * k : static_cast<float*>(out);
+      const int64_t col = ocol0 + 4 * (lane & 31);
+#pragma unroll
+      for (int p = 0; p < 16; ++p) {
+        const int r = 2 * p + (lane >> 5);
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(st + r * kStageRow + 4 * (lane & 31));
+        const int64_t row = orow0 + 32 * i + r;
+        if (row < n && col < k) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst + row * k + col));
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
@@ -304,7 +398,7 @@ hipError_t launch_weight_grad(const uint16_t* gy, int64_t m, int64_t n, const ui
   using Fn = decltype(&launch_t<false, false>);
   static constexpr Fn f[2][2] = {{launch_t<false, false>, launch_t<false, true>},
                                  {launch_t<true, false>, launch_t<true, true>}};
-  return f[n % 8 == 0 ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, splits, partial, s);
+  return f[n % 8 == 0 && n < kBufferWidth && k < kBufferWidth ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, splits, partial, s);
 }
 
 }  // namespace nvfp4
