@@ -11,16 +11,17 @@
 // LDS holds the tiles as they are in memory, [64 rows][256 columns] of bf16, and
 // ds_read_b64_tr_b16 hands each lane four rows of its column.
 //
-// One 256-thread workgroup per 256 x 256 tile of grad_w, one wave per SIMD, each wave
-// 128 x 128 (4 x 4 tiles of v_mfma_f32_32x32x16_bf16), rows in steps of 64 through two
-// LDS stages:
+// A 256-thread workgroup owns a square tile of grad_w, each of its four waves a quarter in
+// kT x kT tiles of v_mfma_f32_32x32x16_bf16: kT = 4 gives 256 x 256 (one wave per SIMD),
+// kT = 2 gives 128 x 128 (two workgroups per compute unit) for products with too few large
+// tiles.  Rows advance in steps of 64 through two LDS stages:
 //   * gy goes global -> LDS directly, 16 bytes a lane;
 //   * codes go through registers: loaded a step ahead, expanded by the hardware's scaled
 //     conversion (one instruction per two values), written to LDS as bf16;
 //   * both come by buffer loads, whose range check supplies zeros for rows and columns past
 //     the end: they add nothing even where gy holds infinities, and the loop carries no
 //     per-lane address arithmetic;
-//   * a 512-byte row holds 32 chunks of 16 bytes, chunk c at position c ^ 4 (row % 4) (the
+//   * a row of a panel is chunks of 16 bytes, chunk c at position c ^ 4 (row % 4) (the
 //     four rows that one transposed read gathers lie in different banks), for x with bit 0
 //     also flipped by bit 3 of c (so that the 32-byte writes of neighbouring lanes do).
 // Few tiles (a narrow projection) leave compute units idle, so the rows are split across
@@ -43,11 +44,21 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef short short8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 256;                  // columns of gy, and of x, per workgroup
 constexpr int kStep = 64;                   // rows per LDS stage
-constexpr int kRowBytes = kTile * 2;
-constexpr int kPanel = kStep * kRowBytes;   // one operand of one stage, 32 KB
-constexpr int kLds = 4 * kPanel;
+template <int kT>
+struct Geo {
+  static constexpr int kTile = 64 * kT;                // columns of gy, and of x, per workgroup
+  static constexpr int kRowBytes = kTile * 2;
+  static constexpr int kPanel = kStep * kRowBytes;     // one operand of one stage
+  static constexpr int kLds = 4 * kPanel;              // 128 KB or 64 KB
+  static constexpr int kRowChunks = kTile / 8;         // 16-byte chunks of a panel row
+  static constexpr int kCopyRows = 64 / kRowChunks;    // rows one copy instruction of a wave fills
+  static constexpr int kXChunks = kTile / 16;          // 16-code chunks of a row
+  static constexpr int kXRows = 256 / kXChunks;        // rows of codes the workgroup loads at a time
+  static constexpr int kOutRow = 32 * kT + 4;          // words per staged output row
+  static_assert(kStep / kXRows == kT && kStep / (4 * kCopyRows) == 2 * kT, "passes");
+  static_assert(4 * 32 * kOutRow * 4 <= kLds, "output staging fits");
+};
 constexpr int kBand = 4;                    // tile rows per band of the tile order
 
 // Position of chunk c in row r.
@@ -79,13 +90,13 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Scheduling of one sub-step: kN times an MFMA, an access of kind kMem and some vector work.
-template <int kMem, int kN>
+// Scheduling of one sub-step: kN times an MFMA, kReads LDS reads and some vector work.
+template <int kN, int kReads>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
   for (int g = 0; g < kN; ++g) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kMem, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
     __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -110,13 +121,15 @@ __device__ __forceinline__ void expand16(const u32x4_t& w, float scale, uint4 (&
 
 // kAligned: rows of gy start on 16-byte boundaries (N a multiple of 8) and a step's rows fit
 // 31-bit offsets; otherwise gy is gathered value by value and addresses are 64-bit.
-template <bool kAligned, bool kOutBf16>
-__global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __restrict__ gy, int64_t m, int64_t n,
+template <int kT, bool kAligned, bool kOutBf16>
+__global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(const uint16_t* __restrict__ gy, int64_t m, int64_t n,
                                                              const uint8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, int64_t k,
                                                              void* __restrict__ out, int tiles_n, int tiles_k,
                                                              int splits, float* __restrict__ partial) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  using G = Geo<kT>;
+  constexpr int kTile = G::kTile, kRowBytes = G::kRowBytes, kPanel = G::kPanel;
   // Workgroups are dealt round-robin to the 8 XCDs: each XCD gets a contiguous run of
   // tiles, ordered in bands of kBand tile rows, so the tiles resident on one XCD share
   // operand columns in its L2.  With splits, the splits of a tile follow each other.
@@ -147,12 +160,13 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
     const int64_t rows = s < s_end ? min(m - s * kStep, (int64_t)kStep) : 0;
     return (uint32_t)(rows * width);
   };
-  // gy: instruction i of wave w fills rows 16 w + 2 i and + 1 of the panel
-  uint32_t goff[8];
+  // gy: instruction i of wave w fills rows (2 kT w + i) kCopyRows .. of the panel
+  const int crow = lane / G::kRowChunks, cchunk = lane % G::kRowChunks;
+  uint32_t goff[2 * kT];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 16 * wave + 2 * i + (lane >> 5);
-    const int64_t col = n0 + 8 * swz(r, lane & 31);
+  for (int i = 0; i < 2 * kT; ++i) {
+    const int r = (2 * kT * wave + i) * G::kCopyRows + crow;
+    const int64_t col = n0 + 8 * swz(r, cchunk);
     goff[i] = col < n ? (uint32_t)((r * n + col) * 2) : kOutside;
   }
   auto stage_gy = [&](int64_t s) {
@@ -160,10 +174,10 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
     if constexpr (kAligned) {
       const u32x4_t rs = buffer_of(gy + s * kStep * n, step_bytes(s, 2 * n));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) copy16_to_lds(rs, goff[i], dst + (16 * wave + 2 * i) * kRowBytes);
+      for (int i = 0; i < 2 * kT; ++i) copy16_to_lds(rs, goff[i], dst + (2 * kT * wave + i) * 1024);
     } else {
-      for (int i = t; i < kStep * 32; i += 256) {
-        const int r = i >> 5, c = i & 31;
+      for (int i = t; i < kStep * G::kRowChunks; i += 256) {
+        const int r = i / G::kRowChunks, c = i % G::kRowChunks;
         const int64_t row = s * kStep + r;
         uint32_t w[4] = {0, 0, 0, 0};
         if (s < s_end && row < m) {
@@ -177,30 +191,31 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
       }
     }
   };
-  // codes: thread t takes 16-value chunk t % 16 of rows t / 16 + 16 i
-  const int64_t xcol = k0 + 16 * (t & 15);
-  uint32_t xoff[4], soff[4];
+  // codes: thread t takes one 16-value chunk of rows xrow + kXRows i
+  const int xrow = t / G::kXChunks, xchunk = t % G::kXChunks;
+  const int64_t xcol = k0 + 16 * xchunk;
+  uint32_t xoff[kT], soff[kT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 4) + 16 * i;
+  for (int i = 0; i < kT; ++i) {
+    const int r = xrow + G::kXRows * i;
     xoff[i] = xcol < k ? (uint32_t)(r * k + xcol) : kOutside;
     soff[i] = xcol < k ? (uint32_t)(r * kb + (xcol >> 5)) : kOutside;
   }
-  u32x4_t xc[4];
-  uint32_t xs[4];
+  u32x4_t xc[kT];
+  uint32_t xs[kT];
   auto load_x = [&](int64_t s) {
     if constexpr (kAligned) {
       const auto rc = rsrc_of(codes + s * kStep * k, step_bytes(s, k));
       const auto rs = rsrc_of(scales + s * kStep * kb, step_bytes(s, kb));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kT; ++i) {
         xc[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)xoff[i], 0, 0);
         xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)soff[i], 0, 0);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = s * kStep + (t >> 4) + 16 * i;
+      for (int i = 0; i < kT; ++i) {
+        const int64_t row = s * kStep + xrow + G::kXRows * i;
         const bool in = s < s_end && row < m && xcol < k;
         xc[i] = in ? *reinterpret_cast<const u32x4_t*>(codes + row * k + xcol) : u32x4_t{0, 0, 0, 0};
         xs[i] = in ? scales[row * kb + (xcol >> 5)] : 0u;
@@ -210,11 +225,11 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   auto store_x = [&](int64_t s) {
     uint8_t* dst = panel_b(s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (t >> 4) + 16 * i;
+    for (int i = 0; i < kT; ++i) {
+      const int r = xrow + G::kXRows * i;
       uint4 o[2];
       expand16(xc[i], pow2f((int)xs[i] - 127), o);
-      const int c = 2 * (t & 15);
+      const int c = 2 * xchunk;
       *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c) * 16) = o[0];
       *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c + 1) * 16) = o[1];
     }
@@ -227,39 +242,40 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   const int q = (lane & 15) >> 2;
   const int lrow = 8 * (lane >> 5) + q;
   const int lbyte = lrow * kRowBytes + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-  // flip: chunk c = 16 half + 4 i + ... of x sits one off where bit 3 of c, bit 1 of i, is set
-  auto fragment = [&](const uint8_t* panel, int half, int i, int sub, int flip) {
-    const uint8_t* p = panel + (lbyte ^ (flip << 4)) + half * 256 + ((i ^ q) << 6) + sub * 16 * kRowBytes;
+  // Column tile ti of the panel holds chunks 4 ti ..; those of x sit one off where bit 3 of
+  // the chunk, bit 1 of ti, is set.
+  auto fragment = [&](const uint8_t* panel, int ti, int sub, int flip) {
+    const uint8_t* p = panel + (lbyte ^ (flip << 4)) + ((ti ^ q) << 6) + sub * 16 * kRowBytes;
     const short4_t lo = read_tr(p), hi = read_tr(p + 4 * kRowBytes);
     return __builtin_bit_cast(bf16x8_t, (short8_t){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
   };
 
-  float16_t acc[4][4];
+  float16_t acc[kT][kT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  auto load_fragments = [&](int64_t s, int sub, bf16x8_t (&fa)[4], bf16x8_t (&fb)[4]) {
+  auto load_fragments = [&](int64_t s, int sub, bf16x8_t (&fa)[kT], bf16x8_t (&fb)[kT]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fa[i] = fragment(panel_a(s), wn, i, sub, 0);
+    for (int i = 0; i < kT; ++i) fa[i] = fragment(panel_a(s), kT * wn + i, sub, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fb[j] = fragment(panel_b(s), wk, j, sub, j >> 1);
+    for (int j = 0; j < kT; ++j) fb[j] = fragment(panel_b(s), kT * wk + j, sub, ((kT * wk + j) >> 1) & 1);
   };
-  auto multiply = [&](const bf16x8_t (&fa)[4], const bf16x8_t (&fb)[4]) {
+  auto multiply = [&](const bf16x8_t (&fa)[kT], const bf16x8_t (&fb)[kT]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < kT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
   };
 
   // Four sub-steps of 16 rows per step; each reads the fragments of the next while its own
   // MFMAs run.  The barrier stands before the last: by then this step's panels are read
   // (their last fragments are in registers) and the next step's are complete, so the loads
   // of the step after that start into the freed panels.
-  bf16x8_t fa[2][4], fb[2][4];
+  bf16x8_t fa[2][kT], fb[2][kT];
   stage_gy(s_begin);
   load_x(s_begin);
   store_x(s_begin);
@@ -271,46 +287,45 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
   for (int64_t s = s_begin; s < s_end; ++s) {
     load_fragments(s, 1, fa[1], fb[1]);
     multiply(fa[0], fb[0]);
-    interleave<0x100, 16>();
+    interleave<kT * kT, 4 / kT>();
     load_fragments(s, 2, fa[0], fb[0]);
     store_x(s + 1);
     multiply(fa[1], fb[1]);
-    interleave<0x100, 16>();
+    interleave<kT * kT, 4 / kT>();
     load_fragments(s, 3, fa[1], fb[1]);
     multiply(fa[0], fb[0]);
-    interleave<0x100, 16>();
+    interleave<kT * kT, 4 / kT>();
     step_barrier();
     stage_gy(s + 2);
     load_x(s + 2);
     load_fragments(s + 1, 0, fa[0], fb[0]);
     multiply(fa[1], fb[1]);
-    interleave<0x100, 16>();
+    interleave<kT * kT, 4 / kT>();
   }
   step_barrier();   // no copy still landing in LDS
 
   // The product is computed transposed (x as the first operand): entry e of lane l is
   // column 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32, so a lane holds runs of four
-  // columns.  32 rows at a time pass through the wave's own LDS region (a row stride of 132
-  // words keeps eight rows in different banks) and leave as whole 512-byte rows.
-  constexpr int kStageRow = 132;
-  float* st = reinterpret_cast<float*>(lds) + wave * 32 * kStageRow;
-  static_assert(4 * 32 * kStageRow * 4 <= kLds, "staging fits");
-  const int64_t orow0 = n0 + wn * 128, ocol0 = k0 + wk * 128;
+  // columns.  32 rows at a time pass through the wave's own LDS region (a row stride of 4
+  // words past a multiple of 32 keeps eight rows in different banks) and leave row by row.
+  float* st = reinterpret_cast<float*>(lds) + wave * 32 * G::kOutRow;
+  const int64_t orow0 = n0 + wn * 32 * kT, ocol0 = k0 + wk * 32 * kT;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kT; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4*>(st + (lane & 31) * kStageRow + 32 * j + 8 * e + 4 * (lane >> 5)) =
+        *reinterpret_cast<float4*>(st + (lane & 31) * G::kOutRow + 32 * j + 8 * e + 4 * (lane >> 5)) =
             make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (kOutBf16 && splits == 1) {
-      const int64_t col = ocol0 + 8 * (lane & 15);
+      constexpr int kLanes = 4 * kT;   // lanes per row, 8 values each
+      const int64_t col = ocol0 + 8 * (lane % kLanes);
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int r = 4 * p + (lane >> 4);
-        const float4* f = reinterpret_cast<const float4*>(st + r * kStageRow + 8 * (lane & 15));
+      for (int p = 0; p < 32 * kLanes / 64; ++p) {
+        const int r = 64 / kLanes * p + lane / kLanes;
+        const float4* f = reinterpret_cast<const float4*>(st + r * G::kOutRow + 8 * (lane % kLanes));
         const float4 a = f[0], b = f[1];
         const int64_t row = orow0 + 32 * i + r;
         if (row < n && col < k)
@@ -319,14 +334,20 @@ __global__ void __launch_bounds__(256, 1) weight_grad_kernel(const uint16_t* __r
                                       reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + row * k + col));
       }
     } else {
+      constexpr int kLanes = 8 * kT;   // lanes per row, 4 values each
       float* dst = splits > 1 ? partial + (int64_t)split * n * k : static_cast<float*>(out);
-      const int64_t col = ocol0 + 4 * (lane & 31);
+      const int64_t col = ocol0 + 4 * (lane % kLanes);
 #pragma unroll
-      for (int p = 0; p < 16; ++p) {
-        const int r = 2 * p + (lane >> 5);
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(st + r * kStageRow + 4 * (lane & 31));
+      for (int p = 0; p < 32 * kLanes / 64; ++p) {
+        const int r = 64 / kLanes * p + lane / kLanes;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(st + r * G::kOutRow + 4 * (lane % kLanes));
         const int64_t row = orow0 + 32 * i + r;
-        if (row < n && col < k) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst + row * k + col));
+        if (row < n && col < k) {
+          // partials are read again at once, the result is not
+          u32x4_t* d = reinterpret_cast<u32x4_t*>(dst + row * k + col);
+          if (splits > 1) *d = v;
+          else __builtin_nontemporal_store(v, d);
+        }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -355,24 +376,47 @@ __global__ void __launch_bounds__(256) weight_grad_reduce(const float* __restric
     *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = a;
 }
 
-// Row splits: as many as fill the compute units once, each at least four steps long.
-int row_splits(int64_t m, int64_t n, int64_t k, int cus) {
-  const int64_t tiles = ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
+// Tile size and row splits.
+//
+// A round of large tiles (one per compute unit) takes about 5/3 of a round of small ones
+// (two per compute unit, half the work), so the sizes are weighed by their whole rounds
+// (measured, 4096 rows, large against small: 5120 x 5120, 2 rounds against 4, 210 us against
+// 250; 3328 x 5120, 2 against 3, 208 against 186; 8192 x 5120, 3 against 5, 317 against 360;
+// 777 rows, 1024 x 5120, 1 against 1, 29 against 19).
+//
+// A small tile's rows are split across workgroups while there are fewer tiles than compute
+// units, each split four steps long at least: the partials (4 bytes a value and split,
+// written and read again) cost more than idle slots beyond that (777 rows, 1024 x 5120, 320
+// tiles: unsplit 19 us, two ways 33; 4096 rows, 64 x 5120, 40 tiles: unsplit 50, six ways
+// 17.5, twelve 18.4).  Splits that stay 32 steps long fill the second slot of each compute
+// unit too (16384 rows, 1024 x 1024: four ways 59 us, eight 48).
+struct Plan {
+  int t, splits;
+};
+int64_t tiles_of(int64_t n, int64_t k, int tile) { return ((n + tile - 1) / tile) * ((k + tile - 1) / tile); }
+Plan plan_of(int64_t m, int64_t n, int64_t k, int cus) {
+  const int64_t tiles = tiles_of(n, k, Geo<2>::kTile);
+  const int64_t large_rounds = (tiles_of(n, k, Geo<4>::kTile) + cus - 1) / cus;
+  const int64_t small_rounds = (tiles + 2 * cus - 1) / (2 * cus);
+  if (5 * large_rounds <= 3 * small_rounds) return {4, 1};
   const int64_t steps = (m + kStep - 1) / kStep;
   int64_t sp = std::min<int64_t>(cus / tiles, steps / 4);
-  return (int)std::max<int64_t>(sp, 1);
+  const int64_t twice = 2 * cus / tiles;
+  if (steps >= 32 * twice) sp = twice;
+  return {2, (int)std::max<int64_t>(sp, 1)};
 }
 
-template <bool kAligned, bool kOutBf16>
+template <int kT, bool kAligned, bool kOutBf16>
 hipError_t launch_t(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales, int64_t k,
                     void* grad_w, int splits, float* partial, hipStream_t s) {
+  constexpr int kTile = Geo<kT>::kTile, kLds = Geo<kT>::kLds;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&weight_grad_kernel<kAligned, kOutBf16>), kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&weight_grad_kernel<kT, kAligned, kOutBf16>), kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tn = (int)((n + kTile - 1) / kTile), tk = (int)((k + kTile - 1) / kTile);
-  hipLaunchKernelGGL((weight_grad_kernel<kAligned, kOutBf16>), dim3((uint32_t)((int64_t)tn * tk * splits)), dim3(256),
+  hipLaunchKernelGGL((weight_grad_kernel<kT, kAligned, kOutBf16>), dim3((uint32_t)((int64_t)tn * tk * splits)), dim3(256),
                      kLds, s, gy, m, n, codes, scales, k, grad_w, tn, tk, splits, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
@@ -385,20 +429,24 @@ hipError_t launch_t(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* cod
 }  // namespace
 
 size_t weight_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int cus) {
-  const int sp = row_splits(m, n, k, cus);
+  const int sp = plan_of(m, n, k, cus).splits;
   return sp > 1 ? (size_t)sp * (size_t)n * (size_t)k * sizeof(float) : 0;
 }
 
 hipError_t launch_weight_grad(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales,
                               int64_t k, void* grad_w, bool out_bf16, void* workspace, size_t workspace_bytes,
                               int cus, hipStream_t s) {
-  int splits = row_splits(m, n, k, cus);
-  if (splits > 1 && (workspace == nullptr || workspace_bytes < weight_grad_workspace_bytes(m, n, k, cus))) splits = 1;
-  float* partial = splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  using Fn = decltype(&launch_t<false, false>);
-  static constexpr Fn f[2][2] = {{launch_t<false, false>, launch_t<false, true>},
-                                 {launch_t<true, false>, launch_t<true, true>}};
-  return f[n % 8 == 0 && n < kBufferWidth && k < kBufferWidth ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, splits, partial, s);
+  Plan p = plan_of(m, n, k, cus);
+  if (p.splits > 1 && (workspace == nullptr || workspace_bytes < weight_grad_workspace_bytes(m, n, k, cus))) p.splits = 1;
+  float* partial = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  using Fn = decltype(&launch_t<4, false, false>);
+  static constexpr Fn f[2][2][2] = {{{launch_t<2, false, false>, launch_t<2, false, true>},
+                                     {launch_t<2, true, false>, launch_t<2, true, true>}},
+                                    {{launch_t<4, false, false>, launch_t<4, false, true>},
+                                     {launch_t<4, true, false>, launch_t<4, true, true>}}};
+  const bool aligned = n % 8 == 0 && n < kBufferWidth && k < kBufferWidth;
+  return f[p.t == 4 ? 1 : 0][aligned ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, p.splits, partial,
+                                                                s);
 }
 
 }  // namespace nvfp4

@@ -68,7 +68,7 @@ def test_pack_non_finite_and_leading_dims():
     assert torch.equal(v.nan_to_num(), ref.nan_to_num())
 
 
-WG = [(1, 16, 16), (1, 300, 272), (63, 8, 48), (64, 256, 256), (65, 264, 272), (777, 1024, 512), (130, 129, 144),
+WG = [(1, 16, 16), (4200, 136, 272), (140, 4096, 4112), (66, 4099, 4112), (1, 300, 272), (63, 8, 48), (64, 256, 256), (65, 264, 272), (777, 1024, 512), (130, 129, 144),
       (2000, 40, 5120), (513, 1000, 1040)]
 
 
