@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "checkpoint_device.h"
 #include "nvfp4_device.h"
@@ -44,9 +45,10 @@ RowShape row_shape(int64_t k) {
   return {t, t};
 }
 
-// 16 weights as loaded (8 words of bf16 pairs or 16 of fp32), expanded where used.
+// 16 values as loaded (8 words of bf16 pairs or 16 of fp32), expanded where used: a load
+// can be in flight while other work goes on.
 template <bool kF32>
-struct Weight16 {
+struct Raw16 {
   uint4 raw[kF32 ? 4 : 2];
   __device__ __forceinline__ void load(const void* w, int64_t off) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + off * (kF32 ? 4 : 2));
@@ -115,7 +117,7 @@ __device__ __forceinline__ T group_sum(T v, int lanes) {
 
 // y = bf16((r * s) * w), over r.
 template <bool kWF32>
-__device__ __forceinline__ void normalize16(float (&v)[16], float s, const Weight16<kWF32>& w) {
+__device__ __forceinline__ void normalize16(float (&v)[16], float s, const Raw16<kWF32>& w) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], s), w.get(i));
   round_bf16(v);
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormForward a) {
   const int c = t - sub * a.lanes;
   const int64_t k = a.k;
   const bool in_k = c < k / kBlock;
-  Weight16<kWF32> w;
+  Raw16<kWF32> w;
   if (in_k) w.load(a.w, (int64_t)c * kBlock);
   else w.zero();
   const float gsf_static = a.mode == kNormStatic ? *a.gsf : 0.0f;
@@ -218,7 +220,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormForward a) {
 
 // Second pass of a dynamic scale: y again from r and s (r is in the memory-side cache, and
 // storing y in the first pass would cost more than forming it twice), then its codes.
-// Units and lanes as in the quantizer's own pass.
+// Eight lanes own a 128-wide tile of a row, as in the quantizer's own pass; the grid is a
+// whole number of rows wide (quantize_blocks), so a lane keeps its tile of the weight and
+// walks down the rows, the next row's load in flight.
 constexpr int kQThreads = 256;
 template <bool kSF32, bool kWF32>
 __global__ void __launch_bounds__(kQThreads) rmsnorm_quantize_kernel(const NormForward a, int n_partials) {
@@ -233,40 +237,54 @@ __global__ void __launch_bounds__(kQThreads) rmsnorm_quantize_kernel(const NormF
   const float gsf = global_scale_from_amax(m);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.gsf_out != nullptr) *a.gsf_out = gsf;
 
-  const int64_t kt_count = (a.k + kScaleTileK - 1) / kScaleTileK;
-  const int64_t units = a.rows * kt_count;
+  const int kt_count = (int)((a.k + kScaleTileK - 1) / kScaleTileK);
   const int j = threadIdx.x & 7;
+  const uint32_t unit = blockIdx.x * (kQThreads / 8) + (threadIdx.x >> 3);
+  const int kt = (int)(unit % (uint32_t)kt_count);
+  const int64_t stride = gridDim.x * (kQThreads / 8) / (uint32_t)kt_count;   // rows
+  const int64_t first = unit / (uint32_t)kt_count;
+  const int blk = kt * 8 + j;
+  const bool in_k = blk < a.k / kBlock;
   const void* r = a.r != nullptr ? a.r : a.x;
-  for (int64_t u0 = (int64_t)blockIdx.x * (kQThreads / 8); u0 < units; u0 += (int64_t)gridDim.x * (kQThreads / 8)) {
-    const int64_t unit = u0 + (threadIdx.x >> 3);
-    const int64_t row = unit / kt_count, kt = unit - row * kt_count;
-    const int64_t blk = kt * 8 + j;
-    float v[16];
-    Weight16<kWF32> w;
-    float s = 0.0f;
-    if (row < a.rows && blk < a.k / kBlock) {
-      load_stream16<kSF32>(r, row * a.k + blk * kBlock, v);
-      w.load(a.w, blk * kBlock);
+  Raw16<kWF32> w;
+  if (in_k) w.load(a.w, (int64_t)blk * kBlock);
+  else w.zero();
+  Raw16<kSF32> cur;
+  float s = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row < a.rows && in_k) {
+      cur.load(r, row * a.k + (int64_t)blk * kBlock);
       s = a.rstd[row];
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-      w.zero();
+      cur.zero();
+      s = 0.0f;
     }
-    normalize16<kWF32>(v, s, w);
-    quantize_unit<false>(v, row, kt, j, a.rows, a.k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
+  };
+  fetch(first);
+  // the wave loops while any of its rows is left: quantize_unit shuffles across its lanes
+  for (int64_t row = first; __any(row < a.rows); row += stride) {
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = cur.get(i);
+    const float sr = s;
+    fetch(row + stride);
+    normalize16<kWF32>(y, sr, w);
+    quantize_unit<false>(y, row, kt, j, a.rows, a.k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
   }
 }
 
 // Gradient.  With n = r s, g = gy w and d = sum(g r) over the row:
 //   grad_r = s g - r (s^3 d / K) + grad_residual,   grad_w = sum over rows of gy n
-// (the rounding of y taken as the identity).  Each workgroup walks its rows with its
-// lanes' 16 columns of grad_w in registers and writes one partial row of them;
-// rmsnorm_weight_grad_kernel adds the partials in a fixed order.
+// (the rounding of y taken as the identity).  Each workgroup walks its rows, the next row's
+// loads in flight while one is computed, with its lanes' 16 columns of grad_w in registers,
+// and writes one partial row of them; rmsnorm_weight_grad_kernel adds the partials in a
+// fixed order.  The bound of 1024 threads also holds every variant to 128 registers, four
+// waves per SIMD: a few values spill, and the fourth wave is worth it (4096 x 5120 with
+// 146 registers 49 us, with 128 34 us: 168 MB at 5.0 TB/s).
 template <bool kSF32, bool kWF32, bool kRes>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackward a) {
-  __shared__ double part_ss[16];
-  __shared__ float part_d[16];
+  __shared__ double part_ss[2][16];
+  __shared__ float part_d[2][16];
   __shared__ float colsum[kGroupThreads * 16];
   const int t = threadIdx.x;
   const int rows_here = blockDim.x / a.lanes;
@@ -274,60 +292,75 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
   const int c = t - sub * a.lanes;
   const int64_t k = a.k;
   const bool in_k = c < k / kBlock;
-  Weight16<kWF32> w;
+  Raw16<kWF32> w;
   if (in_k) w.load(a.w, (int64_t)c * kBlock);
   else w.zero();
   float gw[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) gw[i] = 0.0f;
 
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_here) {
-    const int64_t row = row0 + sub;
-    const bool valid = row < a.rows && in_k;
-    const int64_t off = row * k + (int64_t)c * kBlock;
-    float r[16], g[16], q[16];
-    if (valid) {
-      load_stream16<kSF32>(a.r, off, r);
-      load16_bf16(a.gy + off, g);
-      if constexpr (kRes) load_stream16<kSF32>(a.grad_residual, off, q);
+  struct Row {
+    Raw16<kSF32> r, q;
+    Raw16<false> g;
+  };
+  auto fetch = [&](int64_t row, Row& x) {
+    if (row < a.rows && in_k) {
+      const int64_t off = row * k + (int64_t)c * kBlock;
+      x.r.load(a.r, off);
+      x.g.load(a.gy, off);
+      if constexpr (kRes) x.q.load(a.grad_residual, off);
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) r[i] = g[i] = q[i] = 0.0f;
+      x.r.zero();
+      x.g.zero();
+      if constexpr (kRes) x.q.zero();
     }
+  };
+  const int64_t stride = (int64_t)gridDim.x * rows_here;
+  Row cur;
+  fetch((int64_t)blockIdx.x * rows_here + sub, cur);
+  int parity = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += stride, parity ^= 1) {
+    const int64_t row = row0 + sub;
+    Row nxt;
+    fetch(row + stride, nxt);
+    float r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = cur.r.get(i);
     double ss = sum_squares(r);
     float d = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d = fmaf(g[i] * w.get(i), r[i], d);
+    for (int i = 0; i < 16; ++i) d = fmaf(cur.g.get(i) * w.get(i), r[i], d);
     const int lanes = a.lanes < 64 ? a.lanes : 64;
     ss = group_sum(ss, lanes);
     d = group_sum(d, lanes);
     if (a.lanes > 64) {
+      // the other parity's slots may still be read by slower waves; these are free
       if ((t & 63) == 0) {
-        part_ss[t >> 6] = ss;
-        part_d[t >> 6] = d;
+        part_ss[parity][t >> 6] = ss;
+        part_d[parity][t >> 6] = d;
       }
       __syncthreads();
       ss = 0.0;
       d = 0.0f;
       for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
-        ss += part_ss[i];
-        d += part_d[i];
+        ss += part_ss[parity][i];
+        d += part_d[parity][i];
       }
-      __syncthreads();
     }
     const float s = row_scale(ss, k, a.eps);
     const float f = s * s * (d / (float)k);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float n = r[i] * s;
-      gw[i] = fmaf(g[i], n, gw[i]);
-      const float x = fmaf(s, g[i] * w.get(i), -(n * f));
-      r[i] = kRes ? x + q[i] : x;
+      const float n = r[i] * s, g = cur.g.get(i);
+      gw[i] = fmaf(g, n, gw[i]);
+      const float x = fmaf(s, g * w.get(i), -(n * f));
+      r[i] = kRes ? x + cur.q.get(i) : x;
     }
-    if (valid) {
+    if (row < a.rows && in_k) {
       if constexpr (!kSF32) round_bf16(r);
-      store_stream16<kSF32>(a.grad_r, off, r);
+      store_stream16<kSF32>(a.grad_r, row * k + (int64_t)c * kBlock, r);
     }
+    cur = nxt;
   }
   if (a.grad_w == nullptr) return;
   if (rows_here == 1) {
@@ -346,22 +379,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
   }
 }
 
-// grad_w[j] = sum of n partial rows, 32 columns and 8 interleaved row sets per workgroup.
-__global__ void __launch_bounds__(256) rmsnorm_weight_grad_kernel(const float* __restrict__ partials, int n, int64_t k,
-                                                                  float* __restrict__ grad_w) {
-  __shared__ float lds[8][32];
-  const int64_t col = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int set = threadIdx.x >> 5;
+// grad_w[j] = sum of n partial rows: 32 columns per workgroup, 32 interleaved row sets
+// added in order.
+__global__ void __launch_bounds__(1024) rmsnorm_weight_grad_kernel(const float* __restrict__ partials, int n,
+                                                                   int64_t k, float* __restrict__ grad_w) {
+  __shared__ float lds[32][33];
+  const int x = threadIdx.x & 31, set = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + x;
   float a = 0.0f;
   if (col < k) {
 #pragma unroll 8
-    for (int i = set; i < n; i += 8) a += partials[(int64_t)i * k + col];
+    for (int i = set; i < n; i += 32) a += partials[(int64_t)i * k + col];
   }
-  lds[set][threadIdx.x & 31] = a;
+  lds[set][x] = a;
   __syncthreads();
   if (set == 0 && col < k) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += lds[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) a += lds[i][x];
     grad_w[col] = a;
   }
 }
@@ -381,10 +415,23 @@ ForwardFn forward_kernel(const NormForward& a) {
   return f[!a.stream_f32 ? 0 : !a.x_f32 ? 1 : 2][w];
 }
 
-// Workgroups of the row-walking kernels whose per-workgroup results are joined afterwards.
-int64_t walking_blocks(int64_t rows, const RowShape& s) {
+// Workgroups of the row-walking kernels whose per-workgroup results are joined afterwards,
+// at most `most`.
+int64_t walking_blocks(int64_t rows, const RowShape& s, int64_t most) {
   const int64_t per = s.threads / s.lanes;
-  return std::min<int64_t>((rows + per - 1) / per, kNormPartials);
+  return std::min<int64_t>((rows + per - 1) / per, most);
+}
+// The gradient's workgroups leave a row of partials each: enough of them to fill the GPU
+// (4096 x 5120: 256 workgroups 48 us, 512 34, 768 43 with their larger partials).
+constexpr int64_t kBackwardBlocks = 512;
+
+// Second-pass workgroups: a whole number of rows' tiles (at most 128) between a lane's
+// units, so that its tile of the weight stays the same.
+int64_t quantize_blocks(int64_t rows, int64_t k) {
+  const int64_t kt = (k + kScaleTileK - 1) / kScaleTileK;
+  const int64_t want = std::min<int64_t>((rows * kt + kQThreads / 8 - 1) / (kQThreads / 8), 2048);
+  const int64_t unit = kt / std::gcd(kt, (int64_t)(kQThreads / 8));
+  return std::max<int64_t>(want / unit, 1) * unit;
 }
 
 }  // namespace
@@ -397,7 +444,7 @@ hipError_t launch_rmsnorm(NormForward a, hipStream_t s) {
   if (a.mode == kNormDynamic) {
     // one row needs no second pass: its workgroup knows the whole abs-max
     a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
-    blocks = walking_blocks(a.rows, shape);
+    blocks = walking_blocks(a.rows, shape, kNormPartials);
   }
   hipLaunchKernelGGL(forward_kernel(a), dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
   hipError_t e = hipGetLastError();
@@ -405,21 +452,20 @@ hipError_t launch_rmsnorm(NormForward a, hipStream_t s) {
   using QuantFn = void (*)(const NormForward, int);
   static constexpr QuantFn q[2][2] = {{rmsnorm_quantize_kernel<false, false>, rmsnorm_quantize_kernel<false, true>},
                                       {rmsnorm_quantize_kernel<true, false>, rmsnorm_quantize_kernel<true, true>}};
-  const int64_t units = a.rows * ((a.k + kScaleTileK - 1) / kScaleTileK);
-  const int64_t grid = std::min<int64_t>((units + kQThreads / 8 - 1) / (kQThreads / 8), 4096);
+  const int64_t grid = quantize_blocks(a.rows, a.k);
   const bool sf32 = a.residual != nullptr ? a.stream_f32 : a.x_f32;
   hipLaunchKernelGGL(q[sf32 ? 1 : 0][a.w_f32 ? 1 : 0], dim3((uint32_t)grid), dim3(kQThreads), 0, s, a, (int)blocks);
   return hipGetLastError();
 }
 
 size_t rmsnorm_backward_partial_floats(int64_t rows, int64_t k) {
-  return (size_t)walking_blocks(rows, row_shape(k)) * (size_t)k;
+  return (size_t)walking_blocks(rows, row_shape(k), kBackwardBlocks) * (size_t)k;
 }
 
 hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s) {
   const RowShape shape = row_shape(a.k);
   a.lanes = shape.lanes;
-  const int64_t blocks = walking_blocks(a.rows, shape);
+  const int64_t blocks = walking_blocks(a.rows, shape, kBackwardBlocks);
   using Fn = void (*)(const NormBackward);
   static constexpr Fn f[2][2][2] = {
       {{rmsnorm_backward_kernel<false, false, false>, rmsnorm_backward_kernel<false, false, true>},
@@ -431,7 +477,7 @@ hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s) {
                        dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.grad_w == nullptr) return e;
-  hipLaunchKernelGGL(rmsnorm_weight_grad_kernel, dim3((uint32_t)((a.k + 31) / 32)), dim3(256), 0, s, a.partials,
+  hipLaunchKernelGGL(rmsnorm_weight_grad_kernel, dim3((uint32_t)((a.k + 31) / 32)), dim3(1024), 0, s, a.partials,
                      (int)blocks, a.k, a.grad_w);
   return hipGetLastError();
 }
