@@ -65,10 +65,11 @@ def _saved(name: str, ck: Checkpoint) -> tuple[torch.Tensor, torch.Tensor, int, 
     return codes, scales if scales.is_contiguous() else scales.contiguous(), rows, k
 
 
-def _empty_checkpoint(shape, device, rotation_group: int = 0) -> Checkpoint:
-    k = shape[-1]
-    return Checkpoint(torch.empty(shape, dtype=torch.uint8, device=device),
-                      torch.empty((*shape[:-1], _scale_columns(k)), dtype=torch.uint8, device=device), rotation_group)
+def _empty_checkpoint(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
+    """Room for the checkpoint of x."""
+    shape = x.shape
+    return Checkpoint(x.new_empty(shape, dtype=torch.uint8),
+                      x.new_empty((*shape[:-1], _scale_columns(shape[-1])), dtype=torch.uint8), rotation_group)
 
 
 @_on_device
@@ -76,7 +77,7 @@ def checkpoint_pack(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
     """bf16 [..., K] (K a multiple of 16) to its 8-bit checkpoint, after the optional block
     rotation.  A value moves by at most 2^-4 of itself; infinities and NaN become NaN."""
     x2, rows, k = _rows("x", x)
-    ck = _empty_checkpoint(x.shape, x.device, int(rotation_group))
+    ck = _empty_checkpoint(x, int(rotation_group))
     check(lib().nvfp4_checkpoint_pack(_ptr(x2), rows, k, int(rotation_group), _ptr(ck.codes), _ptr(ck.scales),
                                       _stream(x.device)))
     return ck
@@ -110,9 +111,9 @@ def weight_grad(grad_y: torch.Tensor, ck: Checkpoint, dtype: torch.dtype = torch
     _require_device(gy.device, checkpoint=codes)
     if rows != m:
         raise ValueError(f"grad_y has {m} rows, the checkpoint {rows}")
-    out = torch.empty((n, k), dtype=dtype, device=gy.device)
-    need = int(lib().nvfp4_weight_grad_workspace_bytes(m, n, k))
-    ws = torch.empty((need,), dtype=torch.uint8, device=gy.device) if need else None
+    out = gy.new_empty((n, k), dtype=dtype)
+    need = lib().nvfp4_weight_grad_workspace_bytes(m, n, k)
+    ws = gy.new_empty((need,), dtype=torch.uint8) if need else None
     check(lib().nvfp4_weight_grad(_ptr(gy), m, n, _ptr(codes), _ptr(scales), k, _ptr(out), DTYPE_CODES[dtype], _ptr(ws),
                                   need, _stream(gy.device)))
     return out
@@ -123,8 +124,8 @@ def swiglu_checkpoint(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tenso
     """:func:`swiglu` and the 8-bit checkpoints of ``gate`` and ``up``, in one pass."""
     g2, u2 = _gate_up(gate, up)
     _require_device(gate.device, up=up)
-    x = torch.empty(gate.shape, dtype=torch.bfloat16, device=gate.device)
-    g, u = _empty_checkpoint(gate.shape, gate.device), _empty_checkpoint(gate.shape, gate.device)
+    x = gate.new_empty(gate.shape)
+    g, u = _empty_checkpoint(gate), _empty_checkpoint(gate)
     check(lib().nvfp4_swiglu_checkpoint(_ptr(g2), _ptr(u2), g2.shape[0], g2.shape[1], _ptr(x), _ptr(g.codes),
                                         _ptr(g.scales), _ptr(u.codes), _ptr(u.scales), _stream(gate.device)))
     return x, g, u
@@ -149,8 +150,7 @@ def swiglu_backward(grad_x: torch.Tensor, gate, up) -> tuple[torch.Tensor, torch
     if gm != [rows, k] or um != [rows, k]:
         raise ValueError(f"grad_x, gate and up must have the same shape, got {list(gx.shape)}, {list(g.shape)} and "
                          f"{list(u.shape)}")
-    dg = torch.empty(grad_x.shape, dtype=torch.bfloat16, device=gx.device)
-    du = torch.empty_like(dg)
+    dg, du = gx.new_empty(grad_x.shape), gx.new_empty(grad_x.shape)
     check(lib().nvfp4_swiglu_backward(_ptr(gx), _ptr(g), _ptr(gs), _ptr(u), _ptr(us), rows, k, _ptr(dg), _ptr(du),
                                       _stream(gx.device)))
     return dg, du
@@ -172,7 +172,7 @@ def activation_backward(grad_y: torch.Tensor, z, activation: str | None) -> torc
     _require_device(gy.device, z=z2)
     if zm != [rows, n]:
         raise ValueError(f"grad_y and z must have the same shape, got {list(gy.shape)} and {list(z2.shape)}")
-    out = torch.empty(grad_y.shape, dtype=torch.bfloat16, device=gy.device)
+    out = gy.new_empty(grad_y.shape)
     check(lib().nvfp4_activation_backward(_ptr(gy), _ptr(z2), _ptr(zs), rows, n, act, _ptr(out), _stream(gy.device)))
     return out
 

@@ -42,7 +42,7 @@ class _Inputs:
                                  f"{list(residual.shape)}")
             if x.dtype == torch.float32 and residual.dtype != torch.float32:
                 raise ValueError("an fp32 x needs an fp32 residual")
-            self.out = torch.empty_like(self.res)
+            self.out = x.new_empty(x.shape, dtype=self.res.dtype)
         self.args = (_ptr(self.x), DTYPE_CODES[x.dtype], _ptr(self.res),
                      DTYPE_CODES[x.dtype if self.res is None else self.res.dtype], _ptr(self.w),
                      DTYPE_CODES[self.w.dtype], self.rows, self.k, float(eps))
@@ -50,8 +50,8 @@ class _Inputs:
 
 def _rmsnorm(x, weight, eps, residual, packed: bool):
     a = _Inputs(x, weight, eps, residual)
-    y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    ck = _empty_checkpoint(x.shape, x.device) if packed else None
+    y = x.new_empty(x.shape, dtype=torch.bfloat16)
+    ck = _empty_checkpoint(x) if packed else None
     check(lib().nvfp4_rmsnorm(*a.args, _ptr(a.out), _ptr(y), _ptr(ck.codes) if ck else None,
                               _ptr(ck.scales) if ck else None, _stream(x.device)))
     return y, a.out, ck
@@ -83,13 +83,13 @@ def quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     them; with ``residual`` also r.  ``global_sf_x=None``: dynamic scale."""
     a = _Inputs(x, weight, eps, residual)
     dev = x.device
-    codes = torch.empty((a.rows, a.k // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((scale_bytes(a.rows, a.k),), dtype=torch.uint8, device=dev)
-    gsf = torch.empty((), dtype=torch.float32, device=dev)
+    codes = x.new_empty((a.rows, a.k // 2), dtype=torch.uint8)
+    scales = x.new_empty((scale_bytes(a.rows, a.k),), dtype=torch.uint8)
+    gsf = x.new_empty((), dtype=torch.float32)
     g = None if global_sf_x is None else _scalar_f32(global_sf_x, dev)
     _require_device(dev, global_sf_x=g)
     need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(a.rows) if g is None else 0
-    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    ws = x.new_empty((need,), dtype=torch.uint8) if need else None
     check(lib().nvfp4_quantize_rmsnorm(*a.args, _ptr(g), _ptr(a.out), _ptr(codes), _ptr(scales), _ptr(gsf), _ptr(ws),
                                        need, _stream(dev)))
     return (codes, scales, gsf) if residual is None else (codes, scales, gsf, a.out)
@@ -113,10 +113,10 @@ def rmsnorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor
         if rm != [rows, k]:
             raise ValueError(f"grad_residual and r must have the same shape, got {list(grad_residual.shape)} and "
                              f"{list(r.shape)}")
-    grad_r = torch.empty(r.shape, dtype=r.dtype, device=r.device)
-    grad_w = torch.empty((k,), dtype=torch.float32, device=r.device)
+    grad_r = r.new_empty(r.shape)
+    grad_w = r.new_empty((k,), dtype=torch.float32)
     need = lib().nvfp4_rmsnorm_backward_workspace_bytes(rows, k)
-    ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=r.device)
+    ws = r.new_empty((max(need, 256),), dtype=torch.uint8)
     check(lib().nvfp4_rmsnorm_backward(_ptr(gy), _ptr(r2), DTYPE_CODES[r.dtype], _ptr(w), DTYPE_CODES[w.dtype], _ptr(gr),
                                        rows, k, float(eps), _ptr(grad_r), _ptr(grad_w), _ptr(ws), ws.numel(),
                                        _stream(r.device)))

@@ -250,7 +250,7 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         raise ValueError(f"x must be bf16, got {x.dtype}")
     orig = x.shape
     k = orig[-1]
-    x2d = x.reshape(-1, k)
+    x2d = x if x.dim() == 2 else x.reshape(-1, k)
     if not x2d.is_contiguous():
         x2d = x2d.contiguous()
     _require_cuda("x", x2d, torch.bfloat16, 2)
@@ -270,9 +270,9 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     m = x2d.shape[0]
     need = linear_workspace_bytes(m, k, out_features)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        workspace = x2d.new_empty((need,), dtype=torch.uint8)
     if out is None:
-        out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
+        out = x2d.new_empty((m, out_features))
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
         _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias)
@@ -281,11 +281,11 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
                                           _stream(x.device)))
-        return out.reshape(*orig[:-1], out_features)
+        return out if x.dim() == 2 else out.reshape(*orig[:-1], out_features)
     check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
                              _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
                              _stream(x.device)))
-    return out.reshape(*orig[:-1], out_features)
+    return out if x.dim() == 2 else out.reshape(*orig[:-1], out_features)
 
 
 def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor, global_sf_w: torch.Tensor,
