@@ -105,9 +105,10 @@ __device__ __forceinline__ uint32_t finish_bf16(float y, const uint16_t* bias, i
 }
 
 // Eight consecutive elements of a row, z already with its bias, packed to bf16.  Wide
-// accesses: the caller has checked epilogue_wide and that all eight are in the row.
+// accesses: the caller has checked epilogue_wide and that all eight are in the row, and has
+// loaded the residual's eight values r (ignored without one).
 template <int kAct>
-__device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const Epilogue& ep, int64_t idx) {
+__device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const uint4& r, const Epilogue& ep, int64_t idx) {
   if (ep.preact != nullptr)
     *reinterpret_cast<uint4*>(ep.preact + idx) = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
                                                             pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
@@ -115,7 +116,6 @@ __device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const Epilogu
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate_t<kAct>(z[i]);
   if (ep.residual != nullptr) {
-    const uint4 r = *reinterpret_cast<const uint4*>(ep.residual + idx);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -125,6 +125,10 @@ __device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const Epilogu
   }
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                     pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ uint4 residual8(const Epilogue& ep, int64_t idx) {
+  return ep.residual != nullptr ? *reinterpret_cast<const uint4*>(ep.residual + idx) : make_uint4(0, 0, 0, 0);
 }
 
 // Whether finish8_bf16's wide accesses, and such a store to out, are aligned for rows of

@@ -45,7 +45,9 @@ using namespace gemm;
 constexpr int kRows = 256;                       // rows of B (output columns) per tile
 constexpr int kEpiRowBytes = 128 * 2 + 16;
 constexpr int kEpiF32RowBytes = 128 * 4 + 16;
-constexpr int kEpiF32Lds = 4 * 32 * kEpiF32RowBytes;   // four waves' staging of the fp32 epilogue
+constexpr int kEpiF32Wave = 32 * kEpiF32RowBytes;         // a wave's staging of the fp32 epilogue,
+constexpr int kEpiResWave = 8 * 64 * 16;                  // and of the residual it adds
+constexpr int kEpiF32Lds = 4 * (kEpiF32Wave + kEpiResWave);
 
 // Tile geometry for kTM 32-row MFMA tiles per wave along M (2 x 2 waves): A rows per
 // tile 64 * kTM (256, or 128 for few activation rows), B rows 256.  One LDS stage holds
@@ -346,10 +348,11 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     // (16-byte writes of 4 consecutive columns; a row stride of 132 words keeps eight rows
     // in different banks), read back as 8 consecutive columns of a row per lane.  Each wave
     // uses its own LDS region, as in the plain epilogue below.
-    uint8_t* st = lds + wave * 32 * kEpiF32RowBytes;
+    uint8_t* st = lds + wave * kEpiF32Wave;
+    uint8_t* rst = lds + 4 * kEpiF32Wave + wave * kEpiResWave + lane * 16;   // this lane's own slots
     const int64_t er0 = row0 + wm * (32 * kTM);
     const int64_t ec = col0 + wn * 128 + 8 * (lane & 15);
-    const bool wide = ec + 8 <= n && epilogue_wide(ep, out, ldo);
+    const bool wide = (n & 7) == 0 && epilogue_wide(ep, out, ldo);   // whole 8-column groups
     float bv[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && ec + h < n ? bf16_to_f32(bias[ec + h]) : 0.0f;
@@ -357,6 +360,19 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
       const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, min(er0 + i * 32 + lr, m - 1)) : alpha;
+      // The residual of this lane's eight rows is in flight while the product is staged, then
+      // waits in LDS: the loop over the rows stays rolled (unrolled, 32 copies of the
+      // activation overflow the instruction cache: 32768 x 1024 -> 4096 with gelu 368 us
+      // against 342), and a load inside it would be waited for every time (residual 388 us
+      // against 317).
+      uint4 res[8];
+      if (ep.residual != nullptr) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int64_t row = er0 + i * 32 + 4 * p + (lane >> 4);
+          res[p] = wide && row < m && ec < n ? residual8(ep, row * ldo + ec) : make_uint4(0, 0, 0, 0);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -367,27 +383,39 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
           *reinterpret_cast<float4*>(st + lr * kEpiF32RowBytes + (32 * j + 8 * q + 4 * kh) * 4) =
               make_float4(y[0], y[1], y[2], y[3]);
         }
-      lds_order();
-#pragma unroll 1
-      for (int p = 0; p < 8; ++p) {
-        const int r = 4 * p + (lane >> 4);
-        const int64_t row = er0 + i * 32 + r;
-        const float4* f = reinterpret_cast<const float4*>(st + r * kEpiF32RowBytes + (lane & 15) * 32);
-        const float4 f0 = f[0], f1 = f[1];
-        const float z[8] = {__fadd_rn(f0.x, bv[0]), __fadd_rn(f0.y, bv[1]), __fadd_rn(f0.z, bv[2]),
-                            __fadd_rn(f0.w, bv[3]), __fadd_rn(f1.x, bv[4]), __fadd_rn(f1.y, bv[5]),
-                            __fadd_rn(f1.z, bv[6]), __fadd_rn(f1.w, bv[7])};
-        if (row >= m) continue;
-        const int64_t idx = row * ldo + ec;
-        if (wide) {
-          const uint4 o = finish8_bf16<kEpi>(z, ep, idx);
-          typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-          __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(out + idx));
-        } else {
-          const float y[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+      if (ep.residual != nullptr) {
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
-            if (ec + h < n) out[idx + h] = (uint16_t)finish_bf16(y[h], bias, ec + h, ep, idx + h);
+        for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(rst + p * 1024) = res[p];
+      }
+      lds_order();
+      if (wide) {
+#pragma unroll 1
+        for (int p = 0; p < 8; ++p) {
+          const int64_t row = er0 + i * 32 + 4 * p + (lane >> 4);
+          const float4* f =
+              reinterpret_cast<const float4*>(st + (4 * p + (lane >> 4)) * kEpiF32RowBytes + (lane & 15) * 32);
+          const float4 f0 = f[0], f1 = f[1];
+          const float z[8] = {__fadd_rn(f0.x, bv[0]), __fadd_rn(f0.y, bv[1]), __fadd_rn(f0.z, bv[2]),
+                              __fadd_rn(f0.w, bv[3]), __fadd_rn(f1.x, bv[4]), __fadd_rn(f1.y, bv[5]),
+                              __fadd_rn(f1.z, bv[6]), __fadd_rn(f1.w, bv[7])};
+          if (row < m && ec < n) {
+            const int64_t idx = row * ldo + ec;
+            const uint4 r = ep.residual != nullptr ? *reinterpret_cast<const uint4*>(rst + p * 1024) : make_uint4(0, 0, 0, 0);
+            const uint4 o = finish8_bf16<kEpi>(z, r, ep, idx);
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(out + idx));
+          }
+        }
+      } else {
+        // any width and alignment: value by value, neighbouring lanes on neighbouring columns
+        const int64_t c0 = col0 + wn * 128;
+#pragma unroll 1
+        for (int v = lane; v < 32 * 128; v += 64) {
+          const int64_t row = er0 + i * 32 + (v >> 7), c = c0 + (v & 127);
+          if (row < m && c < n)
+            out[row * ldo + c] = (uint16_t)finish_bf16(
+                *reinterpret_cast<const float*>(st + (v >> 7) * kEpiF32RowBytes + (v & 127) * 4), bias, c, ep,
+                row * ldo + c);
         }
       }
       lds_order();
@@ -538,12 +566,13 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
       if (bias != nullptr)
 #pragma unroll
         for (int h = 0; h < 8; ++h) z[h] = __fadd_rn(z[h], bf16_to_f32(bias[col + h]));
+      const uint4 r = residual8(ep, idx);
       uint4 o;
       switch (ep.act) {
-        case NVFP4_ACT_SILU: o = finish8_bf16<NVFP4_ACT_SILU>(z, ep, idx); break;
-        case NVFP4_ACT_GELU: o = finish8_bf16<NVFP4_ACT_GELU>(z, ep, idx); break;
-        case NVFP4_ACT_GELU_TANH: o = finish8_bf16<NVFP4_ACT_GELU_TANH>(z, ep, idx); break;
-        default: o = finish8_bf16<NVFP4_ACT_NONE>(z, ep, idx);
+        case NVFP4_ACT_SILU: o = finish8_bf16<NVFP4_ACT_SILU>(z, r, ep, idx); break;
+        case NVFP4_ACT_GELU: o = finish8_bf16<NVFP4_ACT_GELU>(z, r, ep, idx); break;
+        case NVFP4_ACT_GELU_TANH: o = finish8_bf16<NVFP4_ACT_GELU_TANH>(z, r, ep, idx); break;
+        default: o = finish8_bf16<NVFP4_ACT_NONE>(z, r, ep, idx);
       }
       *reinterpret_cast<uint4*>(out + idx) = o;
     } else {
