@@ -6,7 +6,8 @@ import torch
 
 from ._lib import check, lib
 from .checkpoint import Checkpoint, _empty_checkpoint, _rows
-from .nvfp4 import DTYPE_CODES, _on_device, _ptr, _require_device, _scalar_f32, _stream, scale_bytes
+from .nvfp4 import (DTYPE_CODES, _on_device, _ptr, _require_device, _scalar_f32, _stream, scale_bytes,
+                    static_global_sf)
 
 NORM_MAX_K = 16384
 
@@ -88,6 +89,9 @@ def quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     gsf = x.new_empty((), dtype=torch.float32)
     g = None if global_sf_x is None else _scalar_f32(global_sf_x, dev)
     _require_device(dev, global_sf_x=g)
+    if a.rows == 0:
+        # nothing is launched: the scale is the given one, or that of an abs-max of 0
+        gsf.copy_(static_global_sf(torch.zeros_like(gsf)) if g is None else g.reshape(()))
     need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(a.rows) if g is None else 0
     ws = x.new_empty((need,), dtype=torch.uint8) if need else None
     check(lib().nvfp4_quantize_rmsnorm(*a.args, _ptr(g), _ptr(a.out), _ptr(codes), _ptr(scales), _ptr(gsf), _ptr(ws),

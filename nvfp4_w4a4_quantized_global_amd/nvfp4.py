@@ -578,6 +578,7 @@ class _NVFP4STEFn(torch.autograd.Function):
         ctx.save_for_backward(x, weight, z, x_scales, z_scales)
         ctx.group = group
         ctx.activation = activation
+        ctx.res_shape = None if residual is None else residual.shape
         ctx.has_bias = bias is not None
         ctx.bias_dtype = None if bias is None else bias.dtype
         return y
@@ -589,7 +590,7 @@ class _NVFP4STEFn(torch.autograd.Function):
         packed_input = x_scales is not None
         n, k = weight.shape
         g = ctx.group
-        grad_r = grad_y if ctx.needs_input_grad[7] else None
+        grad_r = grad_y.reshape(ctx.res_shape) if ctx.needs_input_grad[7] else None
         gy2 = grad_y.reshape(-1, n)
         if z is not None:
             saved_z = z if z_scales is None else ck.Checkpoint(z, z_scales)

@@ -28,7 +28,8 @@ def _f(t):
 # tiles; K % 32 != 0 takes the generic kernel; odd widths)
 PATHS = [(1, 512, 96, None), (1, 5120, 1024, 8.0), (1, 25600, 400, None), (3, 1024, 333, None), (16, 1024, 1000, None),
          (20, 512, 96, 4.0), (40, 2048, 520, None), (100, 1024, 777, None), (300, 1280, 640, None), (513, 256, 257, None),
-         (9, 272, 77, None), (300, 144, 300, None), (257, 528, 1024, 8.0)]
+         (9, 272, 77, None), (300, 144, 300, None), (257, 528, 1024, 8.0),
+         (100, 256, 4100, None), (128, 128, 4096, 4.0)]
 
 
 def _case(m, k, n, gsf, seed=0):
@@ -79,6 +80,19 @@ def test_every_path(m, k, n, gsf):
             _check(got, pre, plain, bias, act, r)
             if act or r is not None:
                 assert torch.equal(lib.nvfp4_linear(x, pk, sc, gw, bias, n, g, activation=act, residual=r), got)
+
+
+@pytest.mark.parametrize("m,k,n", [(2048, 256, 8192), (2300, 128, 8200), (1100, 48, 6600)])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_whole_rounds_equal_row_slices(m, k, n, act):
+    """At least one tile per compute unit (whole rounds; the fallback kernel's larger tile for
+    K = 48): the same bits as 256-row slices of the call, under one static scale."""
+    lib = nv()
+    x, (pk, sc, gw), b, res, g = _case(m, k, n, 6.0)
+    got = lib.nvfp4_linear(x, pk, sc, gw, b, n, g, activation=act, residual=res)
+    for r in range(0, m, 256):
+        part = lib.nvfp4_linear(x[r:r + 256], pk, sc, gw, b, n, g, activation=act, residual=res[r:r + 256])
+        assert torch.equal(got[r:r + 256], part), r
 
 
 @pytest.mark.parametrize("m,k,n", [(1, 512, 2048), (16, 1024, 1000), (40, 2048, 520), (300, 1280, 640), (300, 144, 300),
@@ -226,6 +240,18 @@ def test_train(g, act, with_res, packed):
     assert torch.all((x.grad.double().cpu() - gxr).abs() <= rel * mag + 2.0 ** -8 * (gxr.abs() + rel * mag))
     if with_res:
         assert torch.equal(res.grad, gy)
+
+
+def test_train_residual_of_another_shape():
+    """A residual given as [rows, N] to a [batch, tokens, K] input gets its gradient as [rows, N]."""
+    lib = nv()
+    x = workloads.draw("normal", (2, 6, 64), 110, 0).to(DEV)
+    w = workloads.draw("normal", (48, 64), 110, 1).float().to(DEV)
+    res = workloads.draw("normal", (12, 48), 110, 2).to(DEV).requires_grad_(True)
+    y = lib.nvfp4_linear_train(x, w, residual=res, checkpoint=True)
+    assert y.shape == (2, 6, 48)
+    y.sum().backward()                     # an expanded, strided gradient
+    assert torch.equal(res.grad, torch.ones_like(res))
 
 
 def test_train_shared_checkpoint_block():

@@ -93,16 +93,43 @@ def test_outputs_bitwise(m, k, xd, rd, wd):
             assert np.array_equal(_f(got[3]), r_ref)
 
 
-@pytest.mark.parametrize("m", [1, 2, 1025, 4099])
-def test_many_rows_dynamic_equals_two_steps(m):
-    """Past the row-walking grid: the dynamic scale's partial maxima, and codes equal to
-    quantizing the written norm."""
-    k = 512 if m > 2 else 5120
+@pytest.mark.parametrize("m,k", [(1, 5120), (2, 5120), (2, 16384), (3, 16384), (8, 16384), (9, 16384), (11, 144),
+                                 (15, 8192), (16, 8192), (16, 8208), (17, 5120), (1025, 512), (4099, 512)])
+def test_dynamic_equals_two_steps(m, k):
+    """The one-row and the two-pass form (and past the row-walking grid): codes equal
+    to quantizing the written norm."""
     x, res, w = (t.to(DEV) for t in _inputs(m, k, BF, BF, F, m))
     c, s, g, r = nv().quantize_rmsnorm(x, w, 1e-5, res)
     y, r2 = nv().rmsnorm(x, w, 1e-5, res)
     c2, s2, g2 = nv().quantize_activation(y)
     assert torch.equal(c, c2) and torch.equal(s, s2) and torch.equal(g, g2) and torch.equal(r, r2)
+
+
+@pytest.mark.parametrize("m,k", [(1, 512), (6, 2048), (40, 1024)])
+def test_residual_in_place(m, k):
+    """The C call may update the residual (or x) in place, on every form."""
+    from nvfp4_w4a4_quantized_global_amd._lib import check, lib
+    x, res, w = (t.to(DEV) for t in _inputs(m, k, BF, BF, F, 5))
+    c0, s0, g0, r0 = nv().quantize_rmsnorm(x, w, 1e-6, res)
+    y0, _, ck0 = nv().rmsnorm_checkpoint(x, w, 1e-6, res)
+    stream = torch.cuda.current_stream().cuda_stream
+    for over in ("residual", "x"):
+        for quantize in (True, False):
+            xi, ri = x.clone(), res.clone()
+            dst = ri if over == "residual" else xi
+            args = (xi.data_ptr(), 0, ri.data_ptr(), 0, w.data_ptr(), 1, m, k, 1e-6)
+            if quantize:
+                c, s, g = torch.zeros_like(c0), torch.zeros_like(s0), torch.zeros_like(g0)
+                need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(m)
+                ws = torch.empty((max(need, 1),), dtype=torch.uint8, device=DEV)
+                check(lib().nvfp4_quantize_rmsnorm(*args, None, dst.data_ptr(), c.data_ptr(), s.data_ptr(), g.data_ptr(),
+                                                   ws.data_ptr(), need, stream))
+                assert torch.equal(c, c0) and torch.equal(s, s0) and torch.equal(g, g0)
+            else:
+                y, cc, cs = torch.empty_like(y0), torch.empty_like(ck0.codes), torch.empty_like(ck0.scales)
+                check(lib().nvfp4_rmsnorm(*args, dst.data_ptr(), y.data_ptr(), cc.data_ptr(), cs.data_ptr(), stream))
+                assert torch.equal(y, y0) and torch.equal(cc, ck0.codes) and torch.equal(cs, ck0.scales)
+            assert torch.equal(dst, r0)
 
 
 def test_accuracy_against_float64():
@@ -150,6 +177,7 @@ def test_empty_input():
     assert ck.codes.shape == (0, 64) and ck.scales.shape == (0, 2) and r.shape == (0, 64)
     c, s, g = nv().quantize_rmsnorm(x, w)
     assert c.shape == (0, 32) and s.numel() == 0
+    assert np.float32(g.item()) == o.global_sf(0.0) and nv().quantize_rmsnorm(x, w, 1e-6, x, 3.0)[2].item() == 3.0
     gx, gw = nv().rmsnorm_backward(x, x, w)
     assert gx.shape == (0, 64) and torch.equal(gw, torch.zeros_like(gw))
 
