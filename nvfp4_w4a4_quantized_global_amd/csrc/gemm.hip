@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, const Epilogue ep,
-    uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16) {
+    const uint16_t* __restrict__ bias,
+    uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16, const Epilogue ep) {
   using C = Cfg<WM, WN, TM, TN>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
@@ -316,8 +316,8 @@ hipError_t launch_cfg(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m
   const int tiles_m = (int)((m + C::BM - 1) / C::BM);
   const int tiles_n = (int)((n + C::BN - 1) / C::BN);
   hipLaunchKernelGGL((gemm_kernel<WM, WN, TM, TN, kEpi>), dim3(tiles_m * tiles_n), dim3(C::kThreads), C::kLds, s, a_codes,
-                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, b_srows, ldo, tiles_m,
-                     tiles_n, aligned16);
+                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, b_srows, ldo, tiles_m,
+                     tiles_n, aligned16, ep);
   return hipGetLastError();
 }
 

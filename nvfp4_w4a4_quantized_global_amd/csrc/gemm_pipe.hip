@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, const Epilogue ep, uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m,
+    const uint16_t* __restrict__ bias, uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m,
     int tiles_n, int tile0, int splits, int sub,
-    float* __restrict__ partial) {
+    float* __restrict__ partial, const Epilogue ep) {   // ep last: the plain variants never fetch it
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   using G = Geo<kTM>;
   constexpr int kOffB = G::kOffB, kOffAS = G::kOffAS, kOffBS = G::kOffBS, kStage = G::kStage;
@@ -506,12 +506,12 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
 // Each thread finishes 8 consecutive columns of one output row: entries 4 q' .. 4 q' + 3
 // of accumulator block (i, j) of the main kernel's lanes l and l + 32 (l < 32) of one
 // wave; consecutive threads take consecutive l, so the partial reads coalesce.
-template <int kTM>
+template <int kTM, bool kEpi>
 __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ partial, int splits, int tiles,
                                                       int tile0, int sub, int tiles_m, int64_t m, int64_t n,
                                                       const float* __restrict__ gsf_a, const float* __restrict__ gsf_b,
                                                       int64_t a_seg_rows, const uint16_t* __restrict__ bias,
-                                                      const Epilogue ep, bool epi, uint16_t* out, int64_t ldo) {
+                                                      uint16_t* out, int64_t ldo, const Epilogue ep) {
   using G = Geo<kTM>;
   constexpr int kPerTile = G::kAcc * 256 / 8;     // threads per tile
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
   const int64_t col = (int64_t)tn * kRows + (wave & 1) * 128 + j * 32 + 8 * qq;
   if (row >= m || col >= n) return;
   const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, row);
-  if (epi) {
+  if constexpr (kEpi) {
     float z[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) z[h] = __fmul_rn(alpha, __fmul_rn(acc[h], kAccUnscale));
@@ -665,12 +665,17 @@ hipError_t launch_split_tail(const PipePlan& p, int sub, const uint8_t* a_codes,
   const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
   const int64_t units = p.rest * sub;
   hipLaunchKernelGGL((gemm_pipe_kernel<true, kTM, kPlain>), dim3((uint32_t)(units * p.splits)), dim3(256), kLds, s, a_codes,
-                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn,
-                     (int)p.full, p.splits, sub, partial);
+                     a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn,
+                     (int)p.full, p.splits, sub, partial, ep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((split_k_reduce<kTM>), dim3((uint32_t)(units * Geo<kTM>::kAcc / 8)), dim3(256), 0, s, partial,
-                     p.splits, (int)units, (int)p.full, sub, tm, m, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, n);
+  const dim3 grid((uint32_t)(units * Geo<kTM>::kAcc / 8));
+  if (ep.active())
+    hipLaunchKernelGGL((split_k_reduce<kTM, true>), grid, dim3(256), 0, s, partial, p.splits, (int)units, (int)p.full,
+                       sub, tm, m, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, ep);
+  else
+    hipLaunchKernelGGL((split_k_reduce<kTM, false>), grid, dim3(256), 0, s, partial, p.splits, (int)units, (int)p.full,
+                       sub, tm, m, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, ep);
   return hipGetLastError();
 }
 
@@ -688,16 +693,16 @@ hipError_t launch_plan(const PipePlan& p, const uint8_t* a_codes, const uint8_t*
   const int tm = (int)p.tiles_m, tn = (int)p.tiles_n;
   if (p.full > 0) {
     hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM, kEpi>), dim3((uint32_t)p.full), dim3(256), kLds, s, a_codes, a_scales,
-                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn, 0, 1, 1,
-                       (float*)nullptr);
+                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn, 0, 1, 1,
+                       (float*)nullptr, ep);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (p.rest == 0) return hipSuccess;
   if (p.splits == 1) {
     hipLaunchKernelGGL((gemm_pipe_kernel<false, kTM, kEpi>), dim3((uint32_t)p.rest), dim3(256), kLds, s, a_codes, a_scales,
-                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, n, n, tm, tn, (int)p.full, 1,
-                       1, (float*)nullptr);
+                       m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, n, n, tm, tn, (int)p.full, 1,
+                       1, (float*)nullptr, ep);
     return hipGetLastError();
   }
   if (kTM == 4 && p.sub == 2)

@@ -40,13 +40,15 @@ typedef float float4_t __attribute__((ext_vector_type(4)));
 constexpr int kCols = 64;            // output columns per block (4 MFMA tiles of 16)
 constexpr int kWaves = 4;
 
-template <int MT>   // M tiles of 16 rows
+// MT: M tiles of 16 rows.  kEpi (here and below): the epilogue with activation and residual,
+// a variant of its own so that the plain kernels stay as small as they are.
+template <int MT, bool kEpi>
 __global__ void __launch_bounds__(256) gemm_skinny_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi, uint16_t* out, int splits,
-    float* __restrict__ partial) {
+    const uint16_t* __restrict__ bias, uint16_t* out, int splits,
+    float* __restrict__ partial, const Epilogue ep) {   // ep last: the plain variants never fetch it
   __shared__ float red[MT * 4][4][64];     // waves 1..3 hand their sums to wave 0, one at a time
 
   const int col_group = blockIdx.x / splits;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
           const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
           const float v = __fmul_rn(al, __fmul_rn(acc[i][j][e], kAccUnscale));
           uint32_t y = f32_to_bf16(v);
-          if (epi) y = finish_bf16(v, bias, col, ep, row * n + col);
+          if constexpr (kEpi) y = finish_bf16(v, bias, col, ep, row * n + col);
           else if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
           out[row * n + col] = (uint16_t)y;
         }
@@ -200,11 +202,12 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
 }
 
 // Sums the per-split partials [splits][m][n] in split order, then the epilogue.
+template <bool kEpi>
 __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restrict__ partial, int splits, int64_t m,
                                                           int64_t n, const float* __restrict__ gsf_a,
                                                           const float* __restrict__ gsf_b, int64_t a_seg_rows,
-                                                          const uint16_t* __restrict__ bias, const Epilogue ep,
-                                                          bool epi, uint16_t* out) {
+                                                          const uint16_t* __restrict__ bias, uint16_t* out,
+                                                          const Epilogue ep) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= m * n) return;
   float acc = 0.0f;
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restric
   const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, idx / n);
   const float v = __fmul_rn(alpha, __fmul_rn(acc, kAccUnscale));
   uint32_t y = f32_to_bf16(v);
-  if (epi) y = finish_bf16(v, bias, idx % n, ep, idx);
+  if constexpr (kEpi) y = finish_bf16(v, bias, idx % n, ep, idx);
   else if (bias != nullptr) y = add_bias_bf16(y, bias[idx % n]);
   out[idx] = (uint16_t)y;
 }
@@ -304,15 +307,15 @@ __device__ __forceinline__ void dec_lds_order() { asm volatile("s_waitcnt lgkmcn
 // blocks (six super tiles) or two eight-wave blocks (eight) fit a compute unit's LDS.
 constexpr int fuse_max_st(int waves) { return waves == 8 ? 8 : 6; }
 constexpr int kFuseStatic = 1, kFuseDynamic = 2;
-template <bool kA16, int kDW, bool kOne, int kFuse = 0>
+template <bool kA16, int kDW, bool kOne, int kFuse, bool kEpi>
 __global__ void __launch_bounds__(64 * kDW)
 __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 : 4))) gemm_decode_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, const Epilogue ep, bool epi, uint16_t* out, int splits,
+    const uint16_t* __restrict__ bias, uint16_t* out, int splits,
     float* __restrict__ partial,
-    const uint16_t* __restrict__ a16, float* __restrict__ gsf_dst) {
+    const uint16_t* __restrict__ a16, float* __restrict__ gsf_dst, const Epilogue ep) {
   // direct-load instructions per super tile and wave; bytes per slot and where the
   // weight's scale words sit in it
   constexpr int kLoads = kFuse ? 3 : kOne || kA16 ? 5 : 6;
@@ -576,7 +579,7 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
       const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
       const float v = __fmul_rn(al, __fmul_rn(acc[e], kAccUnscale));
       uint32_t y = f32_to_bf16(v);
-      if (epi) y = finish_bf16(v, bias, col, ep, row * n + col);
+      if constexpr (kEpi) y = finish_bf16(v, bias, col, ep, row * n + col);
       else if (bias != nullptr) y = add_bias_bf16(y, bias[col]);
       out[row * n + col] = (uint16_t)y;
     }
@@ -605,39 +608,60 @@ DecodePlan decode_plan(int64_t k, int64_t n, int cus) {
   return {8, (int)(sp / 2)};
 }
 
-template <bool kA16, int kDW, bool kOne, int kFuse = 0>
+template <bool kA16, int kDW, bool kOne, int kFuse, bool kEpi>
 void launch_decode_t(dim3 grid, hipStream_t s, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                      int64_t k, const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, const float* gsf_a,
-                     const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, int splits,
-                     float* partial, const uint16_t* x16, float* gsf_dst) {
-  hipLaunchKernelGGL((gemm_decode_kernel<kA16, kDW, kOne, kFuse>), grid, dim3(64 * kDW), 0, s, a_codes, a_scales, m, k,
-                     b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out, splits, partial, x16,
-                     gsf_dst);
+                     const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out,
+                     int splits, float* partial, const uint16_t* x16, float* gsf_dst) {
+  hipLaunchKernelGGL((gemm_decode_kernel<kA16, kDW, kOne, kFuse, kEpi>), grid, dim3(64 * kDW), 0, s, a_codes, a_scales,
+                     m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits, partial, x16,
+                     gsf_dst, ep);
+}
+
+// The decode kernels with or without the epilogue: [activation form][one row][eight waves];
+// the fused forms, [dynamic][eight waves], are one-row fp16 only.
+using DecodeLaunch = decltype(&launch_decode_t<false, 4, false, 0, false>);
+template <bool kEpi>
+DecodeLaunch decode_launch(bool a16, int fuse, bool one, int w8) {
+  static constexpr DecodeLaunch kForms[2][2][2] = {
+      {{launch_decode_t<false, 4, false, 0, kEpi>, launch_decode_t<false, 8, false, 0, kEpi>},
+       {launch_decode_t<false, 4, true, 0, kEpi>, launch_decode_t<false, 8, true, 0, kEpi>}},
+      {{launch_decode_t<true, 4, false, 0, kEpi>, launch_decode_t<true, 8, false, 0, kEpi>},
+       {launch_decode_t<true, 4, true, 0, kEpi>, launch_decode_t<true, 8, true, 0, kEpi>}}};
+  static constexpr DecodeLaunch kFused[2][2] = {
+      {launch_decode_t<true, 4, true, kFuseStatic, kEpi>, launch_decode_t<true, 8, true, kFuseStatic, kEpi>},
+      {launch_decode_t<true, 4, true, kFuseDynamic, kEpi>, launch_decode_t<true, 8, true, kFuseDynamic, kEpi>}};
+  return fuse != 0 ? kFused[fuse == kFuseDynamic ? 1 : 0][w8] : kForms[a16 ? 1 : 0][one ? 1 : 0][w8];
 }
 
 hipError_t launch_decode(bool a16, int fuse, int waves, uint32_t blocks, hipStream_t s, const uint8_t* a_codes,
                          const uint8_t* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
                          const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b,
-                         int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, int splits, float* partial,
-                         const uint16_t* x16, float* gsf_dst = nullptr) {
+                         int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep, uint16_t* out, int splits,
+                         float* partial, const uint16_t* x16, float* gsf_dst = nullptr) {
 #ifndef NVFP4_DECODE_ONE_ROW
 #define NVFP4_DECODE_ONE_ROW 1
 #endif
   const bool one = NVFP4_DECODE_ONE_ROW && m == 1;
-  using Launch = decltype(&launch_decode_t<false, 4, false>);
-  // [activation form][one row][eight waves]; the fused forms are one-row fp16 only
-  static constexpr Launch kPlain[2][2][2] = {
-      {{launch_decode_t<false, 4, false>, launch_decode_t<false, 8, false>},
-       {launch_decode_t<false, 4, true>, launch_decode_t<false, 8, true>}},
-      {{launch_decode_t<true, 4, false>, launch_decode_t<true, 8, false>},
-       {launch_decode_t<true, 4, true>, launch_decode_t<true, 8, true>}}};
-  static constexpr Launch kFused[2][2] = {
-      {launch_decode_t<true, 4, true, kFuseStatic>, launch_decode_t<true, 8, true, kFuseStatic>},
-      {launch_decode_t<true, 4, true, kFuseDynamic>, launch_decode_t<true, 8, true, kFuseDynamic>}};
   const int w8 = waves == 8 ? 1 : 0;
-  const Launch fn = fuse != 0 ? kFused[fuse == kFuseDynamic ? 1 : 0][w8] : kPlain[a16 ? 1 : 0][one ? 1 : 0][w8];
+  // with a K split the reduce applies the epilogue
+  const DecodeLaunch fn =
+      ep.active() && splits == 1 ? decode_launch<true>(a16, fuse, one, w8) : decode_launch<false>(a16, fuse, one, w8);
   fn(dim3(blocks), s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, splits,
      partial, x16, gsf_dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_reduce(const float* partial, int splits, int64_t m, int64_t n, const float* gsf_a,
+                         const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias, const Epilogue& ep,
+                         uint16_t* out, hipStream_t s) {
+  const dim3 grid((uint32_t)((m * n + 255) / 256));
+  if (ep.active())
+    hipLaunchKernelGGL(gemm_skinny_reduce<true>, grid, dim3(256), 0, s, partial, splits, m, n, gsf_a, gsf_b,
+                       a_seg_rows, bias, out, ep);
+  else
+    hipLaunchKernelGGL(gemm_skinny_reduce<false>, grid, dim3(256), 0, s, partial, splits, m, n, gsf_a, gsf_b,
+                       a_seg_rows, bias, out, ep);
   return hipGetLastError();
 }
 
@@ -646,8 +670,13 @@ hipError_t launch_mt(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                      const uint8_t* b_scales, int64_t n, const float* gsf_a, const float* gsf_b, const uint16_t* bias,
                      const Epilogue& ep, int64_t a_seg_rows, uint16_t* out, int splits, float* partial, hipStream_t s) {
   const int64_t groups = (n + kCols - 1) / kCols;
-  hipLaunchKernelGGL((gemm_skinny_kernel<MT>), dim3((uint32_t)(groups * splits)), dim3(256), 0, s, a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep,
-                     ep.active(), out, splits, partial);
+  const dim3 grid((uint32_t)(groups * splits));
+  if (ep.active() && splits == 1)   // with a K split the reduce applies the epilogue
+    hipLaunchKernelGGL((gemm_skinny_kernel<MT, true>), grid, dim3(256), 0, s, a_codes, a_scales, m, k, b_codes,
+                       b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits, partial, ep);
+  else
+    hipLaunchKernelGGL((gemm_skinny_kernel<MT, false>), grid, dim3(256), 0, s, a_codes, a_scales, m, k, b_codes,
+                       b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, out, splits, partial, ep);
   return hipGetLastError();
 }
 
@@ -687,10 +716,7 @@ hipError_t launch_gemm_skinny(const uint8_t* a_codes, const uint8_t* a_scales, i
     e = launch_mt<8>(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, bias, ep, a_seg_rows, out, splits, partial, s);
   }
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t total = m * n;
-  hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s, partial, splits, m,
-                     n, gsf_a, gsf_b, a_seg_rows, bias, ep, ep.active(), out);
-  return hipGetLastError();
+  return launch_reduce(partial, splits, m, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out, s);
 }
 
 bool gemm_decode_a16_supported(int64_t m, int64_t k, const void* a16, const void* b_codes, const void* b_scales) {
@@ -711,10 +737,7 @@ hipError_t launch_gemm_decode_a16(const uint16_t* a16, int64_t m, int64_t k, con
   hipError_t e = launch_decode(true, 0, plan.waves, (uint32_t)(tiles * splits), s, nullptr, nullptr, m, k,
                                b_codes, b_scales, n, gsf_a, gsf_b, 0, bias, ep, out, splits, partial, a16);
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t total = m * n;
-  hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s, partial, splits, m,
-                     n, gsf_a, gsf_b, (int64_t)0, bias, ep, ep.active(), out);
-  return hipGetLastError();
+  return launch_reduce(partial, splits, m, n, gsf_a, gsf_b, 0, bias, ep, out, s);
 }
 
 namespace {
@@ -757,9 +780,7 @@ hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_
   hipError_t e = launch_decode(true, gsf_x != nullptr ? kFuseStatic : kFuseDynamic, waves, (uint32_t)(tiles * splits), s, nullptr, nullptr, 1, k, b_codes,
                                b_scales, n, gsf_x, gsf_w, 0, bias, ep, out, splits, partial, x, gsf_used);
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(gemm_skinny_reduce, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, partial, splits,
-                     (int64_t)1, n, gsf_x != nullptr ? gsf_x : gsf_used, gsf_w, (int64_t)0, bias, ep, ep.active(), out);
-  return hipGetLastError();
+  return launch_reduce(partial, splits, 1, n, gsf_x != nullptr ? gsf_x : gsf_used, gsf_w, 0, bias, ep, out, s);
 }
 
 }  // namespace nvfp4
