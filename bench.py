@@ -72,7 +72,7 @@ def parse():
 
 # The sources that decide which kernels one step runs and what they do: the GEMM
 # dispatch, the pipelined GEMM, the quantize kernels and their device code.
-STEP_SOURCES = ("gemm.hip", "gemm_pipe.hip", "quantize.hip", "gemm_common.h", "nvfp4_device.h")
+STEP_SOURCES = ("gemm.hip", "gemm_pipe.hip", "quantize.hip", "quantize_device.h", "gemm_common.h", "nvfp4_device.h")
 
 
 def kernel_source_digest() -> str:

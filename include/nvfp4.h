@@ -82,7 +82,8 @@ enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_GEL
  *   - every array of the RMS norm, checkpoint and gradient calls: 16 bytes, except fp32
  *     scalars and the norm's grad_w (4), checkpoint scales (bytes: any address), and the
  *     residual and preact of a linear's epilogue (2).
- * The scale-layout converters access bytes and need no alignment. */
+ * The scale-layout converters access bytes and need no alignment.
+ * Outputs overlap neither each other nor inputs, except where a call says so. */
 
 /* Bytes of a block-scale array for a [rows, k] tensor in the layout above. */
 size_t nvfp4_scale_bytes(int64_t rows, int64_t k);
@@ -340,7 +341,7 @@ int nvfp4_gemm_epilogue(const uint8_t* x_codes_dev, const uint8_t* x_scale_dev, 
  * in the residual's type; it may be residual_dev, or x_dev of that type (unused without a
  * residual).  y_dev bf16 [rows][k].  ck_codes_dev / ck_scales_dev: both NULL, or y's 8-bit
  * checkpoint (nvfp4_checkpoint_pack of y_dev, bit for bit).  k: a multiple of 16, at most
- * NVFP4_NORM_MAX_K.  eps >= 0.
+ * NVFP4_NORM_MAX_K.  eps >= 0 (a zero row with eps 0 is 0 * infinity, NaN).
  */
 int nvfp4_rmsnorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
                   const void* weight_dev, int weight_dtype, int64_t rows, int64_t k, float eps,
@@ -383,7 +384,8 @@ int nvfp4_rmsnorm_backward(const void* grad_y_dev, const void* r_dev, int r_dtyp
  * 16); value = code * 2^(s - 127), exact in bf16.  2^(s - 127) is the smallest power of
  * two, from 2^-110 to 2^120, that brings the block's largest finite magnitude to 448 or
  * below; codes round to nearest even, so a value moves by at most 2^-4 of itself (or 2^-10
- * of 2^(s - 127), if that is more).  Infinities and NaN become NaN.
+ * of 2^(s - 127), if that is more; magnitudes from 248 * 2^120 = 3.3e38 up unpack to
+ * infinity).  Infinities and NaN become NaN.
  * nvfp4_checkpoint_pack: x_dev bf16; rotation_group as for nvfp4_quantize_activation (the
  * checkpoint holds the rotated, bf16-rounded values).  k: a multiple of 16.
  * nvfp4_checkpoint_unpack: the values, to bf16 or fp32 [rows][k].

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import check, lib
 from .nvfp4 import (DTYPE_CODES, _activation_code, _gate_up, _on_device, _ptr, _require_device, _stream)
@@ -34,13 +35,13 @@ def _scale_columns(k: int) -> int:
     return (k + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
 
 
-def _rows(name: str, t: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> tuple[torch.Tensor, int, int]:
-    """``t`` [..., K] as contiguous 16-byte aligned rows on a GPU (copied where its strides or
-    address differ), with the number of rows and K."""
+def _rows(name: str, t: torch.Tensor, dtype: torch.dtype | None = torch.bfloat16) -> tuple[torch.Tensor, int, int]:
+    """``t`` [..., K] of ``dtype`` (None: bf16 or fp32) as contiguous 16-byte aligned rows on a
+    GPU (copied where its strides or address differ), with the number of rows and K."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dtype != dtype and (dtype is not None or t.dtype not in DTYPE_CODES):
+        raise ValueError(f"{name} must be {dtype or 'bf16 or fp32'}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device, got {t.device}")
     if t.dim() < 1:
@@ -191,6 +192,7 @@ class _SwiGLUFn(torch.autograd.Function):
         return x
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_x):
         if ctx.packed:
             gc, gs, uc, us = ctx.saved_tensors

@@ -3,6 +3,7 @@ output as bf16, with an 8-bit checkpoint, or as the NVFP4 codes the linears take
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import check, lib
 from .checkpoint import Checkpoint, _empty_checkpoint, _rows
@@ -12,50 +13,43 @@ from .nvfp4 import (DTYPE_CODES, _on_device, _ptr, _require_device, _scalar_f32,
 NORM_MAX_K = 16384
 
 
-def _stream_rows(name: str, t: torch.Tensor) -> tuple[torch.Tensor, int, int]:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in DTYPE_CODES:
-        raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    return _rows(name, t, t.dtype)
-
-
 def _weight(weight: torch.Tensor, k: int, device: torch.device) -> torch.Tensor:
-    w, rows, n = _stream_rows("weight", weight)
+    w, rows, n = _rows("weight", weight, None)
     if n != k or rows != 1 or w.dim() != 1:
         raise ValueError(f"weight must be bf16 or fp32 [{k}], got {weight.dtype} {list(weight.shape)}")
-    _require_device(device, weight=w)
+    if w.device != device:
+        raise ValueError(f"weight must be on {device}, got {w.device}")
     return w
 
 
-class _Inputs:
-    """The checked inputs of one norm call, in the order of the C calls' first arguments."""
-
-    def __init__(self, x, weight, eps, residual):
-        self.x, self.rows, self.k = _stream_rows("x", x)
-        self.w = _weight(weight, self.k, x.device)
-        self.res = self.out = None
-        if residual is not None:
-            self.res, _, _ = _stream_rows("residual", residual)
-            _require_device(x.device, residual=residual)
-            if residual.shape != x.shape:
-                raise ValueError(f"x and residual must have the same shape, got {list(x.shape)} and "
-                                 f"{list(residual.shape)}")
-            if x.dtype == torch.float32 and residual.dtype != torch.float32:
-                raise ValueError("an fp32 x needs an fp32 residual")
-            self.out = x.new_empty(x.shape, dtype=self.res.dtype)
-        self.args = (_ptr(self.x), DTYPE_CODES[x.dtype], _ptr(self.res),
-                     DTYPE_CODES[x.dtype if self.res is None else self.res.dtype], _ptr(self.w),
-                     DTYPE_CODES[self.w.dtype], self.rows, self.k, float(eps))
+def _inputs(x, weight, eps, residual):
+    """The checked inputs of one norm call in the order of the C calls' first arguments, the
+    tensors behind them (which may be copies), r's tensor (None without a residual), rows, K."""
+    x2, rows, k = _rows("x", x, None)
+    w = _weight(weight, k, x.device)
+    xd = rd = DTYPE_CODES[x.dtype]
+    r2 = out = None
+    if residual is not None:
+        r2, _, _ = _rows("residual", residual, None)
+        if r2.device != x.device:
+            raise ValueError(f"residual must be on {x.device}, got {r2.device}")
+        if residual.shape != x.shape:
+            raise ValueError(f"x and residual must have the same shape, got {list(x.shape)} and {list(residual.shape)}")
+        if x.dtype == torch.float32 and residual.dtype != torch.float32:
+            raise ValueError("an fp32 x needs an fp32 residual")
+        rd = DTYPE_CODES[residual.dtype]
+        out = x.new_empty(x.shape, dtype=residual.dtype)
+    args = (x2.data_ptr(), xd, _ptr(r2), rd, w.data_ptr(), DTYPE_CODES[w.dtype], rows, k, float(eps))
+    return args, (x2, r2, w), out, rows, k
 
 
 def _rmsnorm(x, weight, eps, residual, packed: bool):
-    a = _Inputs(x, weight, eps, residual)
+    args, _held, r, _, _ = _inputs(x, weight, eps, residual)
     y = x.new_empty(x.shape, dtype=torch.bfloat16)
     ck = _empty_checkpoint(x) if packed else None
-    check(lib().nvfp4_rmsnorm(*a.args, _ptr(a.out), _ptr(y), _ptr(ck.codes) if ck else None,
-                              _ptr(ck.scales) if ck else None, _stream(x.device)))
-    return y, a.out, ck
+    check(lib().nvfp4_rmsnorm(*args, _ptr(r), y.data_ptr(), ck.codes.data_ptr() if ck else None,
+                              ck.scales.data_ptr() if ck else None, _stream(x.device)))
+    return y, r, ck
 
 
 @_on_device
@@ -82,21 +76,24 @@ def quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     """quantize_activation(rmsnorm(x)) without writing the normed tensor: codes uint8
     [rows, K/2], scales (library layout) and the global scale, as :func:`nvfp4_gemm` takes
     them; with ``residual`` also r.  ``global_sf_x=None``: dynamic scale."""
-    a = _Inputs(x, weight, eps, residual)
+    args, _held, r, rows, k = _inputs(x, weight, eps, residual)
     dev = x.device
-    codes = x.new_empty((a.rows, a.k // 2), dtype=torch.uint8)
-    scales = x.new_empty((scale_bytes(a.rows, a.k),), dtype=torch.uint8)
+    codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
+    scales = x.new_empty((scale_bytes(rows, k),), dtype=torch.uint8)
     gsf = x.new_empty((), dtype=torch.float32)
-    g = None if global_sf_x is None else _scalar_f32(global_sf_x, dev)
-    _require_device(dev, global_sf_x=g)
-    if a.rows == 0:
+    g, ws, need = None, None, 0
+    if global_sf_x is not None:
+        g = _scalar_f32(global_sf_x, dev)
+        _require_device(dev, global_sf_x=g)
+    else:
+        need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(rows)
+        ws = x.new_empty((need,), dtype=torch.uint8) if need else None
+    if rows == 0:
         # nothing is launched: the scale is the given one, or that of an abs-max of 0
         gsf.copy_(static_global_sf(torch.zeros_like(gsf)) if g is None else g.reshape(()))
-    need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(a.rows) if g is None else 0
-    ws = x.new_empty((need,), dtype=torch.uint8) if need else None
-    check(lib().nvfp4_quantize_rmsnorm(*a.args, _ptr(g), _ptr(a.out), _ptr(codes), _ptr(scales), _ptr(gsf), _ptr(ws),
-                                       need, _stream(dev)))
-    return (codes, scales, gsf) if residual is None else (codes, scales, gsf, a.out)
+    check(lib().nvfp4_quantize_rmsnorm(*args, _ptr(g), _ptr(r), codes.data_ptr(), scales.data_ptr(), gsf.data_ptr(),
+                                       _ptr(ws), need, _stream(dev)))
+    return (codes, scales, gsf) if residual is None else (codes, scales, gsf, r)
 
 
 @_on_device
@@ -106,7 +103,7 @@ def rmsnorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor
     gradient of x and of the residual alike; grad_weight fp32 [K]).  ``grad_residual``: the
     gradient that reaches r along the residual stream, of r's dtype, added to grad_r."""
     gy, *gm = _rows("grad_y", grad_y)
-    r2, rows, k = _stream_rows("r", r)
+    r2, rows, k = _rows("r", r, None)
     _require_device(gy.device, r=r, grad_residual=grad_residual)
     if gm != [rows, k]:
         raise ValueError(f"grad_y and r must have the same shape, got {list(grad_y.shape)} and {list(r.shape)}")
@@ -144,6 +141,7 @@ class _RMSNormFn(torch.autograd.Function):
         return (y, r, *extra)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y, grad_r, _codes, _scales):
         r, weight = ctx.saved_tensors
         if grad_y is None:

@@ -630,7 +630,8 @@ def nvfp4_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     checkpoint packed here; a :class:`Checkpoint` of ``x`` (from :func:`rmsnorm_train` or
     :func:`checkpoint_pack` with this rotation group) is shared, so several linears on one
     input keep it once.  grad_W is then taken at the checkpoint's values.  ``activation``
-    and ``residual`` (bf16, gets its gradient too): the epilogue of :func:`nvfp4_linear`."""
+    and ``residual`` (bf16, gets its gradient too): the epilogue of :func:`nvfp4_linear`; the
+    activation's gradient is taken at the kept z, in bf16, or in 8 bits with a checkpoint."""
     from . import checkpoint as ck
     x = x.to(torch.bfloat16)
     if x.dim() < 1 or not x.is_contiguous():
@@ -643,10 +644,12 @@ def nvfp4_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
         held = ck.checkpoint_pack(x.detach(), group) if checkpoint is True else checkpoint
         if not isinstance(held, ck.Checkpoint):
             raise TypeError("checkpoint must be None, True or a Checkpoint")
-        if held.rotation_group != group or held.codes.numel() != x.numel() or held.codes.shape[-1] != x.shape[-1]:
+        codes, scales, rows, k = ck._saved("checkpoint", held)
+        _require_device(x.device, checkpoint=codes)
+        if held.rotation_group != group or rows * k != x.numel() or k != x.shape[-1]:
             raise ValueError(f"checkpoint holds {list(held.codes.shape)} under rotation group {held.rotation_group}; "
                              f"the linear's input is {list(x.shape)} under {group}")
-        saved = (held.codes.reshape(-1, x.shape[-1]), held.scales.reshape(-1, held.scales.shape[-1]))
+        saved = (codes.reshape(rows, k), scales.reshape(rows, scales.shape[-1]))
     return _NVFP4STEFn.apply(x, weight, bias, gx, group, saved, activation, residual)
 
 
