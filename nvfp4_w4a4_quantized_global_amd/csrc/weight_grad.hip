@@ -77,8 +77,8 @@ constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer here
 constexpr int64_t kBufferWidth = 1 << 24;    // columns up to which a step's rows fit 31-bit offsets
 
 // One 16-byte global -> LDS copy per lane; the address is a wave-uniform LDS base plus
-// 16 bytes a lane.  Inline asm so that the compiler does not hold LDS reads back for it:
-// step_barrier waits for it.
+// 16 bytes a lane.  Inline asm so that the compiler does not hold LDS reads back for it: the
+// loop waits for it before the barrier that precedes them.
 __device__ __forceinline__ void copy16_to_lds(u32x4_t rsrc, uint32_t offset, uint8_t* dst) {
   asm volatile("buffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(offset), "s"(rsrc) : "memory");
@@ -90,7 +90,12 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Scheduling of one sub-step: kN times an MFMA, kReads LDS reads and some vector work.
+// A barrier for panels whose copies each wave has waited for already.
+__device__ __forceinline__ void panel_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Scheduling of a group of MFMAs: kN times an MFMA, kReads LDS reads and some vector work.
 template <int kN, int kReads>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
@@ -169,26 +174,22 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(const
     const int64_t col = n0 + 8 * swz(r, cchunk);
     goff[i] = col < n ? (uint32_t)((r * n + col) * 2) : kOutside;
   }
-  auto stage_gy = [&](int64_t s) {
+  auto stage_gy = [&](int64_t s, int i) {
     uint8_t* dst = panel_a(s);
     if constexpr (kAligned) {
-      const u32x4_t rs = buffer_of(gy + s * kStep * n, step_bytes(s, 2 * n));
-#pragma unroll
-      for (int i = 0; i < 2 * kT; ++i) copy16_to_lds(rs, goff[i], dst + (2 * kT * wave + i) * 1024);
+      copy16_to_lds(buffer_of(gy + s * kStep * n, step_bytes(s, 2 * n)), goff[i], dst + (2 * kT * wave + i) * 1024);
     } else {
-      for (int i = t; i < kStep * G::kRowChunks; i += 256) {
-        const int r = i / G::kRowChunks, c = i % G::kRowChunks;
-        const int64_t row = s * kStep + r;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (s < s_end && row < m) {
+      const int r = (256 * i + t) / G::kRowChunks, c = t % G::kRowChunks;
+      const int64_t row = s * kStep + r;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (s < s_end && row < m) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int64_t col = n0 + 8 * c + e;
-            if (col < n) w[e >> 1] |= (uint32_t)gy[row * n + col] << (16 * (e & 1));
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int64_t col = n0 + 8 * c + e;
+          if (col < n) w[e >> 1] |= (uint32_t)gy[row * n + col] << (16 * (e & 1));
         }
-        *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
   // codes: thread t takes one 16-value chunk of rows xrow + kXRows i
@@ -203,36 +204,24 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(const
   }
   u32x4_t xc[kT];
   uint32_t xs[kT];
-  auto load_x = [&](int64_t s) {
+  auto load_x = [&](int64_t s, int i) {
     if constexpr (kAligned) {
-      const auto rc = rsrc_of(codes + s * kStep * k, step_bytes(s, k));
-      const auto rs = rsrc_of(scales + s * kStep * kb, step_bytes(s, kb));
-#pragma unroll
-      for (int i = 0; i < kT; ++i) {
-        xc[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)xoff[i], 0, 0);
-        xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)soff[i], 0, 0);
-      }
+      xc[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_of(codes + s * kStep * k, step_bytes(s, k)), (int)xoff[i], 0, 0);
+      xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rsrc_of(scales + s * kStep * kb, step_bytes(s, kb)), (int)soff[i], 0, 0);
     } else {
-#pragma unroll
-      for (int i = 0; i < kT; ++i) {
-        const int64_t row = s * kStep + xrow + G::kXRows * i;
-        const bool in = s < s_end && row < m && xcol < k;
-        xc[i] = in ? *reinterpret_cast<const u32x4_t*>(codes + row * k + xcol) : u32x4_t{0, 0, 0, 0};
-        xs[i] = in ? scales[row * kb + (xcol >> 5)] : 0u;
-      }
+      const int64_t row = s * kStep + xrow + G::kXRows * i;
+      const bool in = s < s_end && row < m && xcol < k;
+      xc[i] = in ? *reinterpret_cast<const u32x4_t*>(codes + row * k + xcol) : u32x4_t{0, 0, 0, 0};
+      xs[i] = in ? scales[row * kb + (xcol >> 5)] : 0u;
     }
   };
-  auto store_x = [&](int64_t s) {
+  auto store_x = [&](int64_t s, int i) {
     uint8_t* dst = panel_b(s);
-#pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      const int r = xrow + G::kXRows * i;
-      uint4 o[2];
-      expand16(xc[i], pow2f((int)xs[i] - 127), o);
-      const int c = 2 * xchunk;
-      *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c) * 16) = o[0];
-      *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c + 1) * 16) = o[1];
-    }
+    const int r = xrow + G::kXRows * i, c = 2 * xchunk;
+    uint4 o[2];
+    expand16(xc[i], pow2f((int)xs[i] - 127), o);
+    *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c) * 16) = o[0];
+    *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz_x(r, c + 1) * 16) = o[1];
   };
 
   // Fragment reads.  The 16 lanes of a group together address four rows of 16 columns (lane
@@ -258,49 +247,67 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(const
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  auto load_fragments = [&](int64_t s, int sub, bf16x8_t (&fa)[kT], bf16x8_t (&fb)[kT]) {
-#pragma unroll
-    for (int i = 0; i < kT; ++i) fa[i] = fragment(panel_a(s), kT * wn + i, sub, 0);
-#pragma unroll
-    for (int j = 0; j < kT; ++j) fb[j] = fragment(panel_b(s), kT * wk + j, sub, ((kT * wk + j) >> 1) & 1);
+  auto load_fragments = [&](int64_t s, int sub, int i, bf16x8_t (&fa)[kT], bf16x8_t (&fb)[kT]) {
+    fa[i] = fragment(panel_a(s), kT * wn + i, sub, 0);
+    fb[i] = fragment(panel_b(s), kT * wk + i, sub, ((kT * wk + i) >> 1) & 1);
   };
-  auto multiply = [&](const bf16x8_t (&fa)[kT], const bf16x8_t (&fb)[kT]) {
+  // One sub-step: the MFMAs of fragments fa, fb in kT groups; group i first does fill(i) and
+  // loads part i of the fragments of sub-step `sub` of step s.
+  auto sub_step = [&](const bf16x8_t (&fa)[kT], const bf16x8_t (&fb)[kT], int64_t s, int sub, bf16x8_t (&next_a)[kT],
+                      bf16x8_t (&next_b)[kT], auto fill) {
 #pragma unroll
-    for (int i = 0; i < kT; ++i)
+    for (int i = 0; i < kT; ++i) {
+      fill(i);
+      load_fragments(s, sub, i, next_a, next_b);
 #pragma unroll
       for (int j = 0; j < kT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      interleave<kT, 4 / kT>();
+    }
   };
 
   // Four sub-steps of 16 rows per step; each reads the fragments of the next while its own
   // MFMAs run.  The barrier stands before the last: by then this step's panels are read
-  // (their last fragments are in registers) and the next step's are complete, so the loads
+  // (their last fragments are in registers) and the next step's are complete, so the copies
   // of the step after that start into the freed panels.
+  //
+  // Codes are loaded, and gy is copied, about a step before they are waited for; the one wait
+  // for both stands in the middle of the third sub-step, as late as the LDS writes of the expanded codes allow, and each load is issued
+  // between two groups of MFMAs.  (4096 rows, 25600 x 5120: with the wait in the second
+  // sub-step and all loads together behind the barrier 960 us, so 897; of zeros, where the
+  // clock does not fall under the power of the MFMAs, 890 and 766.)
+  constexpr int kMid = kT / 2;
+  const auto nothing = [](int) {};
   bf16x8_t fa[2][kT], fb[2][kT];
-  stage_gy(s_begin);
-  load_x(s_begin);
-  store_x(s_begin);
-  stage_gy(s_begin + 1);
-  load_x(s_begin + 1);
+#pragma unroll
+  for (int i = 0; i < kT; ++i) load_x(s_begin, i);
+#pragma unroll
+  for (int i = 0; i < 2 * kT; ++i) stage_gy(s_begin, i);
+#pragma unroll
+  for (int i = 0; i < kT; ++i) store_x(s_begin, i);
+#pragma unroll
+  for (int i = 0; i < kT; ++i) load_x(s_begin + 1, i);
+#pragma unroll
+  for (int i = 0; i < 2 * kT; ++i) stage_gy(s_begin + 1, i);
   step_barrier();
-  load_fragments(s_begin, 0, fa[0], fb[0]);
+#pragma unroll
+  for (int i = 0; i < kT; ++i) load_fragments(s_begin, 0, i, fa[0], fb[0]);
 #pragma clang loop unroll(disable)
   for (int64_t s = s_begin; s < s_end; ++s) {
-    load_fragments(s, 1, fa[1], fb[1]);
-    multiply(fa[0], fb[0]);
-    interleave<kT * kT, 4 / kT>();
-    load_fragments(s, 2, fa[0], fb[0]);
-    store_x(s + 1);
-    multiply(fa[1], fb[1]);
-    interleave<kT * kT, 4 / kT>();
-    load_fragments(s, 3, fa[1], fb[1]);
-    multiply(fa[0], fb[0]);
-    interleave<kT * kT, 4 / kT>();
-    step_barrier();
-    stage_gy(s + 2);
-    load_x(s + 2);
-    load_fragments(s + 1, 0, fa[0], fb[0]);
-    multiply(fa[1], fb[1]);
-    interleave<kT * kT, 4 / kT>();
+    sub_step(fa[0], fb[0], s, 1, fa[1], fb[1], nothing);
+    sub_step(fa[1], fb[1], s, 2, fa[0], fb[0], nothing);
+    sub_step(fa[0], fb[0], s, 3, fa[1], fb[1], [&](int i) {
+      if (i < kMid) return;
+      if (i == kMid) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int j = 2 * (i - kMid); j < 2 * (i - kMid) + 2; ++j) store_x(s + 1, j);
+#pragma unroll
+      for (int j = 2 * (i - kMid); j < 2 * (i - kMid) + 2; ++j) load_x(s + 2, j);
+    });
+    panel_barrier();
+    sub_step(fa[1], fb[1], s + 1, 0, fa[0], fb[0], [&](int i) {
+      stage_gy(s + 2, i);
+      stage_gy(s + 2, kT + i);
+    });
   }
   step_barrier();   // no copy still landing in LDS
 
@@ -380,16 +387,16 @@ __global__ void __launch_bounds__(256) weight_grad_reduce(const float* __restric
 //
 // A round of large tiles (one per compute unit) takes about 5/3 of a round of small ones
 // (two per compute unit, half the work), so the sizes are weighed by their whole rounds
-// (measured, 4096 rows, large against small: 5120 x 5120, 2 rounds against 4, 210 us against
-// 250; 3328 x 5120, 2 against 3, 208 against 186; 8192 x 5120, 3 against 5, 317 against 360;
+// (measured, 4096 rows, large against small: 5120 x 5120, 2 rounds against 4, 200 us against
+// 232; 3328 x 5120, 2 against 3, 198 against 173; 8192 x 5120, 3 against 5, 311 against 350;
 // 777 rows, 1024 x 5120, 1 against 1, 29 against 19).
 //
 // A small tile's rows are split across workgroups while there are fewer tiles than compute
 // units, each split four steps long at least: the partials (4 bytes a value and split,
 // written and read again) cost more than idle slots beyond that (777 rows, 1024 x 5120, 320
-// tiles: unsplit 19 us, two ways 33; 4096 rows, 64 x 5120, 40 tiles: unsplit 50, six ways
-// 17.5, twelve 18.4).  Splits that stay 32 steps long fill the second slot of each compute
-// unit too (16384 rows, 1024 x 1024: four ways 59 us, eight 48).
+// tiles: unsplit 19 us, two ways 31; 4096 rows, 64 x 5120, 40 tiles: unsplit 41, six ways
+// 16.3, twelve 18).  Splits that stay 32 steps long fill the second slot of each compute
+// unit too (16384 rows, 1024 x 1024: four ways 51 us, eight 46.5).
 struct Plan {
   int t, splits;
 };
