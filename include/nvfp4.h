@@ -315,8 +315,10 @@ int nvfp4_dequantize(const uint8_t* packed_dev, const uint8_t* scale_dev, int64_
  * activation: NVFP4_ACT_*.  residual_dev: bf16 [m][out_features], NULL for none; it may be
  * out_dev itself (the update in place of a residual stream), but not overlap it otherwise.
  * preact_dev: NULL, or bf16 [m][out_features] that receives bf16(z) (where
- * nvfp4_activation_backward takes the derivative); it overlaps neither.  up_dev: NULL, or the input is the SwiGLU product of
- * x_dev (gate) and up_dev as in nvfp4_linear_swiglu (rotation_group 0).  workspace: that of nvfp4_linear, or of nvfp4_linear_swiglu with up_dev.
+ * nvfp4_activation_backward takes the derivative); it overlaps neither.
+ * up_dev: NULL, or the input is the SwiGLU product of x_dev (gate) and up_dev as in
+ * nvfp4_linear_swiglu (rotation_group 0).
+ * workspace: that of nvfp4_linear, or of nvfp4_linear_swiglu with up_dev.
  */
 int nvfp4_linear_epilogue(const void* x_dev, const void* up_dev, int64_t m, int64_t k,
                           const uint8_t* packed_dev, const uint8_t* inv_scale_dev, const float* global_sf_w_dev,

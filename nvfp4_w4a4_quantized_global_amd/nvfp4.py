@@ -13,6 +13,7 @@ import contextlib
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import check, lib
@@ -188,7 +189,8 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
                residual: torch.Tensor | None = None, preact: torch.Tensor | None = None) -> torch.Tensor:
     """Block-scaled GEMM on already quantized activations; bf16 [M, N].
 
-    ``activation``, ``residual`` and ``preact``: the epilogue of :func:`nvfp4_linear`.  With ``split_k`` (default) a workspace of gemm_workspace_bytes is used (allocated
+    ``activation``, ``residual`` and ``preact``: the epilogue of :func:`nvfp4_linear`.
+    With ``split_k`` (default) a workspace of gemm_workspace_bytes is used (allocated
     here if not given) so the last partial round of tiles is split along K."""
     _require_cuda("x_codes", x_codes, torch.uint8, 2)
     _require_cuda("packed", packed, torch.uint8, 2)
@@ -219,7 +221,8 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         workspace = None
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias)
+        _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias,
+                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, out)
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
@@ -275,17 +278,18 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         out = x2d.new_empty((m, out_features))
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias)
+        _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias,
+                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, out_features, x.device, residual, preact, out)
         check(lib().nvfp4_linear_epilogue(_ptr(x2d), None, m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
                                           _stream(x.device)))
-        return out if x.dim() == 2 else out.reshape(*orig[:-1], out_features)
+        return out if out.dim() == x.dim() == 2 else out.reshape(*orig[:-1], out_features)
     check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
                              _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
                              _stream(x.device)))
-    return out if x.dim() == 2 else out.reshape(*orig[:-1], out_features)
+    return out if out.dim() == x.dim() == 2 else out.reshape(*orig[:-1], out_features)
 
 
 def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor, global_sf_w: torch.Tensor,
@@ -411,7 +415,8 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=gate.device)
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias)
+        _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias,
+                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, out)
         check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
@@ -578,6 +583,7 @@ class _NVFP4STEFn(torch.autograd.Function):
         ctx.save_for_backward(x, weight, z, x_scales, z_scales)
         ctx.group = group
         ctx.activation = activation
+        ctx.packed_input = saved is not None
         ctx.res_shape = None if residual is None else residual.shape
         ctx.has_bias = bias is not None
         ctx.bias_dtype = None if bias is None else bias.dtype
@@ -585,9 +591,16 @@ class _NVFP4STEFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y: torch.Tensor):
+        # the library's gradient kernels have no derivatives of their own
+        if ctx.activation is not None or ctx.packed_input:
+            return _NVFP4STEFn._once(ctx, grad_y)
+        return _NVFP4STEFn._gradients(ctx, grad_y)
+
+    @staticmethod
+    def _gradients(ctx, grad_y: torch.Tensor):
         from . import checkpoint as ck
         x, weight, z, x_scales, z_scales = ctx.saved_tensors
-        packed_input = x_scales is not None
+        packed_input = ctx.packed_input
         n, k = weight.shape
         g = ctx.group
         grad_r = grad_y.reshape(ctx.res_shape) if ctx.needs_input_grad[7] else None
@@ -615,7 +628,10 @@ class _NVFP4STEFn(torch.autograd.Function):
             grad_b = gy.sum(0).to(ctx.bias_dtype)
         return grad_x, grad_w, grad_b, None, None, None, None, grad_r
 
+    _once = staticmethod(once_differentiable(_gradients.__func__))
 
+
+@_on_device
 def nvfp4_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, global_sf_x=None,
                        rotation_group: int = 0, checkpoint=None, activation: str | None = None,
                        residual: torch.Tensor | None = None) -> torch.Tensor:

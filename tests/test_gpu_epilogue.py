@@ -195,7 +195,8 @@ def test_refusals():
     for kw in ({"activation": "relu"}, {"residual": res.float()}, {"residual": res[:2]}, {"residual": res.view(n, m)},
                {"residual": res.cpu()}, {"preact": torch.empty((m, n), device=DEV)},
                {"preact": torch.empty((n, m), dtype=BF, device=DEV)}, {"residual": a, "out": c}, {"residual": a, "preact": a},
-               {"preact": a, "out": a}, {"residual": res, "out": torch.empty((n, m), dtype=BF, device=DEV)}):
+               {"preact": a, "out": a}, {"residual": res, "out": torch.empty((n, m), dtype=BF, device=DEV)},
+               {"residual": res, "workspace": torch.empty(1 << 20, dtype=torch.uint8)}):
         with pytest.raises(ValueError):
             lib.nvfp4_linear(x, pk, sc, gw, b, n, g, **kw)
 
@@ -279,6 +280,31 @@ def test_train_shared_checkpoint_block():
     for a, b in zip(g0, g1):
         assert torch.isfinite(b).all()
         assert (a - b).norm() <= 2.0 ** -4 * a.norm() * 2     # at most two checkpoints on the way of a leaf
+
+
+@pytest.mark.parametrize("kw", [{"checkpoint": True}, {"activation": "silu"}])
+def test_train_second_derivative_is_refused(kw):
+    """The gradients of the checkpoint and the activation have no derivatives of their own: a
+    derivative through them raises instead of missing terms.  First derivatives under
+    create_graph stay what they are."""
+    lib = nv()
+    x = workloads.draw("normal", (6, 64), 111, 0).to(DEV).requires_grad_(True)
+    w = workloads.draw("normal", (48, 64), 111, 1).float().to(DEV).requires_grad_(True)
+    ref = torch.autograd.grad(lib.nvfp4_linear_train(x, w, **kw).float().sum(), (x, w))
+    got = torch.autograd.grad(lib.nvfp4_linear_train(x, w, **kw).float().sum(), (x, w), create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    with pytest.raises(RuntimeError):
+        sum(t.float().square().sum() for t in got).backward()
+
+
+def test_flat_out_of_the_linear():
+    """An ``out`` of another shape and as many values comes back in the output's shape."""
+    lib = nv()
+    x, (pk, sc, gw), b, _, _ = _case(20, 256, 96, None)
+    ref = lib.nvfp4_linear(x, pk, sc, gw, b, 96)
+    out = torch.empty(20 * 96, dtype=BF, device=DEV)
+    got = lib.nvfp4_linear(x, pk, sc, gw, b, 96, out=out)
+    assert got.shape == (20, 96) and got.data_ptr() == out.data_ptr() and torch.equal(got, ref)
 
 
 def test_train_checkpoint_mismatch():
