@@ -28,10 +28,11 @@
 // workgroups into fp32 partials that weight_grad_reduce adds in split order.
 //
 // Measured, 4096 rows, 25600 x 5120: 900-990 us, 1.09-1.19 PFLOP/s, by the box.  The matrix
-// cores are busy 57 % of the cycles at a clock that their power holds to 1.6 GHz; the same
-// launch on zeros takes 766 us, 100 of them the 524 MB that the epilogue writes while every
-// compute unit is at the same place, 115 the codes and 50 the copies of gy.  777 rows,
-// 1024 x 5120 in small tiles: 20 us, 13 steps of a memory latency each.
+// cores are busy 57 % of the cycles, at a clock that falls from 1.9 to 1.5 GHz over calls
+// in a row.  The same launch on zeros takes 766 us, 100 of them the 524 MB that the epilogue
+// writes while every compute unit is at the same place, 115 the codes and 50 the copies of
+// gy.  777 rows, 1024 x 5120 in small tiles: 18-21 us, 13.5 of them without any operand
+// loads (launch, 21 MB of output, and LDS reads that match the MFMAs' rate).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
