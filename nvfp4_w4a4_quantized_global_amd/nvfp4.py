@@ -39,7 +39,7 @@ def _stream(device: torch.device) -> int:
 def _require_cuda(name: str, t: torch.Tensor, dtype: torch.dtype | None = None, dim: int | None = None) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device, got {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -78,15 +78,19 @@ def _on_device(fn):
 
 
 def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, out) -> torch.Tensor | None:
-    """Checks a linear's epilogue arguments; returns the residual as a contiguous [m, n]."""
+    """Checks a linear's epilogue arguments (``out``: the caller's, None for a new one);
+    returns the residual as a contiguous [m, n]."""
     if residual is not None:
         if not isinstance(residual, torch.Tensor) or residual.dtype != torch.bfloat16 or residual.numel() != m * n \
-                or residual.shape[-1:] != (n,):
+                or residual.dim() < 1 or residual.shape[-1] != n:
             raise ValueError(f"residual must be bf16 with {m} rows of {n}, got "
                              f"{getattr(residual, 'dtype', None)} {list(getattr(residual, 'shape', []))}")
-        _require_device(device, residual=residual)
+        if residual.device != device:
+            raise ValueError(f"residual must be on {device}, got {residual.device}")
         if not residual.is_contiguous():
             residual = residual.contiguous()
+    if preact is None and out is None:
+        return residual
     for name, t in (("preact", preact), ("out", out)):
         if t is None:
             continue
@@ -209,6 +213,7 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         _require_cuda("bias", bias, torch.bfloat16)
         if bias.numel() != n:
             raise ValueError(f"bias must have {n} elements, got {bias.numel()}")
+    given = out
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x_codes.device)
     ws_bytes = 0
@@ -223,7 +228,7 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
     if act or residual is not None or preact is not None:
         _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, out)
+        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given)
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
                                         _ptr(workspace), ws_bytes, _stream(x_codes.device)))
@@ -274,13 +279,14 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     need = linear_workspace_bytes(m, k, out_features)
     if workspace is None:
         workspace = x2d.new_empty((need,), dtype=torch.uint8)
+    given = out
     if out is None:
         out = x2d.new_empty((m, out_features))
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
         _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, out_features, x.device, residual, preact, out)
+        residual = _epilogue_tensors(m, out_features, x.device, residual, preact, given)
         check(lib().nvfp4_linear_epilogue(_ptr(x2d), None, m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
@@ -411,13 +417,14 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
     if workspace is None:
         need = int(lib().nvfp4_linear_swiglu_workspace_bytes(m, k, out_features))
         workspace = torch.empty((need,), dtype=torch.uint8, device=gate.device)
+    given = out
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=gate.device)
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
         _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, out)
+        residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, given)
         check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
                                           _ptr(workspace), workspace.numel(), _stream(gate.device)))
