@@ -17,7 +17,7 @@
 // (4096 x 5120, bf16 x and fp32 residual to y, r and y's checkpoint: 273 MB in 52 us,
 // 5.3 TB/s; a plain copy of that size reaches 5.2).  A dynamic scale needs the abs-max of
 // all rows before the first code, so its many-row form reads r again in a second pass
-// (4096 x 5120 in bf16: 126 MB in 27.5 us, then 58 MB in 15.5).  One row is one workgroup
+// (4096 x 5120 in bf16: 126 MB in 25 us, then 58 MB in 14.5).  One row is one workgroup
 // and one launch (5120 values: 4.2 us, the launch and two dependent memory accesses).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormForward a) {
 // storing y in the first pass would cost more than forming it twice), then its codes.
 // Eight lanes own a 128-wide tile of a row, as in the quantizer's own pass; the grid is a
 // whole number of rows wide (quantize_blocks), so a lane keeps its tile of the weight and
-// walks down the rows, the next row's load in flight (4096 x 5120: 15.5 us; 1, 2 or 4 tiles
+// walks down the rows, the next row's load in flight (4096 x 5120: 14.5 us; 1, 2 or 4 tiles
 // in flight per lane without the fixed column 15.1-17.7).
 constexpr int kQThreads = 256;
 template <bool kSF32, bool kWF32>
