@@ -654,7 +654,8 @@ def nvfp4_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     :func:`checkpoint_pack` with this rotation group) is shared, so several linears on one
     input keep it once.  grad_W is then taken at the checkpoint's values.  ``activation``
     and ``residual`` (bf16, gets its gradient too): the epilogue of :func:`nvfp4_linear`; the
-    activation's gradient is taken at the kept z, in bf16, or in 8 bits with a checkpoint."""
+    activation's gradient is taken at the kept z, in bf16, or in 8 bits with a checkpoint
+    (where ``out`` is a multiple of 16)."""
     from . import checkpoint as ck
     x = x.to(torch.bfloat16)
     if x.dim() < 1 or not x.is_contiguous():
