@@ -15,12 +15,14 @@
 // kT x kT tiles of v_mfma_f32_32x32x16_bf16: kT = 4 gives 256 x 256 (one wave per SIMD),
 // kT = 2 gives 128 x 128 (two workgroups per compute unit) for products with too few large
 // tiles.  Rows advance in steps of 64 through two LDS stages:
-//   * gy goes global -> LDS directly, 16 bytes a lane;
+//   * gy goes global -> LDS directly, 16 bytes a lane, where its rows are aligned to that;
+//     else through registers in 16-byte loads at any address (777 rows, 1023 x 5120: 23.8 us,
+//     in 2-byte loads 63; 4096 rows, 5121 x 5120: 242 and 1128; 5120 x 5120 aligned: 203);
 //   * codes go through registers: loaded a step ahead, expanded by the hardware's scaled
 //     conversion (one instruction per two values), written to LDS as bf16;
-//   * both come by buffer loads, whose range check supplies zeros for rows and columns past
-//     the end: they add nothing even where gy holds infinities, and the loop carries no
-//     per-lane address arithmetic;
+//   * copies and code loads are buffer loads, whose range check supplies zeros for rows and
+//     columns past the end: they add nothing even where gy holds infinities, and the loop
+//     carries no per-lane address arithmetic;
 //   * a row of a panel is chunks of 16 bytes, chunk c at position c ^ 4 (row % 4) (the
 //     four rows that one transposed read gathers lie in different banks), for x with bit 0
 //     also flipped by bit 3 of c (so that the 32-byte writes of neighbouring lanes do).
@@ -131,9 +133,13 @@ __device__ __forceinline__ void expand16(const u32x4_t& w, float scale, uint4 (&
   o[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// kAligned: rows of gy start on 16-byte boundaries (N a multiple of 8) and a step's rows fit
-// 31-bit offsets; otherwise gy is gathered value by value and addresses are 64-bit.
-template <int kT, bool kAligned, bool kOutBf16>
+// How gy comes:
+//   kCopy    its rows start on 16-byte boundaries (N a multiple of 8): copied to LDS;
+//   kLoad    at least 8 columns: through registers, in 16-byte loads of any alignment;
+//   kGather  value by value: narrower still, no rows, or an N or K whose rows of a step do
+//            not fit the 31-bit offsets of the others.
+enum Gy { kCopy, kLoad, kGather };
+template <int kT, Gy kGy, bool kOutBf16>
 __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
     const uint16_t* __restrict__ gy, int64_t m, int64_t n, const uint8_t* __restrict__ codes,
     const uint8_t* __restrict__ scales, int64_t k, void* __restrict__ out, int tiles_n, int tiles_k, int splits,
@@ -171,18 +177,23 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
     const int64_t rows = s < s_end ? min(m - s * kStep, (int64_t)kStep) : 0;
     return (uint32_t)(rows * width);
   };
-  // gy: instruction i of wave w fills rows (2 kT w + i) kCopyRows .. of the panel
-  const int crow = lane / G::kRowChunks, cchunk = lane % G::kRowChunks;
+  // gy, kCopy: instruction i of wave w fills rows (2 kT w + i) kCopyRows .. of the panel; the
+  // others: chunk 256 i + t of the panel.
   uint32_t goff[2 * kT];
 #pragma unroll
   for (int i = 0; i < 2 * kT; ++i) {
-    const int r = (2 * kT * wave + i) * G::kCopyRows + crow;
-    const int64_t col = n0 + 8 * swz(r, cchunk);
-    goff[i] = col < n ? (uint32_t)((r * n + col) * 2) : kOutside;
+    if constexpr (kGy == kCopy) {
+      const int r = (2 * kT * wave + i) * G::kCopyRows + lane / G::kRowChunks;
+      const int64_t col = n0 + 8 * swz(r, lane % G::kRowChunks);
+      goff[i] = col < n ? (uint32_t)((r * n + col) * 2) : kOutside;
+    } else {
+      const int r = (256 * i + t) / G::kRowChunks;
+      goff[i] = (uint32_t)((r * n + min(n0 + 8 * (t % G::kRowChunks), n - 1)) * 2);
+    }
   }
   auto stage_gy = [&](int64_t s, int i) {
     uint8_t* dst = panel_a(s);
-    if constexpr (kAligned) {
+    if constexpr (kGy == kCopy) {
       copy16_to_lds(buffer_of(gy + s * kStep * n, step_bytes(s, 2 * n)), goff[i], dst + (2 * kT * wave + i) * 1024);
     } else {
       const int r = (256 * i + t) / G::kRowChunks, c = t % G::kRowChunks;
@@ -198,6 +209,33 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
       *reinterpret_cast<uint4*>(dst + r * kRowBytes + swz(r, c) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
+  // kLoad: what follows a row in memory comes along in its last chunk, and chunks past it
+  // repeat it: both meet only columns past the last, which are not written.  Loads that would
+  // pass the tensor's end move back to it; trim_gy shifts what they hold into place and
+  // clears rows past the last.
+  u32x4_t gr[kGy == kLoad ? 2 * kT : 1];
+  auto bytes_left = [&](int64_t s) { return (uint32_t)min((m - s * kStep) * n * 2, (int64_t)0x7FFFFFFF); };
+  auto load_gy = [&](int64_t s, int i) {
+    s = min(s, steps - 1);   // past the last step: loaded, not used
+    __builtin_memcpy(&gr[i], reinterpret_cast<const uint8_t*>(gy + s * kStep * n) + min(goff[i], bytes_left(s) - 16), 16);
+  };
+  auto trim_gy = [&](int64_t s) {
+    const uint32_t left = bytes_left(min(s, steps - 1));
+    if (left >= (uint32_t)kStep * 2 * (uint32_t)n + 16) return;
+#pragma unroll
+    for (int i = 0; i < 2 * kT; ++i) {
+      const uint32_t d = goff[i] - min(goff[i], left - 16);   // bytes moved back
+      const uint64_t lo = gr[i][0] | (uint64_t)gr[i][1] << 32, hi = gr[i][2] | (uint64_t)gr[i][3] << 32;
+      const uint32_t sh = 8 * (d & 7);
+      const uint64_t hs = hi >> sh, ls = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+      const uint64_t a = d < 8 ? ls : d < 16 ? hs : 0, b = d < 8 ? hs : 0;
+      gr[i] = u32x4_t{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+    }
+  };
+  auto store_gy = [&](int64_t s, int i) {
+    const int r = (256 * i + t) / G::kRowChunks, c = t % G::kRowChunks;
+    *reinterpret_cast<u32x4_t*>(panel_a(s) + r * kRowBytes + swz(r, c) * 16) = gr[i];
+  };
   // codes: thread t takes one 16-value chunk of rows xrow + kXRows i
   const int xrow = t / G::kXChunks, xchunk = t % G::kXChunks;
   const int64_t xcol = k0 + 16 * xchunk;
@@ -211,7 +249,7 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
   u32x4_t xc[kT];
   uint32_t xs[kT];
   auto load_x = [&](int64_t s, int i) {
-    if constexpr (kAligned) {
+    if constexpr (kGy != kGather) {
       xc[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_of(codes + s * kStep * k, step_bytes(s, k)), (int)xoff[i], 0, 0);
       xs[i] = __builtin_amdgcn_raw_buffer_load_b8(rsrc_of(scales + s * kStep * kb, step_bytes(s, kb)), (int)soff[i], 0, 0);
     } else {
@@ -285,16 +323,27 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
   constexpr int kMid = kT / 2;
   const auto nothing = [](int) {};
   bf16x8_t fa[2][kT], fb[2][kT];
+  // a step's gy into its panel, or (kLoad) into registers
+  auto fetch_gy = [&](int64_t s) {
+#pragma unroll
+    for (int i = 0; i < 2 * kT; ++i) {
+      if constexpr (kGy == kLoad) load_gy(s, i);
+      else stage_gy(s, i);
+    }
+  };
 #pragma unroll
   for (int i = 0; i < kT; ++i) load_x(s_begin, i);
-#pragma unroll
-  for (int i = 0; i < 2 * kT; ++i) stage_gy(s_begin, i);
+  fetch_gy(s_begin);
 #pragma unroll
   for (int i = 0; i < kT; ++i) store_x(s_begin, i);
+  if constexpr (kGy == kLoad) {
+    trim_gy(s_begin);
+#pragma unroll
+    for (int i = 0; i < 2 * kT; ++i) store_gy(s_begin, i);
+  }
 #pragma unroll
   for (int i = 0; i < kT; ++i) load_x(s_begin + 1, i);
-#pragma unroll
-  for (int i = 0; i < 2 * kT; ++i) stage_gy(s_begin + 1, i);
+  fetch_gy(s_begin + 1);
   step_barrier();
 #pragma unroll
   for (int i = 0; i < kT; ++i) load_fragments(s_begin, 0, i, fa[0], fb[0]);
@@ -304,16 +353,28 @@ __global__ void __launch_bounds__(256, kT == 4 ? 1 : 2) weight_grad_kernel(
     sub_step(fa[1], fb[1], s, 2, fa[0], fb[0], nothing);
     sub_step(fa[0], fb[0], s, 3, fa[1], fb[1], [&](int i) {
       if (i < kMid) return;
-      if (i == kMid) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (i == kMid) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if constexpr (kGy == kLoad) trim_gy(s + 1);
+      }
+      const int h = i - kMid;
 #pragma unroll
-      for (int j = 2 * (i - kMid); j < 2 * (i - kMid) + 2; ++j) store_x(s + 1, j);
+      for (int j = 2 * h; j < 2 * h + 2; ++j) store_x(s + 1, j);
+      if constexpr (kGy == kLoad)
 #pragma unroll
-      for (int j = 2 * (i - kMid); j < 2 * (i - kMid) + 2; ++j) load_x(s + 2, j);
+        for (int j = 4 * h; j < 4 * h + 4; ++j) store_gy(s + 1, j);
+#pragma unroll
+      for (int j = 2 * h; j < 2 * h + 2; ++j) load_x(s + 2, j);
     });
     panel_barrier();
     sub_step(fa[1], fb[1], s + 1, 0, fa[0], fb[0], [&](int i) {
-      stage_gy(s + 2, i);
-      stage_gy(s + 2, kT + i);
+      if constexpr (kGy == kLoad) {
+        load_gy(s + 2, i);
+        load_gy(s + 2, kT + i);
+      } else {
+        stage_gy(s + 2, i);
+        stage_gy(s + 2, kT + i);
+      }
     });
   }
   step_barrier();   // no copy still landing in LDS
@@ -420,17 +481,17 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int cus) {
   return {2, (int)std::max<int64_t>(sp, 1)};
 }
 
-template <int kT, bool kAligned, bool kOutBf16>
+template <int kT, Gy kGy, bool kOutBf16>
 hipError_t launch_t(const uint16_t* gy, int64_t m, int64_t n, const uint8_t* codes, const uint8_t* scales, int64_t k,
                     void* grad_w, int splits, float* partial, hipStream_t s) {
   constexpr int kTile = Geo<kT>::kTile, kLds = Geo<kT>::kLds;
   static bool attr_set[kMaxDevices] = {};
-  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&weight_grad_kernel<kT, kAligned, kOutBf16>), kLds,
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(&weight_grad_kernel<kT, kGy, kOutBf16>), kLds,
                                           attr_set);
       e != hipSuccess)
     return e;
   const int tn = (int)((n + kTile - 1) / kTile), tk = (int)((k + kTile - 1) / kTile);
-  hipLaunchKernelGGL((weight_grad_kernel<kT, kAligned, kOutBf16>), dim3((uint32_t)((int64_t)tn * tk * splits)), dim3(256),
+  hipLaunchKernelGGL((weight_grad_kernel<kT, kGy, kOutBf16>), dim3((uint32_t)((int64_t)tn * tk * splits)), dim3(256),
                      kLds, s, gy, m, n, codes, scales, k, grad_w, tn, tk, splits, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
@@ -453,14 +514,15 @@ hipError_t launch_weight_grad(const uint16_t* gy, int64_t m, int64_t n, const ui
   Plan p = plan_of(m, n, k, cus);
   if (p.splits > 1 && (workspace == nullptr || workspace_bytes < weight_grad_workspace_bytes(m, n, k, cus))) p.splits = 1;
   float* partial = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  using Fn = decltype(&launch_t<4, false, false>);
-  static constexpr Fn f[2][2][2] = {{{launch_t<2, false, false>, launch_t<2, false, true>},
-                                     {launch_t<2, true, false>, launch_t<2, true, true>}},
-                                    {{launch_t<4, false, false>, launch_t<4, false, true>},
-                                     {launch_t<4, true, false>, launch_t<4, true, true>}}};
-  const bool aligned = n % 8 == 0 && n < kBufferWidth && k < kBufferWidth;
-  return f[p.t == 4 ? 1 : 0][aligned ? 1 : 0][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, p.splits, partial,
-                                                                s);
+  using Fn = decltype(&launch_t<4, kCopy, false>);
+  static constexpr Fn f[2][3][2] = {{{launch_t<2, kCopy, false>, launch_t<2, kCopy, true>},
+                                     {launch_t<2, kLoad, false>, launch_t<2, kLoad, true>},
+                                     {launch_t<2, kGather, false>, launch_t<2, kGather, true>}},
+                                    {{launch_t<4, kCopy, false>, launch_t<4, kCopy, true>},
+                                     {launch_t<4, kLoad, false>, launch_t<4, kLoad, true>},
+                                     {launch_t<4, kGather, false>, launch_t<4, kGather, true>}}};
+  const Gy how = m == 0 || n < 8 || n >= kBufferWidth || k >= kBufferWidth ? kGather : n % 8 == 0 ? kCopy : kLoad;
+  return f[p.t == 4 ? 1 : 0][how][out_bf16 ? 1 : 0](gy, m, n, codes, scales, k, grad_w, p.splits, partial, s);
 }
 
 }  // namespace nvfp4

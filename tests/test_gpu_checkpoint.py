@@ -90,6 +90,24 @@ def test_weight_grad(m, n, k, dtype):
     assert torch.equal(nv().weight_grad(gy.to(DEV), ck, dtype), got)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 8, 16), (1, 9, 32), (1, 15, 16), (63, 9, 48), (64, 11, 32), (65, 9, 272), (129, 13, 16),
+                                   (3, 5, 64), (200, 7, 48), (700, 251, 2064), (128, 2047, 5136), (3000, 61, 1024)])
+def test_weight_grad_odd_widths_on_integers(m, n, k):
+    """Rows of grad_y that start anywhere, the last of them ending inside a 16-byte load: small
+    integers, whose sums are exact in any order.  Infinities reach their own output rows only:
+    the first column's next row lies in the last load of each row."""
+    g = torch.Generator().manual_seed(m + n + k)
+    gy = torch.randint(-4, 5, (m, n), generator=g).to(BF).to(DEV)
+    x = torch.randint(1, 4, (m, k), generator=g).to(BF).to(DEV)
+    ck = nv().checkpoint_pack(x)
+    ref = gy.double().t().contiguous() @ x.double()
+    for dtype in (torch.float32, BF):
+        assert torch.equal(nv().weight_grad(gy, ck, dtype), ref.float().to(dtype))
+    gy[:, 0] = float("inf")
+    got = nv().weight_grad(gy, ck)
+    assert torch.isinf(got[0]).all() and torch.equal(got[1:], ref[1:].float())
+
+
 def test_weight_grad_unsplit_equals_the_formula():
     """Without its workspace the C call runs unsplit."""
     import ctypes
