@@ -104,14 +104,16 @@ __device__ __forceinline__ uint32_t finish_bf16(float y, const uint16_t* bias, i
   return pack_bf16x2(v, 0.0f);
 }
 
-// Eight consecutive elements of a row, z already with its bias, packed to bf16.  Wide
-// accesses: the caller has checked epilogue_wide and that all eight are in the row, and has
-// loaded the residual's eight values r (ignored without one).
+// Eight consecutive elements of a row, z already with its bias, packed to bf16.  All eight
+// are in the row, at any alignment (memcpy: one 16-byte access); the caller has loaded the
+// residual's eight values r (ignored without one).
 template <int kAct>
 __device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const uint4& r, const Epilogue& ep, int64_t idx) {
-  if (ep.preact != nullptr)
-    *reinterpret_cast<uint4*>(ep.preact + idx) = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                                                            pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+  if (ep.preact != nullptr) {
+    const uint4 p = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                               pack_bf16x2(z[6], z[7]));
+    __builtin_memcpy(ep.preact + idx, &p, 16);
+  }
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate_t<kAct>(z[i]);
@@ -128,13 +130,9 @@ __device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const uint4& 
 }
 
 __device__ __forceinline__ uint4 residual8(const Epilogue& ep, int64_t idx) {
-  return ep.residual != nullptr ? *reinterpret_cast<const uint4*>(ep.residual + idx) : make_uint4(0, 0, 0, 0);
-}
-
-// Whether finish8_bf16's wide accesses, and such a store to out, are aligned for rows of
-// ldo elements.
-__device__ __forceinline__ bool epilogue_wide(const Epilogue& ep, const uint16_t* out, int64_t ldo) {
-  return (ldo & 7) == 0 && (((uintptr_t)ep.residual | (uintptr_t)ep.preact | (uintptr_t)out) & 15) == 0;
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (ep.residual != nullptr) __builtin_memcpy(&r, ep.residual + idx, 16);
+  return r;
 }
 
 }  // namespace gemm

@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.h"
 #include "nvfp4_device.h"
@@ -352,7 +353,13 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     uint8_t* rst = lds + 4 * kEpiF32Wave + wave * kEpiResWave + lane * 16;   // this lane's own slots
     const int64_t er0 = row0 + wm * (32 * kTM);
     const int64_t ec = col0 + wn * 128 + 8 * (lane & 15);
-    const bool wide = (n & 7) == 0 && epilogue_wide(ep, out, ldo);   // whole 8-column groups
+    // Widths that are no multiple of 8, or an output at an odd address, take the same 16-byte
+    // accesses (any alignment does; stores through the cache, where neighbouring rows' parts
+    // of a line meet) and a row's last columns value by value: 4091 x 1024 -> 4097 with a
+    // residual 75 us, all of it value by value 212; its own loop, as the tests for it would cost
+    // aligned outputs 3 %.
+    const bool whole = ec + 8 <= n;                                    // this lane's eight columns
+    const bool wide = (n & 7) == 0 && ((uintptr_t)out & 15) == 0;
     float bv[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && ec + h < n ? bf16_to_f32(bias[ec + h]) : 0.0f;
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const int64_t row = er0 + i * 32 + 4 * p + (lane >> 4);
-          res[p] = wide && row < m && ec < n ? residual8(ep, row * ldo + ec) : make_uint4(0, 0, 0, 0);
+          res[p] = whole && row < m ? residual8(ep, row * ldo + ec) : make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
@@ -388,35 +395,32 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
         for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(rst + p * 1024) = res[p];
       }
       lds_order();
+      // Row 4 p + lane / 16 of the 32, this lane's eight columns.
+      auto finish = [&](int p, auto wide) {
+        const int64_t row = er0 + i * 32 + 4 * p + (lane >> 4);
+        const float* f = reinterpret_cast<const float*>(st + (4 * p + (lane >> 4)) * kEpiF32RowBytes + (lane & 15) * 32);
+        const float4 f0 = *reinterpret_cast<const float4*>(f), f1 = *reinterpret_cast<const float4*>(f + 4);
+        const float z[8] = {__fadd_rn(f0.x, bv[0]), __fadd_rn(f0.y, bv[1]), __fadd_rn(f0.z, bv[2]),
+                            __fadd_rn(f0.w, bv[3]), __fadd_rn(f1.x, bv[4]), __fadd_rn(f1.y, bv[5]),
+                            __fadd_rn(f1.z, bv[6]), __fadd_rn(f1.w, bv[7])};
+        const int64_t idx = row * ldo + ec;
+        if (row < m && whole) {
+          const uint4 r = ep.residual != nullptr ? *reinterpret_cast<const uint4*>(rst + p * 1024) : make_uint4(0, 0, 0, 0);
+          const uint4 o = finish8_bf16<kEpi>(z, r, ep, idx);
+          typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+          if constexpr (wide) __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(out + idx));
+          else __builtin_memcpy(out + idx, &o, 16);
+        } else if (!wide && row < m) {
+#pragma unroll 1
+          for (int h = 0; ec + h < n; ++h) out[idx + h] = (uint16_t)finish_bf16(f[h], bias, ec + h, ep, idx + h);
+        }
+      };
       if (wide) {
 #pragma unroll 1
-        for (int p = 0; p < 8; ++p) {
-          const int64_t row = er0 + i * 32 + 4 * p + (lane >> 4);
-          const float4* f =
-              reinterpret_cast<const float4*>(st + (4 * p + (lane >> 4)) * kEpiF32RowBytes + (lane & 15) * 32);
-          const float4 f0 = f[0], f1 = f[1];
-          const float z[8] = {__fadd_rn(f0.x, bv[0]), __fadd_rn(f0.y, bv[1]), __fadd_rn(f0.z, bv[2]),
-                              __fadd_rn(f0.w, bv[3]), __fadd_rn(f1.x, bv[4]), __fadd_rn(f1.y, bv[5]),
-                              __fadd_rn(f1.z, bv[6]), __fadd_rn(f1.w, bv[7])};
-          if (row < m && ec < n) {
-            const int64_t idx = row * ldo + ec;
-            const uint4 r = ep.residual != nullptr ? *reinterpret_cast<const uint4*>(rst + p * 1024) : make_uint4(0, 0, 0, 0);
-            const uint4 o = finish8_bf16<kEpi>(z, r, ep, idx);
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(out + idx));
-          }
-        }
+        for (int p = 0; p < 8; ++p) finish(p, std::true_type{});
       } else {
-        // any width and alignment: value by value, neighbouring lanes on neighbouring columns
-        const int64_t c0 = col0 + wn * 128;
 #pragma unroll 1
-        for (int v = lane; v < 32 * 128; v += 64) {
-          const int64_t row = er0 + i * 32 + (v >> 7), c = c0 + (v & 127);
-          if (row < m && c < n)
-            out[row * ldo + c] = (uint16_t)finish_bf16(
-                *reinterpret_cast<const float*>(st + (v >> 7) * kEpiF32RowBytes + (v & 127) * 4), bias, c, ep,
-                row * ldo + c);
-        }
+        for (int p = 0; p < 8; ++p) finish(p, std::false_type{});
       }
       lds_order();
     }
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
 #pragma unroll
     for (int h = 0; h < 8; ++h) z[h] = __fmul_rn(alpha, __fmul_rn(acc[h], kAccUnscale));
     const int64_t idx = row * ldo + col;
-    if (col + 8 <= n && epilogue_wide(ep, out, ldo)) {
+    if (col + 8 <= n) {
       if (bias != nullptr)
 #pragma unroll
         for (int h = 0; h < 8; ++h) z[h] = __fadd_rn(z[h], bf16_to_f32(bias[col + h]));
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
         case NVFP4_ACT_GELU_TANH: o = finish8_bf16<NVFP4_ACT_GELU_TANH>(z, r, ep, idx); break;
         default: o = finish8_bf16<NVFP4_ACT_NONE>(z, r, ep, idx);
       }
-      *reinterpret_cast<uint4*>(out + idx) = o;
+      __builtin_memcpy(out + idx, &o, 16);
     } else {
 #pragma unroll
       for (int h = 0; h < 8; ++h)
