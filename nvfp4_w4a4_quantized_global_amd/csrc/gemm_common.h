@@ -129,6 +129,16 @@ __device__ __forceinline__ uint4 finish8_bf16(const float (&z)[8], const uint4& 
                     pack_bf16x2(v[6], v[7]));
 }
 
+// The same with the activation chosen at run time (uniform over the launch).
+__device__ __forceinline__ uint4 finish8_any(const float (&z)[8], const uint4& r, const Epilogue& ep, int64_t idx) {
+  switch (ep.act) {
+    case NVFP4_ACT_SILU: return finish8_bf16<NVFP4_ACT_SILU>(z, r, ep, idx);
+    case NVFP4_ACT_GELU: return finish8_bf16<NVFP4_ACT_GELU>(z, r, ep, idx);
+    case NVFP4_ACT_GELU_TANH: return finish8_bf16<NVFP4_ACT_GELU_TANH>(z, r, ep, idx);
+    default: return finish8_bf16<NVFP4_ACT_NONE>(z, r, ep, idx);
+  }
+}
+
 __device__ __forceinline__ uint4 residual8(const Epilogue& ep, int64_t idx) {
   uint4 r = make_uint4(0, 0, 0, 0);
   if (ep.residual != nullptr) __builtin_memcpy(&r, ep.residual + idx, 16);

@@ -570,14 +570,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
       if (bias != nullptr)
 #pragma unroll
         for (int h = 0; h < 8; ++h) z[h] = __fadd_rn(z[h], bf16_to_f32(bias[col + h]));
-      const uint4 r = residual8(ep, idx);
-      uint4 o;
-      switch (ep.act) {
-        case NVFP4_ACT_SILU: o = finish8_bf16<NVFP4_ACT_SILU>(z, r, ep, idx); break;
-        case NVFP4_ACT_GELU: o = finish8_bf16<NVFP4_ACT_GELU>(z, r, ep, idx); break;
-        case NVFP4_ACT_GELU_TANH: o = finish8_bf16<NVFP4_ACT_GELU_TANH>(z, r, ep, idx); break;
-        default: o = finish8_bf16<NVFP4_ACT_NONE>(z, r, ep, idx);
-      }
+      const uint4 o = finish8_any(z, residual8(ep, idx), ep, idx);
       __builtin_memcpy(out + idx, &o, 16);
     } else {
 #pragma unroll
