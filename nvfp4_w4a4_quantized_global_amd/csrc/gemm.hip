@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
     const uint16_t* __restrict__ bias,
-    uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16, const Epilogue ep) {
+    typename OutputOf<kEpi>::ptr out, int64_t b_srows, int64_t ldo, int tiles_m, int tiles_n, int aligned16,
+    const Epilogue ep) {
   using C = Cfg<WM, WN, TM, TN>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 

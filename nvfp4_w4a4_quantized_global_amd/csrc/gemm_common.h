@@ -92,6 +92,16 @@ __device__ __forceinline__ uint32_t add_bias_bf16(uint32_t y_bf16, uint16_t bias
   return f32_to_bf16(__fadd_rn(bf16_to_f32(y_bf16), bf16_to_f32(bias_bf16)));
 }
 
+// A kernel's output: without the epilogue nothing else points into it; a residual may be it.
+template <bool kEpi>
+struct OutputOf {
+  using ptr = uint16_t* __restrict__;
+};
+template <>
+struct OutputOf<true> {
+  using ptr = uint16_t*;
+};
+
 // The epilogue with activation and residual, in fp32 from the product to one rounding:
 // z = y + bias (y = alpha times the accumulator), preact = bf16(z), out = bf16(act(z) +
 // residual).  One element, at idx of the row-major output; returns its bf16 bits.

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* out, int64_t b_srows, int64_t ldo, int tiles_m,
+    const uint16_t* __restrict__ bias, typename OutputOf<kEpi != kPlain>::ptr out, int64_t b_srows, int64_t ldo, int tiles_m,
     int tiles_n, int tile0, int splits, int sub,
     float* __restrict__ partial, const Epilogue ep) {   // ep last: the plain variants never fetch it
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
                                                       int tile0, int sub, int tiles_m, int64_t m, int64_t n,
                                                       const float* __restrict__ gsf_a, const float* __restrict__ gsf_b,
                                                       int64_t a_seg_rows, const uint16_t* __restrict__ bias,
-                                                      uint16_t* out, int64_t ldo, const Epilogue ep) {
+                                                      typename OutputOf<kEpi>::ptr out, int64_t ldo, const Epilogue ep) {
   using G = Geo<kTM>;
   constexpr int kPerTile = G::kAcc * 256 / 8;     // threads per tile
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;

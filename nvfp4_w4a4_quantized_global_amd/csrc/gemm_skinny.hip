@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* out, int splits,
+    const uint16_t* __restrict__ bias, typename OutputOf<kEpi>::ptr out, int splits,
     float* __restrict__ partial, const Epilogue ep) {   // ep last: the plain variants never fetch it
   __shared__ float red[MT * 4][4][64];     // waves 1..3 hand their sums to wave 0, one at a time
 
@@ -206,7 +206,8 @@ template <bool kEpi>
 __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restrict__ partial, int splits, int64_t m,
                                                           int64_t n, const float* __restrict__ gsf_a,
                                                           const float* __restrict__ gsf_b, int64_t a_seg_rows,
-                                                          const uint16_t* __restrict__ bias, uint16_t* out,
+                                                          const uint16_t* __restrict__ bias,
+                                                          typename OutputOf<kEpi>::ptr out,
                                                           const Epilogue ep) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= m * n) return;
@@ -313,7 +314,7 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, int64_t n,
     const float* __restrict__ gsf_a, const float* __restrict__ gsf_b, int64_t a_seg_rows,
-    const uint16_t* __restrict__ bias, uint16_t* out, int splits,
+    const uint16_t* __restrict__ bias, typename OutputOf<kEpi>::ptr out, int splits,
     float* __restrict__ partial,
     const uint16_t* __restrict__ a16, float* __restrict__ gsf_dst, const Epilogue ep) {
   // direct-load instructions per super tile and wave; bytes per slot and where the
