@@ -281,12 +281,13 @@ __global__ void __launch_bounds__(kQThreads) rmsnorm_quantize_kernel(const NormF
 
 // Gradient.  With n = r s, g = gy w and d = sum(g r) over the row:
 //   grad_r = s g - r (s^3 d / K) + grad_residual,   grad_w = sum over rows of gy n
-// (the rounding of y taken as the identity).  Each workgroup walks its rows, the next row's
-// loads in flight while one is computed, with its lanes' 16 columns of grad_w in registers,
-// and writes one partial row of them; rmsnorm_weight_grad_kernel adds the partials in a
-// fixed order.  The bound of 1024 threads also holds every variant to 128 registers, four
-// waves per SIMD: a few values spill, and the fourth wave is worth it (4096 x 5120 with
-// 146 registers 49 us, with 128 34 us: 168 MB at 5.0 TB/s).
+// (the rounding of y taken as the identity).  Each workgroup walks its rows with its lanes'
+// 16 columns of grad_w in registers and writes one partial row of them;
+// rmsnorm_weight_grad_kernel adds the partials in a fixed order.  The bound of 1024 threads
+// also holds every variant to 128 registers, four waves per SIMD, whose loads cover each
+// other's: fetching the next row ahead spilled, and cost more than it hid (4096 x 5120, both
+// kernels: bf16 stream 39 us ahead, 36 so, of which this one 31.7, 5.3 TB/s; fp32 stream 97
+// and 49, 6.0 TB/s).
 template <bool kSF32, bool kWF32, bool kRes>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackward a) {
   __shared__ double part_ss[2][16];
@@ -305,37 +306,30 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
 #pragma unroll
   for (int i = 0; i < 16; ++i) gw[i] = 0.0f;
 
-  struct Row {
-    Raw16<kSF32> r, q;
-    Raw16<false> g;
-  };
-  auto fetch = [&](int64_t row, Row& x) {
-    if (row < a.rows && in_k) {
-      const int64_t off = row * k + (int64_t)c * kBlock;
-      x.r.load(a.r, off);
-      x.g.load(a.gy, off);
-      if constexpr (kRes) x.q.load(a.grad_residual, off);
-    } else {
-      x.r.zero();
-      x.g.zero();
-      if constexpr (kRes) x.q.zero();
-    }
-  };
   const int64_t stride = (int64_t)gridDim.x * rows_here;
-  Row cur;
-  fetch((int64_t)blockIdx.x * rows_here + sub, cur);
   int parity = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += stride, parity ^= 1) {
     const int64_t row = row0 + sub;
-    Row nxt;
-    fetch(row + stride, nxt);
+    const int64_t off = row * k + (int64_t)c * kBlock;
+    const bool valid = row < a.rows && in_k;
+    Raw16<kSF32> rr, gres;
+    Raw16<false> gy;
+    if (valid) {
+      rr.load(a.r, off);
+      gy.load(a.gy, off);
+      if constexpr (kRes) gres.load(a.grad_residual, off);
+    } else {
+      rr.zero();
+      gy.zero();
+      if constexpr (kRes) gres.zero();
+    }
     float r[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = cur.r.get(i);
+    for (int i = 0; i < 16; ++i) r[i] = rr.get(i);
     double ss = sum_squares(r);
     float d = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d = fmaf(cur.g.get(i) * w.get(i), r[i], d);
+    for (int i = 0; i < 16; ++i) d = fmaf(gy.get(i) * w.get(i), r[i], d);
     const int lanes = a.lanes < 64 ? a.lanes : 64;
     ss = group_sum(ss, lanes);
     d = group_sum(d, lanes);
@@ -357,16 +351,15 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
     const float f = s * s * (d / (float)k);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float n = r[i] * s, g = cur.g.get(i);
+      const float n = r[i] * s, g = gy.get(i);
       gw[i] = fmaf(g, n, gw[i]);
       const float x = fmaf(s, g * w.get(i), -(n * f));
-      r[i] = kRes ? x + cur.q.get(i) : x;
+      r[i] = kRes ? x + gres.get(i) : x;
     }
-    if (row < a.rows && in_k) {
+    if (valid) {
       if constexpr (!kSF32) round_bf16(r);
-      store_stream16<kSF32>(a.grad_r, row * k + (int64_t)c * kBlock, r);
+      store_stream16<kSF32>(a.grad_r, off, r);
     }
-    cur = nxt;
   }
   if (a.grad_w == nullptr) return;
   if (rows_here == 1) {
@@ -421,15 +414,18 @@ ForwardFn forward_kernel(const NormForward& a) {
   return f[!a.stream_f32 ? 0 : !a.x_f32 ? 1 : 2][w];
 }
 
-// Workgroups of the row-walking kernels whose per-workgroup results are joined afterwards,
-// at most `most`.
-int64_t walking_blocks(int64_t rows, const RowShape& s, int64_t most) {
+// Workgroups of the row-walking kernels, whose results are joined afterwards: two for each
+// compute unit where they have four waves or more, about ten waves a unit where fewer.
+// Gradient, both kernels: 4096 x 5120 (five waves) with 256 / 512 / 768 workgroups 48 / 36 /
+// 44 us, 16384 x 1040 (two waves) with 512 / 1024 / 1280 75 / 44 / 41.  Statistics and second
+// pass of the dynamic scale: 4096 x 5120 with 256 / 512 / 768 / 1024 48.9 / 39.4 / 39.7 / 41.1,
+// 16384 x 5120 201 / 149 / 150 / 165, 16384 x 1040 with 512 / 1280 71 / 45.
+int64_t walking_blocks(int64_t rows, const RowShape& s) {
   const int64_t per = s.threads / s.lanes;
+  const int64_t most = s.threads >= 256 ? 512 : 2560 * 64 / s.threads;
+  static_assert(2560 * 64 / 128 <= kNormPartials, "rows longer than 1024 take two waves at least");
   return std::min<int64_t>((rows + per - 1) / per, most);
 }
-// The gradient's workgroups leave a row of partials each: enough of them to fill the GPU
-// (4096 x 5120: 256 workgroups 48 us, 512 34, 768 43 with their larger partials).
-constexpr int64_t kBackwardBlocks = 512;
 
 // Second-pass workgroups: a whole number of rows' tiles (at most 128) between a lane's
 // units, so that its tile of the weight stays the same.
@@ -450,7 +446,7 @@ hipError_t launch_rmsnorm(NormForward a, hipStream_t s) {
   if (a.mode == kNormDynamic) {
     // one row needs no second pass: its workgroup knows the whole abs-max
     a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
-    blocks = walking_blocks(a.rows, shape, kNormPartials);
+    blocks = walking_blocks(a.rows, shape);
   }
   hipLaunchKernelGGL(forward_kernel(a), dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
   hipError_t e = hipGetLastError();
@@ -465,13 +461,13 @@ hipError_t launch_rmsnorm(NormForward a, hipStream_t s) {
 }
 
 size_t rmsnorm_backward_partial_floats(int64_t rows, int64_t k) {
-  return (size_t)walking_blocks(rows, row_shape(k), kBackwardBlocks) * (size_t)k;
+  return (size_t)walking_blocks(rows, row_shape(k)) * (size_t)k;
 }
 
 hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s) {
   const RowShape shape = row_shape(a.k);
   a.lanes = shape.lanes;
-  const int64_t blocks = walking_blocks(a.rows, shape, kBackwardBlocks);
+  const int64_t blocks = walking_blocks(a.rows, shape);
   using Fn = void (*)(const NormBackward);
   static constexpr Fn f[2][2][2] = {
       {{rmsnorm_backward_kernel<false, false, false>, rmsnorm_backward_kernel<false, false, true>},

@@ -144,11 +144,7 @@ hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_
 // kNormStatic and kNormDynamic write NVFP4 codes and scales under *gsf or the dynamic
 // scale (gsf_out: the scale used); dynamic takes rstd [rows] and partials [kNormPartials].
 constexpr int64_t kNormMaxK = 16384;
-// Workgroups of the statistics pass at most: two for each compute unit, so that each walks
-// several rows and the second pass has few partials to join (both passes, bf16 with residual,
-// 256 / 512 / 768 / 1024 workgroups: 4096 x 5120 48.9 / 39.4 / 39.7 / 41.1 us, 16384 x 5120
-// 201 / 149 / 150 / 165, 1024 x 16384 33 / 36 / 38 / 40, 32768 x 512 36.5 / 30.3 / 29.6 / 30.8).
-constexpr int kNormPartials = 512;
+constexpr int kNormPartials = 1280;   // workgroups of the statistics pass at most
 enum NormMode { kNormOut, kNormStatic, kNormDynamic, kNormOneRow, kNormStats };   // the last two: internal
 struct NormForward {
   const void* x;
