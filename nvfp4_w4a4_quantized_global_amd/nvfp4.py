@@ -77,9 +77,9 @@ def _on_device(fn):
     return call
 
 
-def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, out) -> torch.Tensor | None:
-    """Checks a linear's epilogue arguments (``out``: the caller's, None for a new one);
-    returns the residual as a contiguous [m, n]."""
+def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, out, *inputs) -> torch.Tensor | None:
+    """Checks a linear's epilogue arguments (``out``: the caller's, None for a new one) against
+    each other and the linear's contiguous inputs; returns the residual as a contiguous [m, n]."""
     if residual is not None:
         if not isinstance(residual, torch.Tensor) or residual.dtype != torch.bfloat16 or residual.numel() != m * n \
                 or residual.dim() < 1 or residual.shape[-1] != n:
@@ -103,6 +103,11 @@ def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, ou
         for b, pb in named[i + 1:]:
             if abs(pa - pb) < 2 * m * n and not (pa == pb and (a, b) == ("out", "residual")):
                 raise ValueError(f"{a} and {b} must not overlap (residual may be out itself)")
+        if a != "residual":
+            for x in inputs:
+                px = x.data_ptr()
+                if pa < px + x.numel() * x.element_size() and px < pa + 2 * m * n:
+                    raise ValueError(f"{a} must not overlap the input")
     return residual
 
 
@@ -228,7 +233,7 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
     if act or residual is not None or preact is not None:
         _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given)
+        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given, x_codes)
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
                                         _ptr(workspace), ws_bytes, _stream(x_codes.device)))
@@ -286,7 +291,7 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     if act or residual is not None or preact is not None:
         _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, out_features, x.device, residual, preact, given)
+        residual = _epilogue_tensors(m, out_features, x.device, residual, preact, given, x2d)
         check(lib().nvfp4_linear_epilogue(_ptr(x2d), None, m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
@@ -424,7 +429,7 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
     if act or residual is not None or preact is not None:
         _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, given)
+        residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, given, g2, u2)
         check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
                                           _ptr(workspace), workspace.numel(), _stream(gate.device)))

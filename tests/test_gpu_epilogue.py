@@ -201,6 +201,27 @@ def test_refusals():
             lib.nvfp4_linear(x, pk, sc, gw, b, n, g, **kw)
 
 
+def test_refuses_an_output_over_its_input():
+    """Workgroups of one launch read the input while others write: h = linear(h) + h in place
+    is refused, also where the ranges only touch at an end; next to it is fine."""
+    lib = nv()
+    m, k = 3, 512
+    x, (pk, sc, gw), b, res, _ = _case(m, k, k, None)
+    buf = torch.empty(3 * m * k, dtype=BF, device=DEV)
+    h = buf[m * k:2 * m * k].view(m, k)
+    h.copy_(x)
+    for bad in (h, buf[8:m * k + 8].view(m, k), buf[2 * m * k - 8:3 * m * k - 8].view(m, k)):
+        with pytest.raises(ValueError):
+            lib.nvfp4_linear(h, pk, sc, gw, b, k, out=bad, residual=res)
+        with pytest.raises(ValueError):
+            lib.nvfp4_linear(h, pk, sc, gw, b, k, preact=bad, activation="silu")
+        with pytest.raises(ValueError):
+            lib.nvfp4_linear_swiglu(x, h, pk, sc, gw, b, k, out=bad, residual=res)
+    ref = lib.nvfp4_linear(x, pk, sc, gw, b, k, residual=res)
+    assert torch.equal(lib.nvfp4_linear(h, pk, sc, gw, b, k, out=buf[:m * k].view(m, k), residual=res), ref)
+    assert torch.equal(lib.nvfp4_linear(h, pk, sc, gw, b, k, residual=h), lib.nvfp4_linear(x, pk, sc, gw, b, k, residual=x))
+
+
 @pytest.mark.parametrize("g", [0, 16])
 @pytest.mark.parametrize("act,with_res", [(None, True), ("silu", False), ("gelu", True), ("gelu_tanh", False)])
 @pytest.mark.parametrize("packed", [False, True])
@@ -305,6 +326,57 @@ def test_flat_out_of_the_linear():
     out = torch.empty(20 * 96, dtype=BF, device=DEV)
     got = lib.nvfp4_linear(x, pk, sc, gw, b, 96, out=out)
     assert got.shape == (20, 96) and got.data_ptr() == out.data_ptr() and torch.equal(got, ref)
+
+
+def test_train_block_graph_replays():
+    """Forward and backward of a block from 8-bit checkpoints captured once and replayed on new
+    values, each replay against the eager block on other leaves with the same values (its
+    graph is gone when the capture runs)."""
+    lib = nv()
+    m, k, f = 48, 256, 512
+    d = lambda shape, i, s=1.0: workloads.draw("normal", shape, 112, i, s).float().to(DEV)  # noqa: E731
+    shapes = [(m, k), (m, k), (k,), (f, k), (f, k), (k, f)]
+
+    def values(seed):
+        return [d(s, 10 * seed + i, 0.05 if i > 2 else 1.0) for i, s in enumerate(shapes)], d((m, k), 10 * seed + 9).to(BF)
+
+    def step(leaves, gy):
+        x, h, nw, wg, wu, wd = leaves
+        y, r, ck = lib.rmsnorm_train(x.to(BF), nw, 1e-6, h.to(BF), True)
+        gate = lib.nvfp4_linear_train(y, wg, checkpoint=ck)
+        up = lib.nvfp4_linear_train(y, wu, checkpoint=ck, activation="gelu")
+        out = lib.nvfp4_linear_train(lib.swiglu_train(gate, up, True), wd, checkpoint=True, residual=r)
+        return [out.detach(), *torch.autograd.grad(out, leaves, gy)]
+
+    def eager(seed):
+        leaves, gy = values(seed)
+        return [t.clone() for t in step([t.requires_grad_(True) for t in leaves], gy)]
+
+    refs = [eager(s) for s in range(4)]
+    leaves, gy = values(0)
+    static = [t.requires_grad_(True) for t in leaves]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(static, gy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(static, gy)
+    for s in (1, 2, 3, 0):
+        new, g = values(s)
+        with torch.no_grad():
+            for a, b in zip(static, new):
+                a.copy_(b)
+            gy.copy_(g)
+        graph.replay()
+        torch.cuda.synchronize()
+        # the output and w_down's gradient come from this library's kernels alone: the same bits;
+        # the others pass grad_y W products of the platform library, fp32 sums in an order of
+        # its choice, whose bf16 rounding may fall one way or the other
+        assert torch.equal(got[0], refs[s][0]) and torch.equal(got[6], refs[s][6])
+        for a, b in zip(got, refs[s]):
+            assert (a.float() - b.float()).norm() <= 1e-3 * b.float().norm()
 
 
 def test_train_checkpoint_mismatch():
