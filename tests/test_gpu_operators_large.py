@@ -114,3 +114,15 @@ def test_weight_grad_on_integers(m, n, k):
     assert torch.equal(ck.dequantized(), x)
     for _ in range(3):
         assert torch.equal(lib.weight_grad(gy, ck), ref)
+
+
+@pytest.mark.parametrize("m,n,k", [(2, (1 << 24) + 8, 256), (3, (1 << 24) + 3, 16), (2, 24, (1 << 24) + 16)])
+def test_weight_grad_widest(m, n, k):
+    """Widths whose rows of a step pass 31-bit byte offsets, in both tile forms."""
+    lib = nv()
+    gy, x = _integers(m, n, 5, 4), _integers(m, k, 6, 3)
+    got = lib.weight_grad(gy, lib.checkpoint_pack(x), BF)
+    step = 1 << 20 if n > k else n
+    for i in range(0, n, step):
+        ref = gy[:, i:i + step].float().t().contiguous() @ x.float()      # at most 36: exact in bf16
+        assert torch.equal(got[i:i + step].float(), ref)
