@@ -66,11 +66,13 @@ def _saved(name: str, ck: Checkpoint) -> tuple[torch.Tensor, torch.Tensor, int, 
     return codes, scales if scales.is_contiguous() else scales.contiguous(), rows, k
 
 
+# New tensors come from empty_like on a contiguous tensor of their shape, or from sizes given
+# one by one: each some 0.5 us less host time than new_empty with a shape.
 def _empty_checkpoint(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
-    """Room for the checkpoint of x."""
-    shape = x.shape
-    return Checkpoint(x.new_empty(shape, dtype=torch.uint8),
-                      x.new_empty((*shape[:-1], _scale_columns(shape[-1])), dtype=torch.uint8), rotation_group)
+    """Room for the checkpoint of x (contiguous)."""
+    *lead, k = x.shape
+    return Checkpoint(torch.empty_like(x, dtype=torch.uint8),
+                      torch.empty(*lead, _scale_columns(k), dtype=torch.uint8, device=x.device), rotation_group)
 
 
 @_on_device
@@ -78,7 +80,7 @@ def checkpoint_pack(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
     """bf16 [..., K] (K a multiple of 16) to its 8-bit checkpoint, after the optional block
     rotation.  A value moves by at most 2^-4 of itself; infinities and NaN become NaN."""
     x2, rows, k = _rows("x", x)
-    ck = _empty_checkpoint(x, int(rotation_group))
+    ck = _empty_checkpoint(x2, int(rotation_group))
     check(lib().nvfp4_checkpoint_pack(_ptr(x2), rows, k, int(rotation_group), _ptr(ck.codes), _ptr(ck.scales),
                                       _stream(x.device)))
     return ck
@@ -112,9 +114,9 @@ def weight_grad(grad_y: torch.Tensor, ck: Checkpoint, dtype: torch.dtype = torch
     _require_device(gy.device, checkpoint=codes)
     if rows != m:
         raise ValueError(f"grad_y has {m} rows, the checkpoint {rows}")
-    out = gy.new_empty((n, k), dtype=dtype)
+    out = torch.empty(n, k, dtype=dtype, device=gy.device)
     need = lib().nvfp4_weight_grad_workspace_bytes(m, n, k)
-    ws = gy.new_empty((need,), dtype=torch.uint8) if need else None
+    ws = torch.empty(need, dtype=torch.uint8, device=gy.device) if need else None
     check(lib().nvfp4_weight_grad(_ptr(gy), m, n, _ptr(codes), _ptr(scales), k, _ptr(out), DTYPE_CODES[dtype], _ptr(ws),
                                   need, _stream(gy.device)))
     return out
@@ -125,8 +127,9 @@ def swiglu_checkpoint(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tenso
     """:func:`swiglu` and the 8-bit checkpoints of ``gate`` and ``up``, in one pass."""
     g2, u2 = _gate_up(gate, up)
     _require_device(gate.device, up=up)
-    x = gate.new_empty(gate.shape)
-    g, u = _empty_checkpoint(gate), _empty_checkpoint(gate)
+    like = g2 if gate.dim() == 2 else g2.view(gate.shape)
+    x = torch.empty_like(like)
+    g, u = _empty_checkpoint(like), _empty_checkpoint(like)
     check(lib().nvfp4_swiglu_checkpoint(_ptr(g2), _ptr(u2), g2.shape[0], g2.shape[1], _ptr(x), _ptr(g.codes),
                                         _ptr(g.scales), _ptr(u.codes), _ptr(u.scales), _stream(gate.device)))
     return x, g, u
@@ -151,7 +154,7 @@ def swiglu_backward(grad_x: torch.Tensor, gate, up) -> tuple[torch.Tensor, torch
     if gm != [rows, k] or um != [rows, k]:
         raise ValueError(f"grad_x, gate and up must have the same shape, got {list(gx.shape)}, {list(g.shape)} and "
                          f"{list(u.shape)}")
-    dg, du = gx.new_empty(grad_x.shape), gx.new_empty(grad_x.shape)
+    dg, du = torch.empty_like(gx), torch.empty_like(gx)
     check(lib().nvfp4_swiglu_backward(_ptr(gx), _ptr(g), _ptr(gs), _ptr(u), _ptr(us), rows, k, _ptr(dg), _ptr(du),
                                       _stream(gx.device)))
     return dg, du
@@ -173,7 +176,7 @@ def activation_backward(grad_y: torch.Tensor, z, activation: str | None) -> torc
     _require_device(gy.device, z=z2)
     if zm != [rows, n]:
         raise ValueError(f"grad_y and z must have the same shape, got {list(gy.shape)} and {list(z2.shape)}")
-    out = gy.new_empty(grad_y.shape)
+    out = torch.empty_like(gy)
     check(lib().nvfp4_activation_backward(_ptr(gy), _ptr(z2), _ptr(zs), rows, n, act, _ptr(out), _stream(gy.device)))
     return out
 

@@ -38,15 +38,15 @@ def _inputs(x, weight, eps, residual):
         if x.dtype == torch.float32 and residual.dtype != torch.float32:
             raise ValueError("an fp32 x needs an fp32 residual")
         rd = DTYPE_CODES[residual.dtype]
-        out = x.new_empty(x.shape, dtype=residual.dtype)
+        out = torch.empty_like(x2, dtype=residual.dtype)
     args = (x2.data_ptr(), xd, _ptr(r2), rd, w.data_ptr(), DTYPE_CODES[w.dtype], rows, k, float(eps))
     return args, (x2, r2, w), out, rows, k
 
 
 def _rmsnorm(x, weight, eps, residual, packed: bool):
-    args, _held, r, _, _ = _inputs(x, weight, eps, residual)
-    y = x.new_empty(x.shape, dtype=torch.bfloat16)
-    ck = _empty_checkpoint(x) if packed else None
+    args, held, r, _, _ = _inputs(x, weight, eps, residual)
+    y = torch.empty_like(held[0], dtype=torch.bfloat16)
+    ck = _empty_checkpoint(held[0]) if packed else None
     check(lib().nvfp4_rmsnorm(*args, _ptr(r), y.data_ptr(), ck.codes.data_ptr() if ck else None,
                               ck.scales.data_ptr() if ck else None, _stream(x.device)))
     return y, r, ck
@@ -78,16 +78,16 @@ def quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     them; with ``residual`` also r.  ``global_sf_x=None``: dynamic scale."""
     args, _held, r, rows, k = _inputs(x, weight, eps, residual)
     dev = x.device
-    codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
-    scales = x.new_empty((scale_bytes(rows, k),), dtype=torch.uint8)
-    gsf = x.new_empty((), dtype=torch.float32)
+    codes = torch.empty(rows, k // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty(scale_bytes(rows, k), dtype=torch.uint8, device=dev)
+    gsf = torch.empty((), dtype=torch.float32, device=dev)
     g, ws, need = None, None, 0
     if global_sf_x is not None:
         g = _scalar_f32(global_sf_x, dev)
         _require_device(dev, global_sf_x=g)
     else:
         need = lib().nvfp4_quantize_rmsnorm_workspace_bytes(rows)
-        ws = x.new_empty((need,), dtype=torch.uint8) if need else None
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if rows == 0:
         # nothing is launched: the scale is the given one, or that of an abs-max of 0
         gsf.copy_(static_global_sf(torch.zeros_like(gsf)) if g is None else g.reshape(()))
@@ -114,10 +114,10 @@ def rmsnorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor
         if rm != [rows, k]:
             raise ValueError(f"grad_residual and r must have the same shape, got {list(grad_residual.shape)} and "
                              f"{list(r.shape)}")
-    grad_r = r.new_empty(r.shape)
-    grad_w = r.new_empty((k,), dtype=torch.float32)
+    grad_r = torch.empty_like(r2)
+    grad_w = torch.empty(k, dtype=torch.float32, device=r.device)
     need = lib().nvfp4_rmsnorm_backward_workspace_bytes(rows, k)
-    ws = r.new_empty((max(need, 256),), dtype=torch.uint8)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=r.device)
     check(lib().nvfp4_rmsnorm_backward(_ptr(gy), _ptr(r2), DTYPE_CODES[r.dtype], _ptr(w), DTYPE_CODES[w.dtype], _ptr(gr),
                                        rows, k, float(eps), _ptr(grad_r), _ptr(grad_w), _ptr(ws), ws.numel(),
                                        _stream(r.device)))

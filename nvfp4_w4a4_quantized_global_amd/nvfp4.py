@@ -220,12 +220,12 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
             raise ValueError(f"bias must have {n} elements, got {bias.numel()}")
     given = out
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=x_codes.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x_codes.device)
     ws_bytes = 0
     if split_k:
         need = gemm_workspace_bytes(m, k, n)
         if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=x_codes.device)
         ws_bytes = 0 if workspace is None else workspace.numel()
     else:
         workspace = None
@@ -283,10 +283,10 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     m = x2d.shape[0]
     need = linear_workspace_bytes(m, k, out_features)
     if workspace is None:
-        workspace = x2d.new_empty((need,), dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     given = out
     if out is None:
-        out = x2d.new_empty((m, out_features))
+        out = torch.empty(m, out_features, dtype=torch.bfloat16, device=x.device)
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
         _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias,
@@ -453,7 +453,7 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, global_sf, dtype: tor
     if scales.numel() < scale_bytes(rows, k):
         raise ValueError("scales is smaller than nvfp4_scale_bytes(rows, K)")
     g = _scalar_f32(global_sf, packed.device)
-    out = torch.empty((rows, k), dtype=dtype, device=packed.device)
+    out = torch.empty(rows, k, dtype=dtype, device=packed.device)
     check(lib().nvfp4_dequantize(_ptr(packed), _ptr(scales), rows, k, _ptr(g), _ptr(out), codes[dtype],
                                  _stream(packed.device)))
     return out
