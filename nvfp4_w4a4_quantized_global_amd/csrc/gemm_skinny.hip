@@ -42,8 +42,8 @@ constexpr int kWaves = 4;
 
 // MT: M tiles of 16 rows.  kEpi (here and below): the epilogue with activation and residual,
 // a variant of its own so that the plain kernels stay as small as they are (one token,
-// 8192 -> 5120 in one launch: 10.0 us plain, 10.3-10.7 with a residual; 16 tokens, 2048 -> 5120,
-// decode and reduce: 9.0 and, with gelu and a residual, 11.8).
+// 8192 -> 5120 in one launch: 10.0 us plain, 10.3-10.7 with a residual; 16 tokens, 25600 ->
+// 5120: 20.1 us, and 4.0 for the reduce that adds the residual).
 template <int MT, bool kEpi>
 __global__ void __launch_bounds__(256) gemm_skinny_kernel(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, int64_t m, int64_t k,
