@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
         d += part_d[parity][i];
       }
     }
-    const float s = row_scale(ss, k, a.eps);
+    // 0 for the rows a workgroup has beyond the last: with eps = 0 theirs would be infinite, and
+    // their part of grad_w (0 times it) NaN
+    const float s = row < a.rows ? row_scale(ss, k, a.eps) : 0.0f;
     const float f = s * s * (d / (float)k);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
