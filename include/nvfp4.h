@@ -371,7 +371,9 @@ int nvfp4_quantize_rmsnorm(const void* x_dev, int x_dtype, const void* residual_
  * grad_y_dev bf16; r_dev, grad_residual_dev (NULL = none: the gradient that reaches r by
  * the residual stream) and grad_r_dev [rows][k] of r_dtype.  grad_r is the gradient of x
  * and of the residual alike.  grad_w_dev: fp32 [k], or NULL (then no workspace).  The row
- * partials of grad_w are added in a fixed order: results repeat bit for bit.
+ * partials of grad_w are added in a fixed order: results repeat bit for bit.  Rows may have
+ * any magnitude whose reciprocal is a normal fp32 number, as long as grad_y * weight * r of
+ * every value stays below 2e37.
  */
 size_t nvfp4_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t k);
 int nvfp4_rmsnorm_backward(const void* grad_y_dev, const void* r_dev, int r_dtype, const void* weight_dev,

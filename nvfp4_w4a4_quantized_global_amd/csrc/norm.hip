@@ -281,17 +281,22 @@ __global__ void __launch_bounds__(kQThreads) rmsnorm_quantize_kernel(const NormF
 
 // Gradient.  With n = r s, g = gy w and d = sum(g r) over the row:
 //   grad_r = s g - r (s^3 d / K) + grad_residual,   grad_w = sum over rows of gy n
-// (the rounding of y taken as the identity).  Each workgroup walks its rows with its lanes'
-// 16 columns of grad_w in registers and writes one partial row of them;
-// rmsnorm_weight_grad_kernel adds the partials in a fixed order.  The bound of 1024 threads
+// (the rounding of y taken as the identity).  s^2 leaves fp32's range from row magnitudes of
+// 1e19 up (and d, summed over a row, long before r does) while s^2 d is of the order of s g:
+// a lane sums its 16 products in fp32, the row's sum is fp64, and s multiplies its mean twice
+// (4096 x 5120 and 16384 x 1040 take the same time as with all of it in fp32; with the
+// products in fp64 too, 3 and 5 % more).
+//
+// Each workgroup walks its rows with its lanes' 16 columns of grad_w in registers and writes
+// one partial row of them; rmsnorm_weight_grad_kernel adds the partials in a fixed order.
+// The bound of 1024 threads
 // also holds every variant to 128 registers, four waves per SIMD, whose loads cover each
 // other's: fetching the next row ahead spilled, and cost more than it hid (4096 x 5120, both
 // kernels: bf16 stream 39 us ahead, 36 so, of which this one 31.7, 5.3 TB/s; fp32 stream 97
 // and 49, 6.0 TB/s).
 template <bool kSF32, bool kWF32, bool kRes>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackward a) {
-  __shared__ double part_ss[2][16];
-  __shared__ float part_d[2][16];
+  __shared__ double part_ss[2][16], part_d[2][16];
   __shared__ float colsum[kGroupThreads * 16];
   const int t = threadIdx.x;
   const int rows_here = blockDim.x / a.lanes;
@@ -307,6 +312,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
   for (int i = 0; i < 16; ++i) gw[i] = 0.0f;
 
   const int64_t stride = (int64_t)gridDim.x * rows_here;
+  const double inv_k = 1.0 / (double)k;
   int parity = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += stride, parity ^= 1) {
     const int64_t row = row0 + sub;
@@ -327,9 +333,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = rr.get(i);
     double ss = sum_squares(r);
-    float d = 0.0f;
+    float dl = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d = fmaf(gy.get(i) * w.get(i), r[i], d);
+    for (int i = 0; i < 16; ++i) dl = fmaf(gy.get(i) * w.get(i), r[i], dl);
+    double d = (double)dl;
     const int lanes = a.lanes < 64 ? a.lanes : 64;
     ss = group_sum(ss, lanes);
     d = group_sum(d, lanes);
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
       }
       __syncthreads();
       ss = 0.0;
-      d = 0.0f;
+      d = 0.0;
       for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
         ss += part_ss[parity][i];
         d += part_d[parity][i];
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
     // 0 for the rows a workgroup has beyond the last: with eps = 0 theirs would be infinite, and
     // their part of grad_w (0 times it) NaN
     const float s = row < a.rows ? row_scale(ss, k, a.eps) : 0.0f;
-    const float f = s * s * (d / (float)k);
+    const float f = s * (s * (float)(d * inv_k));
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float n = r[i] * s, g = gy.get(i);
