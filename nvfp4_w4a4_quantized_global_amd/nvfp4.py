@@ -94,21 +94,41 @@ def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, ou
     for name, t in (("preact", preact), ("out", out)):
         if t is None:
             continue
-        if t.dtype != torch.bfloat16 or t.shape != (m, n) or not t.is_contiguous():
+        if getattr(t, "shape", None) != (m, n):
             raise ValueError(f"{name} must be a contiguous bf16 [{m}, {n}] tensor")
-        _require_device(device, **{name: t})
+        _given_output(name, t, m, n, device, inputs)
     named = [(name, t.data_ptr()) for name, t in (("out", out), ("residual", residual), ("preact", preact))
              if t is not None]
     for i, (a, pa) in enumerate(named):
         for b, pb in named[i + 1:]:
             if abs(pa - pb) < 2 * m * n and not (pa == pb and (a, b) == ("out", "residual")):
                 raise ValueError(f"{a} and {b} must not overlap (residual may be out itself)")
-        if a != "residual":
-            for x in inputs:
-                px = x.data_ptr()
-                if pa < px + x.numel() * x.element_size() and px < pa + 2 * m * n:
-                    raise ValueError(f"{a} must not overlap the input")
     return residual
+
+
+def _given_output(name: str, t: torch.Tensor, m: int, n: int, device: torch.device, inputs, larger: bool = False) -> None:
+    """Checks an output that the caller gives: contiguous bf16 with m * n values (``larger``: or
+    more) on the call's device, apart from its inputs, which workgroups still read while
+    others write."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_contiguous() \
+            or not (t.numel() == m * n or (larger and t.numel() > m * n)):
+        raise ValueError(f"{name} must be contiguous bf16 with {m} x {n} values, got {getattr(t, 'dtype', None)} "
+                         f"{list(getattr(t, 'shape', []))}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    p = t.data_ptr()
+    for x in inputs:
+        px = x.data_ptr()
+        if p < px + x.numel() * x.element_size() and px < p + 2 * m * n:
+            raise ValueError(f"{name} must not overlap the input")
+
+
+def _given_workspace(workspace: torch.Tensor, device: torch.device) -> None:
+    """A caller's workspace: as many bytes of the call's device as it has elements, at least."""
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
 
 
 def scale_bytes(rows: int, k: int) -> int:
@@ -223,6 +243,8 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         out = torch.empty(m, n, dtype=torch.bfloat16, device=x_codes.device)
     ws_bytes = 0
     if split_k:
+        if workspace is not None:
+            _given_workspace(workspace, x_codes.device)
         need = gemm_workspace_bytes(m, k, n)
         if need and (workspace is None or workspace.numel() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=x_codes.device)
@@ -233,11 +255,13 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
     if act or residual is not None or preact is not None:
         _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias,
                         global_sf_x=gx, global_sf_w=gw, workspace=workspace)
-        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given, x_codes)
+        residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given, x_codes, x_scales)
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
                                         _ptr(workspace), ws_bytes, _stream(x_codes.device)))
         return out
+    if given is not None:
+        _given_output("out", given, m, n, x_codes.device, (x_codes, x_scales), larger=True)
     check(lib().nvfp4_gemm(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx), _ptr(gw),
                            _ptr(bias), _ptr(out), _ptr(workspace), ws_bytes, _stream(x_codes.device)))
     return out
@@ -253,6 +277,7 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
 
     ``global_sf_x=None`` computes the activation scale dynamically from the
     call's 2-D input.  Leading dimensions of x are flattened and restored.
+    ``out``: contiguous bf16 with the output's number of values, that does not overlap x.
 
     With ``activation`` ("silu", "gelu" or "gelu_tanh"), ``residual`` (bf16, the output's
     shape) or ``preact`` the epilogue is ``bf16(act(z) + residual)`` from z = product + bias,
@@ -284,6 +309,8 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     need = linear_workspace_bytes(m, k, out_features)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _given_workspace(workspace, x.device)
     given = out
     if out is None:
         out = torch.empty(m, out_features, dtype=torch.bfloat16, device=x.device)
@@ -297,6 +324,8 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
                                           _stream(x.device)))
         return out if out.dim() == x.dim() == 2 else out.reshape(*orig[:-1], out_features)
+    if given is not None:
+        _given_output("out", given, m, out_features, x.device, (x2d,))
     check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
                              _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
                              _stream(x.device)))
@@ -334,6 +363,8 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
     elif out.shape != (m, out_features) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 [{m}, {out_features}] tensor")
+    else:
+        _given_output("out", out, m, out_features, x.device, (x2d,))
     check(lib().nvfp4_linear_noalloc(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                      out_features, _ptr(gx), int(rotation_group), _ptr(out), _stream(x.device)))
     return out.reshape(*orig[:-1], out_features)
@@ -422,6 +453,8 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
     if workspace is None:
         need = int(lib().nvfp4_linear_swiglu_workspace_bytes(m, k, out_features))
         workspace = torch.empty((need,), dtype=torch.uint8, device=gate.device)
+    else:
+        _given_workspace(workspace, gate.device)
     given = out
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=gate.device)
@@ -434,6 +467,8 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
                                           _ptr(workspace), workspace.numel(), _stream(gate.device)))
         return out.reshape(*gate.shape[:-1], out_features)
+    if given is not None:
+        _given_output("out", given, m, out_features, gate.device, (g2, u2))
     check(lib().nvfp4_linear_swiglu(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                     out_features, _ptr(gx), _ptr(out), _ptr(workspace), workspace.numel(),
                                     _stream(gate.device)))
@@ -527,8 +562,12 @@ def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor,
     need = linear_segmented_workspace_bytes(segments, seg_rows, k, out_features)
     if workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    else:
+        _given_workspace(workspace, x.device)
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
+    else:
+        _given_output("out", out, m, out_features, x.device, (x2d,))
     check(lib().nvfp4_linear_segmented(_ptr(x2d), segments, seg_rows, k, _ptr(packed), _ptr(inv_scale), _ptr(gw),
                                        _ptr(bias), out_features, int(rotation_group), _ptr(out), _ptr(gsf_out),
                                        _ptr(workspace), workspace.numel(), _stream(x.device)))
