@@ -323,13 +323,15 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
                                           _ptr(preact), _ptr(out), _ptr(workspace), workspace.numel(),
                                           _stream(x.device)))
-        return out if out.dim() == x.dim() == 2 else out.reshape(*orig[:-1], out_features)
-    if given is not None:
-        _given_output("out", given, m, out_features, x.device, (x2d,))
-    check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
-                             _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
-                             _stream(x.device)))
-    return out if out.dim() == x.dim() == 2 else out.reshape(*orig[:-1], out_features)
+    else:
+        if given is not None:
+            _given_output("out", given, m, out_features, x.device, (x2d,))
+        check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
+                                 _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
+                                 _stream(x.device)))
+    if x.dim() == 2 and (given is None or given.shape == (m, out_features)):
+        return out
+    return out.reshape(*orig[:-1], out_features)
 
 
 def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor, global_sf_w: torch.Tensor,
