@@ -94,9 +94,9 @@ def _epilogue_tensors(m: int, n: int, device: torch.device, residual, preact, ou
     for name, t in (("preact", preact), ("out", out)):
         if t is None:
             continue
-        if getattr(t, "shape", None) != (m, n):
-            raise ValueError(f"{name} must be a contiguous bf16 [{m}, {n}] tensor")
         _given_output(name, t, m, n, device, inputs)
+        if t.dim() < 1 or t.shape[-1] not in (n, m * n):
+            raise ValueError(f"{name} must have rows of {n}, or be flat, got {list(t.shape)}")
     named = [(name, t.data_ptr()) for name, t in (("out", out), ("residual", residual), ("preact", preact))
              if t is not None]
     for i, (a, pa) in enumerate(named):
@@ -281,8 +281,9 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
 
     With ``activation`` ("silu", "gelu" or "gelu_tanh"), ``residual`` (bf16, the output's
     shape) or ``preact`` the epilogue is ``bf16(act(z) + residual)`` from z = product + bias,
-    in fp32 with that one rounding.  ``residual`` may be ``out`` itself; ``preact``
-    (contiguous bf16 [rows, out_features]) receives bf16(z).
+    in fp32 with that one rounding.  ``residual`` may be ``out`` itself; ``preact`` (contiguous
+    bf16) receives bf16(z).  ``out`` and ``preact`` then have rows of out_features under any
+    leading dimensions, or are flat.
     """
     if x.dtype != torch.bfloat16:
         raise ValueError(f"x must be bf16, got {x.dtype}")

@@ -40,3 +40,25 @@ def test_refused_without_an_epilogue(m):
     buf[m:] = 7.0
     got = nv.nvfp4_gemm(c, s, pk, sc, g, gw, out=buf)
     assert got is buf and torch.equal(buf[:m], nv.nvfp4_gemm(c, s, pk, sc, g, gw)) and bool((buf[m:] == 7.0).all())
+
+
+@pytest.mark.parametrize("m", [2, 20, 300])
+def test_residual_stream_of_three_dimensions_in_place(m):
+    """A [batch, tokens, N] stream updated in place, and preact of that shape."""
+    k, n = 256, 136
+    nv, x, (pk, sc, gw) = _case(m, k, n)
+    h = workloads.draw("t3", (m, n), 232, m).to(DEV)
+    ref_pre = torch.empty((m, n), dtype=BF, device=DEV)
+    ref = nv.nvfp4_linear(x, pk, sc, gw, None, n, activation="gelu", residual=h, preact=ref_pre)
+    stream, pre = h.clone().view(2, m // 2, n), torch.empty((2, m // 2, n), dtype=BF, device=DEV)
+    got = nv.nvfp4_linear(x.view(2, m // 2, k), pk, sc, gw, None, n, activation="gelu", residual=stream, out=stream,
+                          preact=pre)
+    assert got.data_ptr() == stream.data_ptr() and got.shape == stream.shape
+    assert torch.equal(stream.view(m, n), ref) and torch.equal(pre.view(m, n), ref_pre)
+    down = nv.quantize_weight(workloads.draw("normal", (k, n - 8), 233, k, 0.05).to(DEV))
+    g, u = (workloads.draw("normal", (m, n - 8), 234, i).to(DEV) for i in range(2))
+    stream = workloads.draw("t3", (m, k), 235, m).to(DEV)
+    ref = nv.nvfp4_linear_swiglu(g, u, *down, None, k, residual=stream)
+    s3 = stream.view(2, m // 2, k)
+    nv.nvfp4_linear_swiglu(g.view(2, m // 2, n - 8), u.view(2, m // 2, n - 8), *down, None, k, residual=s3, out=s3)
+    assert torch.equal(stream, ref)
