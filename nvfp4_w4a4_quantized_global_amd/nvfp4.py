@@ -817,9 +817,9 @@ class NVFP4Linear:
         """Switch to a static scale from a recorded abs-max (a float or an fp32 device scalar)."""
         self.act_scale, self.input_amax, self.margin, self._gsf_x = "static", input_amax, float(margin), None
 
-    def __call__(self, x: torch.Tensor, activation: str | None = None,
-                 residual: torch.Tensor | None = None) -> torch.Tensor:
-        """The linear on ``x``; ``activation`` and ``residual`` as in :func:`nvfp4_linear`."""
+    def __call__(self, x: torch.Tensor, activation: str | None = None, residual: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, preact: torch.Tensor | None = None) -> torch.Tensor:
+        """The linear on ``x``; the other arguments as in :func:`nvfp4_linear`."""
         x = x.to(torch.bfloat16)
         g = self.rotation_group or 0
         if self._record is not None:
@@ -829,7 +829,7 @@ class NVFP4Linear:
         else:
             gsf = self.activation_global_sf()
         return nvfp4_linear(x, self.packed, self.inv_scale, self.global_sf_w, self.bias, self.out_features, gsf, g,
-                            activation=activation, residual=residual)
+                            out=out, activation=activation, residual=residual, preact=preact)
 
     def dequantized_weight(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The packed weight expanded back to ``dtype`` (the W4A16 fallback's weight)."""

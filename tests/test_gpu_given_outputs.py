@@ -62,3 +62,26 @@ def test_residual_stream_of_three_dimensions_in_place(m):
     s3 = stream.view(2, m // 2, k)
     nv.nvfp4_linear_swiglu(g.view(2, m // 2, n - 8), u.view(2, m // 2, n - 8), *down, None, k, residual=s3, out=s3)
     assert torch.equal(stream, ref)
+
+
+@pytest.mark.parametrize("kw", [{}, {"rotation_group": 16}, {"act_scale": "unit"}])
+def test_layer_updates_its_stream_in_place(kw):
+    """NVFP4Linear takes the epilogue's out and preact too."""
+    import nvfp4_w4a4_quantized_global_amd as nv
+    m, k, n = 12, 256, 128
+    layer = nv.NVFP4Linear.from_weight(workloads.draw("normal", (n, k), 236, 0, 0.05).to(DEV),
+                                       workloads.draw("normal", (n,), 236, 1).to(DEV), **kw)
+    x = workloads.draw("normal", (2, m // 2, k), 237, 0).to(DEV)
+    h = workloads.draw("t3", (2, m // 2, n), 237, 1).to(DEV)
+    ref, z = layer(x, "silu", h), torch.empty_like(h)
+    stream = h.clone()
+    got = layer(x, activation="silu", residual=stream, out=stream, preact=z)
+    assert got.data_ptr() == stream.data_ptr() and torch.equal(stream, ref)
+    assert torch.equal(layer(x, residual=h), nv.nvfp4_linear(
+        x, layer.packed, layer.inv_scale, layer.global_sf_w, layer.bias, n, layer.activation_global_sf(),
+        layer.rotation_group or 0, residual=h))
+    plain = torch.empty_like(h)
+    assert torch.equal(layer(x, out=plain), layer(x)) and torch.equal(plain, layer(x))
+    # z is the sum before the activation, rounded once: within the roundings of the plain linear's two
+    y = layer(x).float()
+    assert ((z.float() - y).abs() <= 2.0 ** -8 * (z.float().abs() + 3 * y.abs() + 2 * layer.bias.float().abs())).all()
