@@ -123,6 +123,12 @@ def _given_output(name: str, t: torch.Tensor, m: int, n: int, device: torch.devi
             raise ValueError(f"{name} must not overlap the input")
 
 
+def _written(*tensors: torch.Tensor | None) -> None:
+    """Tells autograd of the caller's tensors that a kernel has written, so that a gradient which
+    saved one of them raises instead of reading the new values."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _given_workspace(workspace: torch.Tensor, device: torch.device) -> None:
     """A caller's workspace: as many bytes of the call's device as it has elements, at least."""
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
@@ -259,11 +265,15 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
                                         _ptr(workspace), ws_bytes, _stream(x_codes.device)))
+        if given is not None or preact is not None:
+            _written(given, preact)
         return out
     if given is not None:
         _given_output("out", given, m, n, x_codes.device, (x_codes, x_scales), larger=True)
     check(lib().nvfp4_gemm(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx), _ptr(gw),
                            _ptr(bias), _ptr(out), _ptr(workspace), ws_bytes, _stream(x_codes.device)))
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -330,6 +340,8 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         check(lib().nvfp4_linear(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias), out_features,
                                  _ptr(gx), int(rotation_group), _ptr(out), _ptr(workspace), workspace.numel(),
                                  _stream(x.device)))
+    if given is not None or preact is not None:
+        _written(given, preact)
     if x.dim() == 2 and (given is None or given.shape == (m, out_features)):
         return out
     return out.reshape(*orig[:-1], out_features)
@@ -362,6 +374,7 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
         if bias.numel() != out_features:
             raise ValueError(f"bias must have {out_features} elements, got {bias.numel()}")
     m = x2d.shape[0]
+    given = out
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
     elif out.shape != (m, out_features) or out.dtype != torch.bfloat16 or not out.is_contiguous():
@@ -370,6 +383,8 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
         _given_output("out", out, m, out_features, x.device, (x2d,))
     check(lib().nvfp4_linear_noalloc(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                      out_features, _ptr(gx), int(rotation_group), _ptr(out), _stream(x.device)))
+    if given is not None:
+        _written(given)
     return out.reshape(*orig[:-1], out_features)
 
 
@@ -384,6 +399,7 @@ def amax(x: torch.Tensor, rotation_group: int = 0, out: torch.Tensor | None = No
     if not x2d.is_contiguous():
         x2d = x2d.contiguous()
     _require_cuda("x", x2d, torch.bfloat16, 2)
+    given = out
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the running value in out")
@@ -392,6 +408,8 @@ def amax(x: torch.Tensor, rotation_group: int = 0, out: torch.Tensor | None = No
     ws = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
     check(lib().nvfp4_amax(_ptr(x2d), x2d.shape[0], k, int(rotation_group), _ptr(out), int(bool(accumulate)), _ptr(ws),
                            ws.numel(), _stream(x.device)))
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -469,12 +487,14 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
         check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
                                           _ptr(workspace), workspace.numel(), _stream(gate.device)))
-        return out.reshape(*gate.shape[:-1], out_features)
-    if given is not None:
-        _given_output("out", given, m, out_features, gate.device, (g2, u2))
-    check(lib().nvfp4_linear_swiglu(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
-                                    out_features, _ptr(gx), _ptr(out), _ptr(workspace), workspace.numel(),
-                                    _stream(gate.device)))
+    else:
+        if given is not None:
+            _given_output("out", given, m, out_features, gate.device, (g2, u2))
+        check(lib().nvfp4_linear_swiglu(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
+                                        out_features, _ptr(gx), _ptr(out), _ptr(workspace), workspace.numel(),
+                                        _stream(gate.device)))
+    if given is not None or preact is not None:
+        _written(given, preact)
     return out.reshape(*gate.shape[:-1], out_features)
 
 
@@ -567,6 +587,7 @@ def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor,
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     else:
         _given_workspace(workspace, x.device)
+    given = out
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
     else:
@@ -574,6 +595,8 @@ def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor,
     check(lib().nvfp4_linear_segmented(_ptr(x2d), segments, seg_rows, k, _ptr(packed), _ptr(inv_scale), _ptr(gw),
                                        _ptr(bias), out_features, int(rotation_group), _ptr(out), _ptr(gsf_out),
                                        _ptr(workspace), workspace.numel(), _stream(x.device)))
+    if given is not None or gsf_out is not None:
+        _written(given, gsf_out)
     return out.reshape(*x.shape[:-1], out_features)
 
 

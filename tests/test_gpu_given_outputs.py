@@ -85,3 +85,25 @@ def test_layer_updates_its_stream_in_place(kw):
     # z is the sum before the activation, rounded once: within the roundings of the plain linear's two
     y = layer(x).float()
     assert ((z.float() - y).abs() <= 2.0 ** -8 * (z.float().abs() + 3 * y.abs() + 2 * layer.bias.float().abs())).all()
+
+
+def test_a_stream_that_the_norms_gradient_saved():
+    """Updating in place the stream that rmsnorm_train saved is an error in its backward, not a
+    gradient at the new values."""
+    import nvfp4_w4a4_quantized_global_amd as nv
+    m, k = 6, 256
+    x = workloads.draw("normal", (m, k), 238, 0).to(DEV).requires_grad_(True)
+    h = workloads.draw("t3", (m, k), 238, 1).to(DEV)
+    wt = torch.ones(k, device=DEV)
+    layer = nv.NVFP4Linear.from_weight(workloads.draw("normal", (k, k), 239, 0, 0.05).to(DEV))
+    for update in (True, False):
+        y, r = nv.rmsnorm_train(x, wt, 1e-6, h)
+        stream = r.detach() if update else r.detach().clone()
+        layer(y.detach(), residual=stream, out=stream)
+        x.grad = None
+        if update:
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.float().sum().backward()
+        else:
+            y.float().sum().backward()
+            assert torch.isfinite(x.grad).all()
