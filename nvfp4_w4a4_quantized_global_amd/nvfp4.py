@@ -28,6 +28,7 @@ DTYPE_CODES = {torch.bfloat16: _lib.NVFP4_DTYPE_BF16, torch.float32: _lib.NVFP4_
 
 # Addresses and streams go to ctypes as plain integers (the argument types are c_void_p):
 # wrapping them, and building a torch Stream object for its handle, costs microseconds a call.
+# The same goes for torch._C's functions here against the public ones that wrap them.
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -65,12 +66,15 @@ def _require_device(device: torch.device, **tensors: torch.Tensor | None) -> Non
 
 
 def _on_device(fn):
-    """Runs ``fn`` with its first tensor's device current: the library launches on, sizes its
-    workspaces for and keeps kernel attributes of the current device."""
+    """Runs ``fn`` with the device of its first GPU tensor current, however the arguments are
+    given: the library launches on, sizes its workspaces for and keeps kernel attributes of
+    the current device."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        t = args[0] if args else next(iter(kwargs.values()), None)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+        t = args[0] if args else None
+        if not isinstance(t, torch.Tensor):
+            t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
+        if t is not None and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(t.device):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -126,7 +130,7 @@ def _given_output(name: str, t: torch.Tensor, m: int, n: int, device: torch.devi
 def _written(*tensors: torch.Tensor | None) -> None:
     """Tells autograd of the caller's tensors that a kernel has written, so that a gradient which
     saved one of them raises instead of reading the new values."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+    torch._C._increment_version([t for t in tensors if t is not None])
 
 
 def _given_workspace(workspace: torch.Tensor, device: torch.device) -> None:
@@ -170,6 +174,7 @@ def _scalar_f32(v, device) -> torch.Tensor:
     return torch.tensor(float(v), dtype=torch.float32, device=device)
 
 
+@_on_device
 def rotate_activation(x: torch.Tensor, group_size: int, out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """Block Hadamard rotation of the last dimension, groups of ``group_size``.
 
@@ -189,6 +194,7 @@ def rotate_activation(x: torch.Tensor, group_size: int, out_dtype: torch.dtype |
     return y
 
 
+@_on_device
 def quantize_weight(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """bf16 weight [N, K] -> (packed uint8 [N, K/2], block scales uint8 (layout), global scale fp32 0-d)."""
     _require_cuda("weight", w, torch.bfloat16, 2)
@@ -202,6 +208,7 @@ def quantize_weight(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.
     return packed, scales, gsf
 
 
+@_on_device
 def quantize_activation(x: torch.Tensor, global_sf_x=None, rotation_group: int = 0
                         ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """bf16 [M, K] -> (codes uint8 [M, K/2], scales uint8 (layout), the global scale used, fp32 0-d)."""
@@ -347,6 +354,7 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
     return out.reshape(*orig[:-1], out_features)
 
 
+@_on_device
 def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor, global_sf_w: torch.Tensor,
                          bias: torch.Tensor | None, out_features: int, global_sf_x=None, rotation_group: int = 0,
                          out: torch.Tensor | None = None) -> torch.Tensor:
@@ -377,10 +385,10 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
     given = out
     if out is None:
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=x.device)
-    elif out.shape != (m, out_features) or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous bf16 [{m}, {out_features}] tensor")
     else:
         _given_output("out", out, m, out_features, x.device, (x2d,))
+        if out.shape != (m, out_features):
+            raise ValueError(f"out must be a contiguous bf16 [{m}, {out_features}] tensor")
     check(lib().nvfp4_linear_noalloc(_ptr(x2d), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                      out_features, _ptr(gx), int(rotation_group), _ptr(out), _stream(x.device)))
     if given is not None:
@@ -388,6 +396,7 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
     return out.reshape(*orig[:-1], out_features)
 
 
+@_on_device
 def amax(x: torch.Tensor, rotation_group: int = 0, out: torch.Tensor | None = None,
          accumulate: bool = False) -> torch.Tensor:
     """max |x| over a bf16 [.., K] input after the optional block rotation, as an fp32 0-d
@@ -425,6 +434,7 @@ def _gate_up(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tensor, torch.
     return g2, u2
 
 
+@_on_device
 def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     """bf16 SwiGLU product silu(gate) * up (the input of down_proj)."""
     g2, u2 = _gate_up(gate, up)
@@ -433,6 +443,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     return x.reshape(gate.shape)
 
 
+@_on_device
 def quantize_swiglu(gate: torch.Tensor, up: torch.Tensor, global_sf_x=None
                     ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """quantize_activation(swiglu(gate, up)) without writing the product."""
@@ -498,6 +509,7 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
     return out.reshape(*gate.shape[:-1], out_features)
 
 
+@_on_device
 def dequantize(packed: torch.Tensor, scales: torch.Tensor, global_sf, dtype: torch.dtype = torch.bfloat16
                ) -> torch.Tensor:
     """NVFP4 [rows, K/2] + scales back to ``dtype`` values fp32(code * scale) / global_sf."""
@@ -517,6 +529,7 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, global_sf, dtype: tor
     return out
 
 
+@_on_device
 def static_global_sf(input_amax: torch.Tensor, margin: float = 1.0) -> torch.Tensor:
     """Static activation scale 2688 / max(fp32(input_amax * margin), 1e-12) (fp32 0-d)."""
     _require_cuda("input_amax", input_amax, torch.float32)
@@ -533,6 +546,7 @@ def _segment_rows(x2d: torch.Tensor, segments: int) -> int:
     return x2d.shape[0] // segments
 
 
+@_on_device
 def quantize_activation_segmented(x: torch.Tensor, segments: int, rotation_group: int = 0
                                   ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Dynamic-scale quantization of ``segments`` equal row blocks, one global scale each.
@@ -551,6 +565,7 @@ def quantize_activation_segmented(x: torch.Tensor, segments: int, rotation_group
     return codes, scales[: scale_bytes(m, k)], gsf
 
 
+@_on_device
 def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor, inv_scale: torch.Tensor,
                            global_sf_w: torch.Tensor, bias: torch.Tensor | None, out_features: int,
                            rotation_group: int = 0, workspace: torch.Tensor | None = None,
@@ -600,6 +615,7 @@ def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor,
     return out.reshape(*x.shape[:-1], out_features)
 
 
+@_on_device
 def scale_to_canonical(layout: torch.Tensor, rows: int, k: int) -> torch.Tensor:
     """Block scales from the library layout to row-major uint8 [rows, K/16]."""
     _require_cuda("layout", layout, torch.uint8)
@@ -608,6 +624,7 @@ def scale_to_canonical(layout: torch.Tensor, rows: int, k: int) -> torch.Tensor:
     return out
 
 
+@_on_device
 def scale_from_canonical(canonical: torch.Tensor) -> torch.Tensor:
     """Row-major uint8 [rows, K/16] block scales to the library layout."""
     _require_cuda("canonical", canonical, torch.uint8, 2)

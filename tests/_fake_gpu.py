@@ -10,6 +10,9 @@ class OnGpu(torch.Tensor):
     is_cuda = property(lambda self: True)
     device = property(lambda self: torch.device("cuda", getattr(self, "gpu", 0)))
 
+    def get_device(self):
+        return getattr(self, "gpu", 0)
+
 
 def on_gpu(t, index=0):
     t = t.as_subclass(OnGpu)
@@ -36,5 +39,5 @@ def install(monkeypatch, *modules, current=0):
     for m in modules:
         monkeypatch.setattr(m, "lib", lambda: rec)
         monkeypatch.setattr(m, "_stream", lambda device: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current)
     return rec
