@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_kernel(
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     float al[16];
-    group_alphas(gsf_a, gsf_b, a_seg_rows, wrow0 + i * 32, kh, m, al);
+    group_alphas(gsf_a, gsf_b, kEpi ? 0 : a_seg_rows, wrow0 + i * 32, kh, m, al);
     if constexpr (kEpi) {
       // in fp32 through the wave's LDS region, then eight columns of a row per lane, the
       // next row's residual in flight (4091 x 1040 -> 4096 with gelu and residual 88 us, value
@@ -407,6 +407,7 @@ hipError_t launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t 
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
                        const float* gsf_a, const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias,
                        const Epilogue& ep, uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t s) {
+  if (ep.active() && a_seg_rows > 0) return hipErrorInvalidValue;   // the epilogue's variants know one scale
   const int cus = compute_units();
   if (prefer_skinny(m, n) && gemm_skinny_supported(m, k, a_codes, a_scales, b_codes, b_scales))
     return launch_gemm_skinny(a_codes, a_scales, m, k, b_codes, b_scales, n, gsf_a, gsf_b, a_seg_rows, bias, ep, out,

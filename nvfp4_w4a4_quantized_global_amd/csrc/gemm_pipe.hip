@@ -363,10 +363,9 @@ __global__ void __launch_bounds__(256, 1) gemm_pipe_kernel(
     float bv[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && ec + h < n ? bf16_to_f32(bias[ec + h]) : 0.0f;
-    const float alpha = a_seg_rows > 0 ? 0.0f : alpha_for(gsf_a, gsf_b, 0, 0);
+    const float al = alpha_for(gsf_a, gsf_b, 0, 0);
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
-      const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, min(er0 + i * 32 + lr, m - 1)) : alpha;
       // The residual of this lane's eight rows is in flight while the product is staged, then
       // waits in LDS: the loop over the rows stays rolled (unrolled, 32 copies of the
       // activation overflow the instruction cache: 32768 x 1024 -> 4096 with gelu 368 us
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(256) split_k_reduce(const float* __restrict__ 
   const int64_t row = ((int64_t)tm * sub + tl % sub) * G::kRowsA + (wave >> 1) * (32 * kTM) + i * 32 + l;
   const int64_t col = (int64_t)tn * kRows + (wave & 1) * 128 + j * 32 + 8 * qq;
   if (row >= m || col >= n) return;
-  const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, row);
+  const float alpha = alpha_for(gsf_a, gsf_b, kEpi ? 0 : a_seg_rows, row);
   if constexpr (kEpi) {
     float z[8];
 #pragma unroll

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_kernel(
         if (splits > 1) {
           partial[((int64_t)split * m + row) * n + col] = acc[i][j][e];
         } else {
-          const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
+          const float al = !kEpi && a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
           const float v = __fmul_rn(al, __fmul_rn(acc[i][j][e], kAccUnscale));
           uint32_t y = f32_to_bf16(v);
           if constexpr (kEpi) y = finish_bf16(v, bias, col, ep, row * n + col);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) gemm_skinny_reduce(const float* __restric
   if (idx >= m * n) return;
   float acc = 0.0f;
   for (int sp = 0; sp < splits; ++sp) acc += partial[sp * m * n + idx];
-  const float alpha = alpha_for(gsf_a, gsf_b, a_seg_rows, idx / n);
+  const float alpha = alpha_for(gsf_a, gsf_b, kEpi ? 0 : a_seg_rows, idx / n);
   const float v = __fmul_rn(alpha, __fmul_rn(acc, kAccUnscale));
   uint32_t y = f32_to_bf16(v);
   if constexpr (kEpi) y = finish_bf16(v, bias, idx % n, ep, idx);
@@ -579,7 +579,7 @@ __attribute__((amdgpu_waves_per_eu(kFuse && kDW == 4 ? 5 : kOne && kDW == 4 ? 7 
     if (splits > 1) {
       partial[((int64_t)split * m + row) * n + col] = acc[e];
     } else {
-      const float al = a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
+      const float al = !kEpi && a_seg_rows > 0 ? alpha_for(gsf_a, gsf_b, a_seg_rows, row) : alpha;
       const float v = __fmul_rn(al, __fmul_rn(acc[e], kAccUnscale));
       uint32_t y = f32_to_bf16(v);
       if constexpr (kEpi) y = finish_bf16(v, bias, col, ep, row * n + col);

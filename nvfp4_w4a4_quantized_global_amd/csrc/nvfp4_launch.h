@@ -78,7 +78,8 @@ hipError_t launch_scale_layout(const uint8_t* src, uint8_t* dst, int64_t rows, i
                                hipStream_t s);
 
 // alpha = 1 / (gsf_a * gsf_b); with a_seg_rows > 0, row r of A takes gsf_a[r / a_seg_rows]
-// (one global scale per block of a_seg_rows rows), otherwise gsf_a[0] for every row.
+// (one global scale per block of a_seg_rows rows; not with an active epilogue), otherwise
+// gsf_a[0] for every row.
 hipError_t launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, int64_t k,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
                        const float* gsf_a, const float* gsf_b, int64_t a_seg_rows, const uint16_t* bias,
