@@ -697,7 +697,11 @@ class _NVFP4STEFn(torch.autograd.Function):
         packed_input = ctx.packed_input
         n, k = weight.shape
         g = ctx.group
-        grad_r = grad_y.reshape(ctx.res_shape) if ctx.needs_input_grad[7] else None
+        grad_r = None
+        if ctx.needs_input_grad[7]:
+            # grad_y itself, which autograd copies into the leaf's gradient while others hold it; a
+            # view of it would be kept as the gradient, and added to in place
+            grad_r = grad_y if grad_y.shape == ctx.res_shape else grad_y.reshape(ctx.res_shape).clone()
         gy2 = grad_y.reshape(-1, n)
         if z is not None:
             saved_z = z if z_scales is None else ck.Checkpoint(z, z_scales)
