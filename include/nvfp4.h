@@ -336,14 +336,17 @@ int nvfp4_gemm_epilogue(const uint8_t* x_codes_dev, const uint8_t* x_scale_dev, 
 /*
  * nvfp4_rmsnorm: the RMS norm with the residual's addition.  Per row of k values
  *     r = x + residual            (fp32, rounded to the residual's type; r = x without one)
- *     s = fp32(1 / sqrt(sum(r^2) / k + eps))      (the sum in fp64: the same bits in any order)
+ *     s = fp32(1 / sqrt(sum(r^2) / k + eps))      (the sum in fp64)
  *     y = bf16(fp32(fp32(r * s) * weight))
  * x_dev [rows][k] of x_dtype, residual_dev NULL or [rows][k] of residual_dtype (fp32 when
  * x is), weight_dev [k] of weight_dtype (each NVFP4_DTYPE_*).  residual_out_dev receives r
  * in the residual's type; it may be residual_dev, or x_dev of that type (unused without a
  * residual).  y_dev bf16 [rows][k].  ck_codes_dev / ck_scales_dev: both NULL, or y's 8-bit
  * checkpoint (nvfp4_checkpoint_pack of y_dev, bit for bit).  k: a multiple of 16, at most
- * NVFP4_NORM_MAX_K.  eps >= 0 (a zero row with eps 0 is 0 * infinity, NaN).
+ * NVFP4_NORM_MAX_K.  eps >= 0 (a zero row with eps 0 is 0 * infinity, NaN).  Every output
+ * form adds a row's squares in the same order, which k fixes, so all have the same s; another
+ * order would give the same bits but where the exact value lies within the fp64 sum's error of
+ * a rounding border of fp32.
  */
 int nvfp4_rmsnorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
                   const void* weight_dev, int weight_dtype, int64_t rows, int64_t k, float eps,

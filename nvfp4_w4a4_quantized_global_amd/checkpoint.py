@@ -78,7 +78,8 @@ def _empty_checkpoint(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
 @_on_device
 def checkpoint_pack(x: torch.Tensor, rotation_group: int = 0) -> Checkpoint:
     """bf16 [..., K] (K a multiple of 16) to its 8-bit checkpoint, after the optional block
-    rotation.  A value moves by at most 2^-4 of itself; infinities and NaN become NaN."""
+    rotation.  A value moves by at most 2^-4 of itself, or 2^-10 of its 32 values' power of two
+    where that is more; infinities and NaN become NaN."""
     x2, rows, k = _rows("x", x)
     ck = _empty_checkpoint(x2, int(rotation_group))
     check(lib().nvfp4_checkpoint_pack(_ptr(x2), rows, k, int(rotation_group), _ptr(ck.codes), _ptr(ck.scales),

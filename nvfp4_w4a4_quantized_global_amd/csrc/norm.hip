@@ -5,10 +5,12 @@
 //   s = fp32(1 / sqrt(sum(r^2) / K + eps))
 //   y = bf16(fp32(fp32(r * s) * w))
 //
-// The squares of bf16 and fp32 values are exact in fp64 and so is, to far below fp32's
-// spacing, their sum in any order: s has the same bits whichever kernel computes it, so
-// the codes of y are the quantizer's bit for bit.  The fp64 additions (one per value)
-// stay hidden under the HBM traffic that bounds every form.
+// The squares of bf16 and fp32 values are exact in fp64, and their sum is off by far less than
+// fp32's spacing.  Every output form adds a row in the same order, which row_shape fixes for
+// its K, so s has the same bits in all of them and the codes of y are the quantizer's bit for
+// bit.  (Another order would give the same s too, but where the value lies within the sum's
+// error of a rounding border of fp32.)  The fp64 additions (one per value) stay hidden under
+// the HBM traffic that bounds every form.
 //
 // A lane owns 16 consecutive values (one NVFP4 block, half a checkpoint block).  Rows of
 // at most 1024 values take a power-of-two group of lanes inside a wave, several rows per
