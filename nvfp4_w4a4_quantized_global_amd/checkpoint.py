@@ -127,7 +127,6 @@ def weight_grad(grad_y: torch.Tensor, ck: Checkpoint, dtype: torch.dtype = torch
 def swiglu_checkpoint(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tensor, Checkpoint, Checkpoint]:
     """:func:`swiglu` and the 8-bit checkpoints of ``gate`` and ``up``, in one pass."""
     g2, u2 = _gate_up(gate, up)
-    _require_device(gate.device, up=up)
     like = g2 if gate.dim() == 2 else g2.view(gate.shape)
     x = torch.empty_like(like)
     g, u = _empty_checkpoint(like), _empty_checkpoint(like)

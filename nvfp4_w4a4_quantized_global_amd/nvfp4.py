@@ -65,6 +65,15 @@ def _require_device(device: torch.device, **tensors: torch.Tensor | None) -> Non
             raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _operands(x: torch.Tensor, **tensors: torch.Tensor | None) -> None:
+    """:func:`_require_device` for a call's operands, by device index: a third of its host time
+    where all is well."""
+    index = x.get_device()
+    for t in tensors.values():
+        if t is not None and t.get_device() != index:
+            _require_device(x.device, **tensors)
+
+
 def _on_device(fn):
     """Runs ``fn`` with the device of its first GPU tensor current, however the arguments are
     given: the library launches on, sizes its workspaces for and keeps kernel attributes of
@@ -218,6 +227,7 @@ def quantize_activation(x: torch.Tensor, global_sf_x=None, rotation_group: int =
     scales = torch.empty((max(scale_bytes(m, k), 1),), dtype=torch.uint8, device=x.device)
     gsf = torch.empty((), dtype=torch.float32, device=x.device)
     g = None if global_sf_x is None else _scalar_f32(global_sf_x, x.device)
+    _operands(x, global_sf_x=g)
     ws = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
     check(lib().nvfp4_quantize_activation(_ptr(x), m, k, _ptr(g), int(rotation_group), _ptr(codes), _ptr(scales),
                                           _ptr(gsf), _ptr(ws), ws.numel(), _stream(x.device)))
@@ -251,6 +261,7 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         _require_cuda("bias", bias, torch.bfloat16)
         if bias.numel() != n:
             raise ValueError(f"bias must have {n} elements, got {bias.numel()}")
+    _operands(x_codes, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias, global_sf_x=gx, global_sf_w=gw)
     given = out
     if out is None:
         out = torch.empty(m, n, dtype=torch.bfloat16, device=x_codes.device)
@@ -266,8 +277,6 @@ def nvfp4_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, packed: torch.Tens
         workspace = None
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(x_codes.device, x_scales=x_scales, packed=packed, inv_scale=inv_scale, bias=bias,
-                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, n, x_codes.device, residual, preact, given, x_codes, x_scales)
         check(lib().nvfp4_gemm_epilogue(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(packed), _ptr(inv_scale), n, _ptr(gx),
                                         _ptr(gw), _ptr(bias), act, _ptr(residual), _ptr(preact), _ptr(out),
@@ -323,6 +332,7 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         _require_cuda("bias", bias, torch.bfloat16)
         if bias.numel() != out_features:
             raise ValueError(f"bias must have {out_features} elements, got {bias.numel()}")
+    _operands(x, packed=packed, inv_scale=inv_scale, bias=bias, global_sf_x=gx, global_sf_w=gw)
     m = x2d.shape[0]
     need = linear_workspace_bytes(m, k, out_features)
     if workspace is None:
@@ -334,8 +344,6 @@ def nvfp4_linear(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch.Tensor,
         out = torch.empty(m, out_features, dtype=torch.bfloat16, device=x.device)
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(x.device, packed=packed, inv_scale=inv_scale, bias=bias,
-                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, out_features, x.device, residual, preact, given, x2d)
         check(lib().nvfp4_linear_epilogue(_ptr(x2d), None, m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), int(rotation_group), act, _ptr(residual),
@@ -381,6 +389,7 @@ def nvfp4_linear_noalloc(x: torch.Tensor, packed: torch.Tensor, inv_scale: torch
         _require_cuda("bias", bias, torch.bfloat16)
         if bias.numel() != out_features:
             raise ValueError(f"bias must have {out_features} elements, got {bias.numel()}")
+    _operands(x, packed=packed, inv_scale=inv_scale, bias=bias, global_sf_x=gx, global_sf_w=gw)
     m = x2d.shape[0]
     given = out
     if out is None:
@@ -414,6 +423,7 @@ def amax(x: torch.Tensor, rotation_group: int = 0, out: torch.Tensor | None = No
             raise ValueError("accumulate needs the running value in out")
         out = torch.empty((), dtype=torch.float32, device=x.device)
     _require_cuda("out", out, torch.float32)
+    _operands(x, out=out)
     ws = torch.empty((quantize_workspace_bytes(),), dtype=torch.uint8, device=x.device)
     check(lib().nvfp4_amax(_ptr(x2d), x2d.shape[0], k, int(rotation_group), _ptr(out), int(bool(accumulate)), _ptr(ws),
                            ws.numel(), _stream(x.device)))
@@ -431,6 +441,7 @@ def _gate_up(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tensor, torch.
     u2 = u2 if u2.is_contiguous() else u2.contiguous()
     _require_cuda("gate", g2, torch.bfloat16, 2)
     _require_cuda("up", u2, torch.bfloat16, 2)
+    _operands(gate, up=up)
     return g2, u2
 
 
@@ -453,6 +464,7 @@ def quantize_swiglu(gate: torch.Tensor, up: torch.Tensor, global_sf_x=None
     scales = torch.empty((max(scale_bytes(m, k), 1),), dtype=torch.uint8, device=gate.device)
     gsf = torch.empty((), dtype=torch.float32, device=gate.device)
     g = None if global_sf_x is None else _scalar_f32(global_sf_x, gate.device)
+    _operands(gate, global_sf_x=g)
     ws = torch.empty((int(lib().nvfp4_quantize_swiglu_workspace_bytes(m, k)),), dtype=torch.uint8, device=gate.device)
     check(lib().nvfp4_quantize_swiglu(_ptr(g2), _ptr(u2), m, k, _ptr(g), _ptr(codes), _ptr(scales), _ptr(gsf),
                                       _ptr(ws), ws.numel(), _stream(gate.device)))
@@ -482,6 +494,7 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
         _require_cuda("bias", bias, torch.bfloat16)
         if bias.numel() != out_features:
             raise ValueError(f"bias must have {out_features} elements, got {bias.numel()}")
+    _operands(gate, packed=packed, inv_scale=inv_scale, bias=bias, global_sf_x=gx, global_sf_w=gw)
     if workspace is None:
         need = int(lib().nvfp4_linear_swiglu_workspace_bytes(m, k, out_features))
         workspace = torch.empty((need,), dtype=torch.uint8, device=gate.device)
@@ -492,8 +505,6 @@ def nvfp4_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, packed: torch.Tens
         out = torch.empty((m, out_features), dtype=torch.bfloat16, device=gate.device)
     act = _activation_code(activation)
     if act or residual is not None or preact is not None:
-        _require_device(gate.device, up=up, packed=packed, inv_scale=inv_scale, bias=bias,
-                        global_sf_x=gx, global_sf_w=gw, workspace=workspace)
         residual = _epilogue_tensors(m, out_features, gate.device, residual, preact, given, g2, u2)
         check(lib().nvfp4_linear_epilogue(_ptr(g2), _ptr(u2), m, k, _ptr(packed), _ptr(inv_scale), _ptr(gw), _ptr(bias),
                                           out_features, _ptr(gx), 0, act, _ptr(residual), _ptr(preact), _ptr(out),
@@ -523,6 +534,7 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, global_sf, dtype: tor
     if scales.numel() < scale_bytes(rows, k):
         raise ValueError("scales is smaller than nvfp4_scale_bytes(rows, K)")
     g = _scalar_f32(global_sf, packed.device)
+    _operands(packed, scales=scales, global_sf=g)
     out = torch.empty(rows, k, dtype=dtype, device=packed.device)
     check(lib().nvfp4_dequantize(_ptr(packed), _ptr(scales), rows, k, _ptr(g), _ptr(out), codes[dtype],
                                  _stream(packed.device)))
@@ -596,6 +608,7 @@ def nvfp4_linear_segmented(x: torch.Tensor, segments: int, packed: torch.Tensor,
         _require_cuda("gsf_out", gsf_out, torch.float32)
         if gsf_out.numel() < segments:
             raise ValueError(f"gsf_out must hold {segments} values")
+    _operands(x, packed=packed, inv_scale=inv_scale, bias=bias, global_sf_w=gw, gsf_out=gsf_out)
     m = x2d.shape[0]
     need = linear_segmented_workspace_bytes(segments, seg_rows, k, out_features)
     if workspace is None:
