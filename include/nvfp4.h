@@ -67,6 +67,8 @@ enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_GEL
 #define NVFP4_WORKSPACE_ALIGN 256
 #define NVFP4_CHECKPOINT_BLOCK 32
 #define NVFP4_NORM_MAX_K 16384
+#define NVFP4_FP8_BLOCK 128
+#define NVFP4_FP8_MAX_DIM ((int64_t)1 << 22)             /* K and N of the 8-bit block calls */
 #define NVFP4_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)   /* nvfp4_linear_noalloc's fixed device scratch */
 
 /* Alignment.  Every call checks its pointers and returns NVFP4_ERR_ARG for a misaligned
@@ -79,9 +81,10 @@ enum { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2, NVFP4_ACT_GEL
  *     kernels take wide stores and loads only where the address allows them);
  *   - fp32 scalars (global scales, gsf_out, amax): 4 bytes;
  *   - workspaces: NVFP4_WORKSPACE_ALIGN;
- *   - every array of the RMS norm, checkpoint and gradient calls: 16 bytes, except fp32
- *     scalars and the norm's grad_w (4), checkpoint scales (bytes: any address), and the
- *     residual and preact of a linear's epilogue (2).
+ *   - every array of the norm, checkpoint, 8-bit block and gradient calls: 16 bytes, except
+ *     fp32 scalars, the norms' grad_w and grad_b, the 8-bit blocks' scales and column sums (4),
+ *     checkpoint scales (bytes: any address), and the out, bias, residual and preact of a
+ *     linear (2).
  * The scale-layout converters access bytes and need no alignment.
  * Outputs overlap neither each other nor inputs, except where a call says so. */
 
@@ -447,6 +450,110 @@ int nvfp4_scale_from_canonical(const uint8_t* canonical_dev, uint8_t* layout_dev
 
 /* Message for the last non-zero return on the calling thread ("" if none). */
 const char* nvfp4_last_error(void);
+
+/*
+ * nvfp4_layernorm: the layer norm with the residual's addition.  Per row of k values
+ *     r  = x + residual           (as nvfp4_rmsnorm)
+ *     mu = sum(r) / k,   s = fp32(1 / sqrt(sum((r - mu)^2) / k + eps))      (both in fp64)
+ *     y  = bf16(fp32(fp32(fp32(r - mu) * s) * weight) + bias)
+ * bias_dev [k] of weight_dtype, or NULL.  The other arguments, types, limits and y's 8-bit
+ * checkpoint are nvfp4_rmsnorm's.  A row with an infinity or NaN is NaN.
+ */
+int nvfp4_layernorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                    const void* weight_dev, const void* bias_dev, int weight_dtype, int64_t rows, int64_t k,
+                    float eps, void* residual_out_dev, void* y_dev, uint8_t* ck_codes_dev, uint8_t* ck_scales_dev,
+                    void* stream);
+
+/* nvfp4_quantize_layernorm: nvfp4_quantize_activation (no rotation) of nvfp4_layernorm's y, which
+ * is never written; arguments and workspace as for nvfp4_quantize_rmsnorm. */
+size_t nvfp4_quantize_layernorm_workspace_bytes(int64_t rows);
+int nvfp4_quantize_layernorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                             const void* weight_dev, const void* bias_dev, int weight_dtype, int64_t rows, int64_t k,
+                             float eps, const float* global_sf_dev, void* residual_out_dev, uint8_t* codes_dev,
+                             uint8_t* scales_dev, float* gsf_out_dev, void* workspace_dev, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * nvfp4_layernorm_backward: the gradient of the norm at r, the rounding of y taken as the
+ * identity.  With n = (r - mu) s and g = grad_y * weight
+ *     grad_r = s (g - mean(g) - n mean(g n)) + grad_residual,
+ *     grad_w = sum over rows of grad_y n,   grad_b = sum over rows of grad_y.
+ * grad_w_dev, grad_b_dev: fp32 [k], both or neither (then no workspace).  The row partials are
+ * added in a fixed order: results repeat bit for bit.  Other arguments and the range of rows as
+ * for nvfp4_rmsnorm_backward.
+ */
+size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t k);
+int nvfp4_layernorm_backward(const void* grad_y_dev, const void* r_dev, int r_dtype, const void* weight_dev,
+                             int weight_dtype, const void* grad_residual_dev, int64_t rows, int64_t k, float eps,
+                             void* grad_r_dev, float* grad_w_dev, float* grad_b_dev, void* workspace_dev,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit block codes: E4M3 (bias 7, finite max 448) with one fp32 scale per block, 128 values of
+ * an activation's row or a 128 x 128 tile of a weight (the last blocks may be smaller):
+ *     a = largest finite magnitude of the block, at least 448 * 2^-110,
+ *     scale = fp32(a / 448),   code = E4M3_nearest_even(fp32(v * fp32(448 / a))),
+ * so value = code * scale.  A code is off by at most 2^-4 of the value, or 2^-10 of the scale where
+ * that is more.  Infinities and NaN become NaN codes and do not enter the scale.
+ * Activations: codes [rows][k], scales [ceil(k / 128)][rows] (block-major).  Weights: codes [n][k],
+ * scales [ceil(n / 128)][ceil(k / 128)].  k (and n where a call says so): a multiple of 16; k and n
+ * at most NVFP4_FP8_MAX_DIM.
+ *
+ * nvfp4_fp8_quantize_activation: x_dev bf16 [rows][k]; up_dev NULL, or the values are
+ * nvfp4_swiglu(x, up).  column_sum_dev: NULL, or fp32 [k] that receives the sums of x over its rows
+ * (a linear's bias gradient when x is its output's; added in a fixed order; not with up), with a
+ * workspace of nvfp4_fp8_quantize_workspace_bytes(rows, k).
+ */
+size_t nvfp4_fp8_quantize_workspace_bytes(int64_t rows, int64_t k);
+int nvfp4_fp8_quantize_activation(const void* x_dev, const void* up_dev, int64_t rows, int64_t k, uint8_t* codes_dev,
+                                  float* scales_dev, float* column_sum_dev, void* workspace_dev,
+                                  size_t workspace_bytes, void* stream);
+
+/* nvfp4_fp8_quantize_weight: w_dev [n][k] of w_dtype.  codes_t_dev / scales_t_dev: both NULL, or the
+ * transposed codes [k][n] and scales [ceil(k / 128)][ceil(n / 128)], the same values (a weight for
+ * the input's gradient; n a multiple of 16 then). */
+int nvfp4_fp8_quantize_weight(const void* w_dev, int w_dtype, int64_t n, int64_t k, uint8_t* codes_dev,
+                              float* scales_dev, uint8_t* codes_t_dev, float* scales_t_dev, void* stream);
+
+/* nvfp4_fp8_dequantize: fp32(code * scale) as bf16 or fp32 [rows][k]; weight 0: scales of an
+ * activation, 1: of a weight. */
+int nvfp4_fp8_dequantize(const uint8_t* codes_dev, const float* scales_dev, int64_t rows, int64_t k, int weight,
+                         void* out_dev, int out_dtype, void* stream);
+
+/* nvfp4_fp8_quantize_rmsnorm, nvfp4_fp8_quantize_layernorm: nvfp4_fp8_quantize_activation of
+ * nvfp4_rmsnorm's or nvfp4_layernorm's y, which is never written: the same codes and scales, bit for
+ * bit. */
+int nvfp4_fp8_quantize_rmsnorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                               const void* weight_dev, int weight_dtype, int64_t rows, int64_t k, float eps,
+                               void* residual_out_dev, uint8_t* codes_dev, float* scales_dev, void* stream);
+int nvfp4_fp8_quantize_layernorm(const void* x_dev, int x_dtype, const void* residual_dev, int residual_dtype,
+                                 const void* weight_dev, const void* bias_dev, int weight_dtype, int64_t rows,
+                                 int64_t k, float eps, void* residual_out_dev, uint8_t* codes_dev, float* scales_dev,
+                                 void* stream);
+
+/*
+ * nvfp4_fp8_gemm: the product of an activation's codes x [m][k] and a weight's w [n][k],
+ *     z[i][j] = sum_b sx[i][b] sw[j / 128][b] sum_{k in b} qx[i][k] qw[j][k] + bias[j],
+ *     out = bf16(act(z) + residual),
+ * in fp32 with that one rounding (summation order fixed by the shapes and the workspace given).
+ * activation, residual_dev and preact_dev as for nvfp4_gemm_epilogue; bias_dev bf16 [n] or NULL.
+ * workspace_dev: NULL, or nvfp4_fp8_gemm_workspace_bytes(m, k, n) bytes for the partial sums of tiles
+ * split along K; without it they are not split.
+ */
+size_t nvfp4_fp8_gemm_workspace_bytes(int64_t m, int64_t k, int64_t n);
+int nvfp4_fp8_gemm(const uint8_t* x_codes_dev, const float* x_scales_dev, int64_t m, int64_t k,
+                   const uint8_t* w_codes_dev, const float* w_scales_dev, int64_t n, const void* bias_dev,
+                   int activation, const void* residual_dev, void* preact_dev, void* out_dev, void* workspace_dev,
+                   size_t workspace_bytes, void* stream);
+
+/* nvfp4_fp8_linear: nvfp4_fp8_quantize_activation of x_dev (and up_dev, NULL for none), then
+ * nvfp4_fp8_gemm; one launch for one or a few rows.  workspace:
+ * nvfp4_fp8_linear_workspace_bytes(m, k, n). */
+size_t nvfp4_fp8_linear_workspace_bytes(int64_t m, int64_t k, int64_t n);
+int nvfp4_fp8_linear(const void* x_dev, const void* up_dev, int64_t m, int64_t k, const uint8_t* w_codes_dev,
+                     const float* w_scales_dev, const void* bias_dev, int64_t n, int activation,
+                     const void* residual_dev, void* preact_dev, void* out_dev, void* workspace_dev,
+                     size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

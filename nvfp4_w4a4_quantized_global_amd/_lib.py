@@ -73,6 +73,22 @@ SIGNATURES = {
     "nvfp4_activation_backward": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp]),
     "nvfp4_weight_grad_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "nvfp4_weight_grad": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _sz, _vp]),
+    "nvfp4_layernorm": (_int, [_vp, _int, _vp, _int, _vp, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_quantize_layernorm_workspace_bytes": (_sz, [_i64]),
+    "nvfp4_quantize_layernorm": (_int, [_vp, _int, _vp, _int, _vp, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _sz, _vp]),
+    "nvfp4_layernorm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_layernorm_backward": (_int, [_vp, _vp, _int, _vp, _int, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_fp8_quantize_workspace_bytes": (_sz, [_i64, _i64]),
+    "nvfp4_fp8_quantize_activation": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_fp8_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_fp8_dequantize": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _int, _vp]),
+    "nvfp4_fp8_quantize_rmsnorm": (_int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp]),
+    "nvfp4_fp8_quantize_layernorm": (_int, [_vp, _int, _vp, _int, _vp, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp]),
+    "nvfp4_fp8_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_fp8_gemm": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_fp8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_fp8_linear": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
     "nvfp4_scale_to_canonical": (_int, [_vp, _vp, _i64, _i64, _vp]),
     "nvfp4_scale_from_canonical": (_int, [_vp, _vp, _i64, _i64, _vp]),
     "nvfp4_last_error": (ctypes.c_char_p, []),

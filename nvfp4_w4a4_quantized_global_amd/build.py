@@ -16,7 +16,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_NAME = "libnvfp4.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ("api.hip", "quantize.hip", "gemm.hip", "gemm_pipe.hip", "gemm_skinny.hip", "norm.hip", "checkpoint.hip",
-           "weight_grad.hip")
+           "weight_grad.hip", "layernorm.hip", "fp8.hip", "gemm_fp8.hip")
 ARCH = "gfx950"
 
 # -ffp-contract=off: the quantizer's multiply/divide sequence must round like the

@@ -331,6 +331,45 @@ int norm_inputs(const char* fn, const void* x, int x_dtype, const void* residual
   return NVFP4_OK;
 }
 
+// The layer norm's inputs: the RMS norm's and a bias of the weight's type.
+int layernorm_inputs(const char* fn, const void* x, int x_dtype, const void* residual, int residual_dtype,
+                     const void* weight, const void* bias, int weight_dtype, int64_t rows, int64_t k, float eps,
+                     void* residual_out, nvfp4::NormForward* a) {
+  if (int rc = norm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, weight_dtype, rows, k, eps, residual_out, a))
+    return rc;
+  if (int rc = check_aligned(fn, "bias", bias)) return rc;
+  a->b = bias;
+  return NVFP4_OK;
+}
+
+// Shapes and pointers of 8-bit block codes.
+int check_fp8_shape(const char* fn, int64_t rows, int64_t k) {
+  if (int rc = check_rows_k(fn, rows, k, true)) return rc;
+  if (k > NVFP4_FP8_MAX_DIM)
+    return fail(NVFP4_ERR_SHAPE, "%s: K must be at most %lld, got %lld", fn, (long long)NVFP4_FP8_MAX_DIM, (long long)k);
+  return NVFP4_OK;
+}
+int check_fp8_out_features(const char* fn, int64_t n) {
+  if (n <= 0 || n > NVFP4_FP8_MAX_DIM)
+    return fail(NVFP4_ERR_SHAPE, "%s: out_features must be in [1, %lld], got %lld", fn, (long long)NVFP4_FP8_MAX_DIM,
+                (long long)n);
+  return NVFP4_OK;
+}
+int check_fp8_operand(const char* fn, const char* codes_name, const void* codes, const char* scales_name,
+                      const void* scales) {
+  if (!codes || !scales) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, codes_name, codes)) return rc;
+  return check_align(fn, scales_name, scales, 4);
+}
+int check_fp8_output(const char* fn, const void* out, const void* bias) {
+  if (!out) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_align(fn, "out", out, 2)) return rc;
+  return check_align(fn, "bias", bias, 2);
+}
+size_t fp8_scale_bytes(int64_t m, int64_t k) {
+  return align_up((size_t)((k + NVFP4_FP8_BLOCK - 1) / NVFP4_FP8_BLOCK) * (size_t)m * sizeof(float));
+}
+
 int check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
   if (need > 0 && (!workspace || bytes < need || ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN)))
     return fail(NVFP4_ERR_WORKSPACE, "%s: need a %d-byte aligned workspace of %zu bytes, got %zu", fn,
@@ -913,6 +952,294 @@ int nvfp4_weight_grad(const void* grad_y, int64_t m, int64_t n, const uint8_t* c
                                               out_dtype == NVFP4_DTYPE_BF16, workspace,
                                               workspace != nullptr ? workspace_bytes : 0, nvfp4::compute_units(),
                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_layernorm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                    const void* bias, int weight_dtype, int64_t rows, int64_t k, float eps, void* residual_out, void* y,
+                    uint8_t* ck_codes, uint8_t* ck_scales, void* stream) {
+  const char* fn = "nvfp4_layernorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = layernorm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, bias, weight_dtype, rows, k, eps,
+                                residual_out, &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!y) return fail(NVFP4_ERR_ARG, "%s: y must not be NULL", fn);
+  if ((ck_codes == nullptr) != (ck_scales == nullptr))
+    return fail(NVFP4_ERR_ARG, "%s: checkpoint codes and scales go together", fn);
+  if (int rc = check_aligned(fn, "y", y)) return rc;
+  if (int rc = check_aligned(fn, "ck_codes", ck_codes)) return rc;
+  a.mode = nvfp4::kNormOut;
+  a.y = static_cast<uint16_t*>(y);
+  a.codes = ck_codes;
+  a.scales = ck_scales;
+  return hip_status(nvfp4::launch_layernorm(a, true, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_quantize_layernorm_workspace_bytes(int64_t rows) {
+  if (rows <= 1) return 0;   // one row is one workgroup's: nothing to hand over
+  return align_up(sizeof(float) * nvfp4::kNormPartials) + align_up(sizeof(float) * (size_t)rows) +
+         align_up(sizeof(double) * (size_t)rows);
+}
+
+int nvfp4_quantize_layernorm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                             const void* bias, int weight_dtype, int64_t rows, int64_t k, float eps,
+                             const float* global_sf, void* residual_out, uint8_t* codes, uint8_t* scales,
+                             float* gsf_out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_quantize_layernorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = layernorm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, bias, weight_dtype, rows, k, eps,
+                                residual_out, &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!codes || !scales) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_nvfp4_operand(fn, "codes", codes, "scales", scales)) return rc;
+  if (int rc = check_align(fn, "global_sf", global_sf, 4)) return rc;
+  if (int rc = check_align(fn, "gsf_out", gsf_out, 4)) return rc;
+  const size_t need = global_sf == nullptr ? nvfp4_quantize_layernorm_workspace_bytes(rows) : 0;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes, need)) return rc;
+  a.mode = global_sf != nullptr ? nvfp4::kNormStatic : nvfp4::kNormDynamic;
+  a.codes = codes;
+  a.scales = scales;
+  a.gsf = global_sf;
+  a.gsf_out = gsf_out;
+  if (need > 0) {
+    uint8_t* p = static_cast<uint8_t*>(workspace);
+    a.partials = reinterpret_cast<float*>(p);
+    a.rstd = reinterpret_cast<float*>(p += align_up(sizeof(float) * nvfp4::kNormPartials));
+    a.mean = reinterpret_cast<double*>(p + align_up(sizeof(float) * (size_t)rows));
+  }
+  return hip_status(nvfp4::launch_layernorm(a, true, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t k) {
+  if (rows < 0 || k <= 0 || k > nvfp4::kNormMaxK || k % NVFP4_BLOCK_SIZE) return 0;
+  return align_up(sizeof(float) * nvfp4::layernorm_backward_partial_floats(rows, k));
+}
+
+int nvfp4_layernorm_backward(const void* grad_y, const void* r, int r_dtype, const void* weight, int weight_dtype,
+                             const void* grad_residual, int64_t rows, int64_t k, float eps, void* grad_r,
+                             float* grad_w, float* grad_b, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_layernorm_backward";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_norm(fn, rows, k, eps)) return rc;
+  if (!is_dtype(r_dtype) || !is_dtype(weight_dtype))
+    return fail(NVFP4_ERR_ARG, "%s: dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if ((grad_w == nullptr) != (grad_b == nullptr))
+    return fail(NVFP4_ERR_ARG, "%s: grad_w and grad_b go together", fn);
+  if (rows == 0 && grad_w == nullptr) return NVFP4_OK;
+  if (rows > 0 && (!grad_y || !r || !weight || !grad_r)) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "grad_y", grad_y)) return rc;
+  if (int rc = check_aligned(fn, "r", r)) return rc;
+  if (int rc = check_aligned(fn, "weight", weight)) return rc;
+  if (int rc = check_aligned(fn, "grad_residual", grad_residual)) return rc;
+  if (int rc = check_aligned(fn, "grad_r", grad_r)) return rc;
+  if (int rc = check_align(fn, "grad_w", grad_w, 4)) return rc;
+  if (int rc = check_align(fn, "grad_b", grad_b, 4)) return rc;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes,
+                               grad_w != nullptr ? nvfp4_layernorm_backward_workspace_bytes(rows, k) : 0))
+    return rc;
+  nvfp4::NormBackward a{};
+  a.gy = static_cast<const uint16_t*>(grad_y);
+  a.r = r;
+  a.w = weight;
+  a.grad_residual = grad_residual;
+  a.rows = rows;
+  a.k = k;
+  a.eps = (double)eps;
+  a.stream_f32 = r_dtype == NVFP4_DTYPE_F32;
+  a.w_f32 = weight_dtype == NVFP4_DTYPE_F32;
+  a.grad_r = grad_r;
+  a.grad_w = grad_w;
+  a.grad_b = grad_b;
+  a.partials = static_cast<float*>(workspace);
+  return hip_status(nvfp4::launch_layernorm_backward(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_fp8_quantize_workspace_bytes(int64_t rows, int64_t k) {
+  if (rows < 0 || k <= 0) return 0;
+  return align_up(sizeof(float) * nvfp4::fp8_column_sum_floats(rows, k));
+}
+
+int nvfp4_fp8_quantize_activation(const void* x, const void* up, int64_t rows, int64_t k, uint8_t* codes, float* scales,
+                                  float* column_sum, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_fp8_quantize_activation";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, rows, k)) return rc;
+  if (column_sum != nullptr && up != nullptr) return fail(NVFP4_ERR_ARG, "%s: no column sums of a SwiGLU product", fn);
+  if (rows == 0 && column_sum == nullptr) return NVFP4_OK;
+  if (rows > 0) {
+    if (!x) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+    if (int rc = check_aligned(fn, "x", x)) return rc;
+    if (int rc = check_aligned(fn, "up", up)) return rc;
+    if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  }
+  if (int rc = check_align(fn, "column_sum", column_sum, 4)) return rc;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes,
+                               column_sum != nullptr ? nvfp4_fp8_quantize_workspace_bytes(rows, k) : 0))
+    return rc;
+  return hip_status(nvfp4::launch_fp8_quantize(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up), rows,
+                                               k, codes, scales, column_sum, static_cast<float*>(workspace),
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_fp8_quantize_weight(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* codes, float* scales,
+                              uint8_t* codes_t, float* scales_t, void* stream) {
+  const char* fn = "nvfp4_fp8_quantize_weight";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, n, k)) return rc;
+  if (int rc = check_fp8_out_features(fn, n)) return rc;
+  if (!is_dtype(w_dtype)) return fail(NVFP4_ERR_ARG, "%s: dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if ((codes_t == nullptr) != (scales_t == nullptr))
+    return fail(NVFP4_ERR_ARG, "%s: transposed codes and scales go together", fn);
+  if (codes_t != nullptr && n % NVFP4_BLOCK_SIZE)
+    return fail(NVFP4_ERR_SHAPE, "%s: transposed codes need out_features divisible by %d, got %lld", fn,
+                NVFP4_BLOCK_SIZE, (long long)n);
+  if (!w) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "w", w)) return rc;
+  if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  if (codes_t != nullptr)
+    if (int rc = check_fp8_operand(fn, "codes_t", codes_t, "scales_t", scales_t)) return rc;
+  return hip_status(nvfp4::launch_fp8_quantize_weight(w, w_dtype == NVFP4_DTYPE_F32, n, k, codes, scales, codes_t,
+                                                      scales_t, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t k, int weight, void* out,
+                         int out_dtype, void* stream) {
+  const char* fn = "nvfp4_fp8_dequantize";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, rows, k)) return rc;
+  if (!is_dtype(out_dtype))
+    return fail(NVFP4_ERR_ARG, "%s: out_dtype must be NVFP4_DTYPE_BF16 or NVFP4_DTYPE_F32", fn);
+  if (rows == 0) return NVFP4_OK;
+  if (!out) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  if (int rc = check_aligned(fn, "out", out)) return rc;
+  return hip_status(nvfp4::launch_fp8_dequantize(codes, scales, rows, k, weight != 0, out,
+                                                 out_dtype == NVFP4_DTYPE_BF16, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_fp8_quantize_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                               int weight_dtype, int64_t rows, int64_t k, float eps, void* residual_out,
+                               uint8_t* codes, float* scales, void* stream) {
+  const char* fn = "nvfp4_fp8_quantize_rmsnorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = norm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, weight_dtype, rows, k, eps, residual_out,
+                           &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  a.mode = nvfp4::kNormFp8;
+  a.codes = codes;
+  a.block_scales = scales;
+  return hip_status(nvfp4::launch_layernorm(a, false, static_cast<hipStream_t>(stream)), fn);
+}
+
+int nvfp4_fp8_quantize_layernorm(const void* x, int x_dtype, const void* residual, int residual_dtype,
+                                 const void* weight, const void* bias, int weight_dtype, int64_t rows, int64_t k,
+                                 float eps, void* residual_out, uint8_t* codes, float* scales, void* stream) {
+  const char* fn = "nvfp4_fp8_quantize_layernorm";
+  Range call(fn);
+  g_err[0] = 0;
+  nvfp4::NormForward a;
+  if (int rc = layernorm_inputs(fn, x, x_dtype, residual, residual_dtype, weight, bias, weight_dtype, rows, k, eps,
+                                residual_out, &a))
+    return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  a.mode = nvfp4::kNormFp8;
+  a.codes = codes;
+  a.block_scales = scales;
+  return hip_status(nvfp4::launch_layernorm(a, true, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t nvfp4_fp8_gemm_workspace_bytes(int64_t m, int64_t k, int64_t n) {
+  if (m <= 0 || k <= 0 || n <= 0) return 0;
+  return align_up(nvfp4::gemm_fp8_workspace_bytes(m, k, n, nvfp4::compute_units()));
+}
+
+int nvfp4_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t m, int64_t k, const uint8_t* w_codes,
+                   const float* w_scales, int64_t n, const void* bias, int activation, const void* residual,
+                   void* preact, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_fp8_gemm";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, m, k)) return rc;
+  if (int rc = check_fp8_out_features(fn, n)) return rc;
+  nvfp4::Epilogue ep;
+  if (int rc = make_epilogue(fn, activation, residual, preact, out, &ep)) return rc;
+  if (m == 0) return NVFP4_OK;
+  if (int rc = check_fp8_operand(fn, "x_codes", x_codes, "x_scales", x_scales)) return rc;
+  if (int rc = check_fp8_operand(fn, "w_codes", w_codes, "w_scales", w_scales)) return rc;
+  if (int rc = check_fp8_output(fn, out, bias)) return rc;
+  if (workspace != nullptr && ((uintptr_t)workspace % NVFP4_WORKSPACE_ALIGN))
+    return fail(NVFP4_ERR_WORKSPACE, "%s: workspace must be %d-byte aligned", fn, NVFP4_WORKSPACE_ALIGN);
+  return hip_status(nvfp4::launch_gemm_fp8(x_codes, x_scales, m, k, w_codes, w_scales, n,
+                                           static_cast<const uint16_t*>(bias), ep, static_cast<uint16_t*>(out),
+                                           workspace, workspace != nullptr ? workspace_bytes : 0,
+                                           nvfp4::compute_units(), static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+size_t nvfp4_fp8_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
+  if (m <= 0 || k <= 0 || n <= 0) return 0;
+  if (nvfp4::linear_fp8_fused_supported(m, k, n)) return 0;
+  return align_up((size_t)m * (size_t)k) + fp8_scale_bytes(m, k) + nvfp4_fp8_gemm_workspace_bytes(m, k, n);
+}
+
+int nvfp4_fp8_linear(const void* x, const void* up, int64_t m, int64_t k, const uint8_t* w_codes, const float* w_scales,
+                     const void* bias, int64_t n, int activation, const void* residual, void* preact, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "nvfp4_fp8_linear";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, m, k)) return rc;
+  if (int rc = check_fp8_out_features(fn, n)) return rc;
+  nvfp4::Epilogue ep;
+  if (int rc = make_epilogue(fn, activation, residual, preact, out, &ep)) return rc;
+  if (m == 0) return NVFP4_OK;
+  if (!x) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "x", x)) return rc;
+  if (int rc = check_aligned(fn, "up", up)) return rc;
+  if (int rc = check_fp8_operand(fn, "w_codes", w_codes, "w_scales", w_scales)) return rc;
+  if (int rc = check_fp8_output(fn, out, bias)) return rc;
+  if (int rc = check_workspace(fn, workspace, workspace_bytes, nvfp4_fp8_linear_workspace_bytes(m, k, n))) return rc;
+  const uint16_t* b = static_cast<const uint16_t*>(bias);
+  uint16_t* o = static_cast<uint16_t*>(out);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (nvfp4::linear_fp8_fused_supported(m, k, n)) {
+    Range stage("nvfp4.quantize+gemm");
+    return hip_status(nvfp4::launch_linear_fp8_fused(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up),
+                                                     m, k, w_codes, w_scales, n, b, ep, o, s),
+                      fn);
+  }
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + align_up((size_t)m * (size_t)k));
+  uint8_t* gemm = reinterpret_cast<uint8_t*>(scales) + fp8_scale_bytes(m, k);
+  {
+    Range stage("nvfp4.quantize");
+    if (int rc = hip_status(nvfp4::launch_fp8_quantize(static_cast<const uint16_t*>(x),
+                                                       static_cast<const uint16_t*>(up), m, k, codes, scales, nullptr,
+                                                       nullptr, s),
+                            fn))
+      return rc;
+  }
+  Range stage("nvfp4.gemm");
+  return hip_status(nvfp4::launch_gemm_fp8(codes, scales, m, k, w_codes, w_scales, n, b, ep, o, gemm,
+                                           nvfp4_fp8_gemm_workspace_bytes(m, k, n), nvfp4::compute_units(), s),
                     fn);
 }
 

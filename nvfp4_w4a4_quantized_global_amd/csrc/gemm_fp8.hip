@@ -1,0 +1,561 @@
+// The product of 8-bit block codes on gfx950 matrix cores, with the linear's epilogue:
+//
+//   out[i, j] = bf16(act(sum_b sx[i, b] sw[j / 128, b] sum_{k in b} qx[i, k] qw[j, k] + bias[j]) + residual[i, j])
+//
+// qx, qw E4M3 codes, b the 128-wide blocks of K, sx one fp32 scale per row and block, sw one per
+// 128 x 128 tile of the weight.  v_mfma_f32_16x16x128_f8f6f4 multiplies one block of 16 x 16
+// outputs in one instruction (32 cycles), from zero; its four results a lane are then multiplied by
+// the block's scale and added to the fp32 accumulators by four FMAs (16 cycles of the vector unit,
+// beside the next MFMA).  The product is computed transposed, weight first, so that a lane's four
+// results are four columns of one activation row and share one scale sx * sw.  The instruction's
+// own scale operands only take powers of two.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "fp8_device.h"
+#include "gemm_common.h"
+#include "nvfp4_device.h"
+#include "nvfp4_launch.h"
+
+namespace nvfp4 {
+namespace {
+
+using namespace gemm;
+
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// One block of 16 x 16 outputs: lane l holds row l % 16 of each operand and the same 32 of its
+// 128 codes in both (which 32 does not matter to the sum); entry e of the result is row
+// 4 (l / 16) + e of w, row l % 16 of x.
+__device__ __forceinline__ float4v block_mfma(const int8v& w, const int8v& x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, float4v{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ void add_scaled(float4v& acc, float s, const float4v& t) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = fmaf(s, t[e], acc[e]);
+}
+
+// A buffer of `bytes` bytes from p (wave-uniform): loads past them return zero.
+__device__ __forceinline__ u32x4_t buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer here
+static_assert(256 * kFp8MaxK < (int64_t)kOutside, "a tile's rows fit 31-bit offsets");
+
+// Global -> LDS copies of 16 and 4 bytes a lane, to a wave-uniform LDS base plus the lane's.
+// Inline asm so that the compiler does not hold LDS reads back for them: the loop waits for them
+// before the barrier that precedes those.
+__device__ __forceinline__ void copy16_to_lds(u32x4_t rsrc, uint32_t offset, uint8_t* dst) {
+  asm volatile("buffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(offset), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ void copy4_to_lds(u32x4_t rsrc, uint32_t offset, uint8_t* dst) {
+  asm volatile("buffer_load_dword %1, %2, 0 offen lds"
+               :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(offset), "s"(rsrc) : "memory");
+}
+// Waits for this wave's copies and LDS accesses, then the workgroup barrier.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+// Orders this wave's LDS accesses around a point.
+__device__ __forceinline__ void lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// ---- many rows: tiles ----
+
+// kWM x kWN waves, each kTM x kTN MFMA tiles of 16 x 16.  A stage holds one block of K of both
+// operands (128 bytes a row) and the activations' scales.
+template <int kWM_, int kWN_, int kTM_, int kTN_>
+struct Geo {
+  static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_;
+  static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
+  static constexpr int kBM = 16 * kWM * kTM, kBN = 16 * kWN * kTN;
+  static constexpr int kOffB = 128 * kBM, kOffS = kOffB + 128 * kBN, kStage = kOffS + 4 * kBM;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kCopyA = kBM / 8 / kWaves, kCopyB = kBN / 8 / kWaves;   // copy instructions of a wave
+  static constexpr int kEpiRow = 16 * kTN + 4;                                  // words per staged output row
+  static constexpr int kEpiWave = 16 * kEpiRow * 4;
+  static_assert(kTN == 4, "a wave's 64 columns: eight lanes a row in the epilogue, one weight scale");
+  static_assert(kCopyA * 8 * kWaves == kBM && kCopyB * 8 * kWaves == kBN && kBM % 64 == 0, "whole copies");
+  static_assert(kWaves * kEpiWave <= kLds, "epilogue staging fits in the stages");
+};
+using Large = Geo<2, 4, 8, 4>;   // 256 x 256, one workgroup of eight waves per compute unit
+using Small = Geo<2, 2, 4, 4>;   // 128 x 128, two workgroups of four
+
+// Tile index -> (tile row, tile column): bands of kGroupM tile rows, column-major inside a band,
+// so that the tiles resident on one XCD share operand panels in its L2.
+constexpr int kGroupM = 4;
+__device__ __forceinline__ void tile_coords(int tile, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int band = tile / (kGroupM * tiles_n);
+  const int first = band * kGroupM;
+  const int rows = min(tiles_m - first, kGroupM);
+  const int in_band = tile - band * kGroupM * tiles_n;
+  tm = first + in_band % rows;
+  tn = in_band / rows;
+}
+
+// kSplit: the tiles from tile0 on, each split along K into `splits` workgroups that write fp32
+// partial tiles; otherwise whole tiles with the epilogue of activation kAct.
+template <class G, bool kSplit, int kAct>
+__global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
+    const uint8_t* __restrict__ a_codes, const float* __restrict__ a_scales, int64_t m, int64_t k,
+    const uint8_t* __restrict__ b_codes, const float* __restrict__ b_scales, int64_t n,
+    const uint16_t* __restrict__ bias, uint16_t* out, int tiles_m, int tiles_n, int tile0, int splits,
+    float* __restrict__ partial, const Epilogue ep) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int kTM = G::kTM, kTN = G::kTN;
+  // Workgroups are dealt round-robin to the 8 XCDs: each gets a contiguous run of tiles.
+  const int nblk = gridDim.x;
+  int bid = blockIdx.x;
+  int split = 0;
+  if (kSplit) {
+    split = bid % splits;
+    bid = bid / splits;
+  } else if ((nblk & 7) == 0) {
+    bid = (bid & 7) * (nblk >> 3) + (bid >> 3);
+  }
+  int tm, tn;
+  tile_coords(bid + tile0, tiles_m, tiles_n, tm, tn);
+  const int64_t row0 = (int64_t)tm * G::kBM, col0 = (int64_t)tn * G::kBN;
+  const int t = threadIdx.x;
+  const int lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / G::kWN, wn = wave % G::kWN;
+  const int kb_all = (int)((k + kFp8Block - 1) / kFp8Block);
+  const int kt_begin = kSplit ? (int)((int64_t)kb_all * split / splits) : 0;
+  const int kt_end = kSplit ? (int)((int64_t)kb_all * (split + 1) / splits) : kb_all;
+
+  // A copy instruction fills eight rows of a panel: lane l lands in 16-byte position l % 8 of row
+  // l / 8.  Position p of row r holds chunk p ^ (r % 8): any eight rows' reads of one chunk lie in
+  // different banks.  Rows past the end are outside the buffer and chunks past the end of K are
+  // sent there: both are zeros.
+  const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+  const u32x4_t abuf = buffer_of(a_codes + row0 * k, (uint32_t)(min(m - row0, (int64_t)G::kBM) * k));
+  const u32x4_t bbuf = buffer_of(b_codes + col0 * k, (uint32_t)(min(n - col0, (int64_t)G::kBN) * k));
+  const uint32_t arow = (uint32_t)((8 * G::kCopyA * wave + (lane >> 3)) * k);
+  const uint32_t brow = (uint32_t)((8 * G::kCopyB * wave + (lane >> 3)) * k);
+  const uint32_t step8 = (uint32_t)(8 * k);
+  const uint32_t srows = (uint32_t)min(m - row0, (int64_t)G::kBM) * 4;
+  auto fetch = [&](int kt) {
+    uint8_t* st = lds + (kt & 1) * G::kStage;
+    const uint32_t koff = (int64_t)kt * kFp8Block + chunk < k ? (uint32_t)(kt * kFp8Block + chunk) : kOutside;
+#pragma unroll
+    for (int i = 0; i < G::kCopyA; ++i)
+      copy16_to_lds(abuf, arow + i * step8 + koff, st + (G::kCopyA * wave + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < G::kCopyB; ++i)
+      copy16_to_lds(bbuf, brow + i * step8 + koff, st + G::kOffB + (G::kCopyB * wave + i) * 1024);
+    if (wave < G::kBM / 64)
+      copy4_to_lds(buffer_of(a_scales + (int64_t)kt * m + row0, srows), (uint32_t)t * 4, st + G::kOffS + wave * 256);
+  };
+
+  // Fragment reads: lane l takes chunks l / 16 and l / 16 + 4 of row l % 16.
+  const int frag0 = (lane & 15) * 128 + 16 * ((lane >> 4) ^ (lane & 7));
+  auto fragment = [&](const uint8_t* rows) {
+    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(rows + frag0);
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(rows + (frag0 ^ 64));
+    return int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+
+  float4v acc[kTM][kTN];
+#pragma unroll
+  for (int i = 0; i < kTM; ++i)
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int64_t nblocks = (n + kFp8Block - 1) / kFp8Block;
+  const float* bs = b_scales + min((col0 + wn * 16 * kTN) / kFp8Block, nblocks - 1) * kb_all;
+
+  fetch(kt_begin);
+#pragma clang loop unroll(disable)
+  for (int kt = kt_begin; kt < kt_end; ++kt) {
+    stage_barrier();   // block kt is in its stage, the other stage is read
+    if (kt + 1 < kt_end) fetch(kt + 1);
+    const uint8_t* st = lds + (kt & 1) * G::kStage;
+    const uint8_t* ap = st + wm * 16 * kTM * 128;
+    const uint8_t* bp = st + G::kOffB + wn * 16 * kTN * 128;
+    const float sb = bs[kt];
+    int8v fb[kTN], fa[2];
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) fb[j] = fragment(bp + j * 2048);
+    fa[0] = fragment(ap);
+    float s[kTM];
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+      s[i] = sb * *reinterpret_cast<const float*>(st + G::kOffS + (wm * 16 * kTM + 16 * i + (lane & 15)) * 4);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      if (i + 1 < kTM) fa[(i + 1) & 1] = fragment(ap + (i + 1) * 2048);
+      float4v p[kTN];
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) p[j] = block_mfma(fb[j], fa[i & 1]);
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) add_scaled(acc[i][j], s[i], p[j]);
+    }
+  }
+  stage_barrier();   // every wave is done with the stages
+
+  // 16 rows at a time pass through the wave's own LDS region: lane l writes four columns of row
+  // l % 16, and reads back eight columns of row 8 p + l / 8.
+  float* stg = reinterpret_cast<float*>(lds + wave * G::kEpiWave);
+  const int ecol = 8 * (lane & 7);
+  auto stage_rows = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < kTN; ++j)
+      *reinterpret_cast<float4v*>(stg + (lane & 15) * G::kEpiRow + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+    lds_order();
+  };
+  if constexpr (kSplit) {
+    float* dst = partial + ((int64_t)split * (gridDim.x / splits) + blockIdx.x / splits) * (G::kBM * G::kBN);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      stage_rows(i);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = 8 * p + (lane >> 3);
+        const float4v* f = reinterpret_cast<const float4v*>(stg + r * G::kEpiRow + ecol);
+        float4v* d = reinterpret_cast<float4v*>(dst + (wm * 16 * kTM + 16 * i + r) * G::kBN + wn * 16 * kTN + ecol);
+        d[0] = f[0];
+        d[1] = f[1];
+      }
+      lds_order();
+    }
+  } else {
+    const int64_t col = col0 + wn * 16 * kTN + ecol;
+    const bool whole = col + 8 <= n;
+    const bool wide = (n & 7) == 0 && ((uintptr_t)out & 15) == 0;
+    float bv[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && col + h < n ? bf16_to_f32(bias[col + h]) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int64_t r0 = row0 + wm * 16 * kTM + 16 * i + (lane >> 3);
+      uint4 res[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        res[p] = whole && r0 + 8 * p < m ? residual8(ep, (r0 + 8 * p) * n + col) : make_uint4(0, 0, 0, 0);
+      stage_rows(i);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int64_t row = r0 + 8 * p;
+        const float* f = stg + (8 * p + (lane >> 3)) * G::kEpiRow + ecol;
+        const float4v f0 = *reinterpret_cast<const float4v*>(f), f1 = *reinterpret_cast<const float4v*>(f + 4);
+        const int64_t idx = row * n + col;
+        if (row < m && whole) {
+          const float z[8] = {__fadd_rn(f0[0], bv[0]), __fadd_rn(f0[1], bv[1]), __fadd_rn(f0[2], bv[2]),
+                              __fadd_rn(f0[3], bv[3]), __fadd_rn(f1[0], bv[4]), __fadd_rn(f1[1], bv[5]),
+                              __fadd_rn(f1[2], bv[6]), __fadd_rn(f1[3], bv[7])};
+          const uint4 o = finish8_bf16<kAct>(z, res[p], ep, idx);
+          if (wide) __builtin_nontemporal_store(u32x4_t{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4_t*>(out + idx));
+          else __builtin_memcpy(out + idx, &o, 16);
+        } else if (row < m) {
+#pragma unroll 1
+          for (int h = 0; h < 8 && col + h < n; ++h) out[idx + h] = (uint16_t)finish_bf16(f[h], bias, col + h, ep, idx + h);
+        }
+      }
+      lds_order();
+    }
+  }
+}
+
+// Adds the partial tiles of `tiles` tiles from tile0 in split order and finishes them: eight
+// columns per thread.
+template <class G>
+__global__ void __launch_bounds__(256) gemm_fp8_reduce(const float* __restrict__ partial, int splits, int tiles,
+                                                       int tile0, int tiles_m, int tiles_n, int64_t m, int64_t n,
+                                                       const uint16_t* __restrict__ bias, uint16_t* out,
+                                                       const Epilogue ep) {
+  constexpr int kPerTile = G::kBM * G::kBN / 8;
+  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int tl = (int)(gid / kPerTile), u = (int)(gid % kPerTile);
+  int tm, tn;
+  tile_coords(tile0 + tl, tiles_m, tiles_n, tm, tn);
+  const int64_t row = (int64_t)tm * G::kBM + u / (G::kBN / 8), col = (int64_t)tn * G::kBN + 8 * (u % (G::kBN / 8));
+  if (row >= m || col >= n) return;
+  const float4v* src = reinterpret_cast<const float4v*>(partial + (int64_t)tl * (G::kBM * G::kBN) + 8 * u);
+  const int64_t stride = (int64_t)tiles * (G::kBM * G::kBN / 4);
+  float4v a = src[0], b = src[1];
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) {
+    a += src[s * stride];
+    b += src[s * stride + 1];
+  }
+  float z[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const int64_t idx = row * n + col;
+  if (col + 8 <= n) {
+    if (bias != nullptr) {
+#pragma unroll
+      for (int h = 0; h < 8; ++h) z[h] = __fadd_rn(z[h], bf16_to_f32(bias[col + h]));
+    }
+    const uint4 o = finish8_any(z, residual8(ep, idx), ep, idx);
+    __builtin_memcpy(out + idx, &o, 16);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (col + h < n) out[idx + h] = (uint16_t)finish_bf16(z[h], bias, col + h, ep, idx + h);
+  }
+}
+
+// ---- few rows: the weight is streamed once ----
+
+// A workgroup owns 16 weight rows, its waves a K range each; a wave multiplies every block of its
+// rows with kTA tiles of 16 activation rows, several blocks' loads in flight, and the waves' sums
+// meet in LDS.  kFused (one tile): x is bf16 (or gate, with up), and each wave first quantizes its
+// own K range of the m rows into LDS.
+constexpr int kFusedRows = 4;
+constexpr int kFusedLds = 60 * 1024;
+
+template <int kTA, int kWaves, bool kFused>
+__global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
+    const void* __restrict__ x, const uint16_t* __restrict__ up, const float* __restrict__ x_scales, int64_t m,
+    int64_t k, const uint8_t* __restrict__ w_codes, const float* __restrict__ w_scales, int64_t n,
+    const uint16_t* __restrict__ bias, uint16_t* out, const Epilogue ep) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int kDepth = kTA == 1 ? 4 : 2;   // blocks in flight
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int kb_all = (int)((k + kFp8Block - 1) / kFp8Block);
+  const int kb0 = (int)((int64_t)kb_all * wave / kWaves), kb1 = (int)((int64_t)kb_all * (wave + 1) / kWaves);
+  const int r = lane & 15, g = lane >> 4;
+
+  const __amdgpu_buffer_rsrc_t wbuf = rsrc_of(w_codes + n0 * k, (uint32_t)(min(n - n0, (int64_t)16) * k));
+  const uint32_t wrow = (uint32_t)(r * k);
+  auto load32 = [&](__amdgpu_buffer_rsrc_t buf, uint32_t row, int kb) {
+    const int64_t c0 = (int64_t)kb * kFp8Block + 16 * g, c1 = c0 + 64;
+    const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(c0 < k && kb < kb1 ? row + (uint32_t)c0 : kOutside), 0, 0);
+    const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(c1 < k && kb < kb1 ? row + (uint32_t)c1 : kOutside), 0, 0);
+    return int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+  int8v fw[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) fw[d] = load32(wbuf, wrow, kb0 + d);
+  const float* ws = w_scales + (n0 / kFp8Block) * kb_all;
+
+  float4v acc[kTA];
+#pragma unroll
+  for (int i = 0; i < kTA; ++i) acc[i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if constexpr (kFused) {
+    // this wave's [m][blocks] codes, and behind all waves' codes its scales; eight lanes own a block
+    const int blocks = kb1 - kb0;
+    uint8_t* xq = lds + kb0 * (int)m * kFp8Block;
+    float* xs = reinterpret_cast<float*>(lds + kb_all * (int)m * kFp8Block) + kb0 * (int)m;
+    const uint16_t* xb = static_cast<const uint16_t*>(x);
+    for (int u0 = 0; u0 < blocks * (int)m; u0 += 8) {
+      const int u = u0 + (lane >> 3);
+      const int row = u / blocks, b = u - row * blocks;
+      const int64_t col = (int64_t)(kb0 + b) * kFp8Block + 16 * (lane & 7);
+      float v[16];
+      if (u < blocks * (int)m && col < k) {
+        load16_bf16(xb + row * k + col, v);
+        if (up != nullptr) {
+          float w[16];
+          load16_bf16(up + row * k + col, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = swiglu_bf16(v[i], w[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      }
+      float scale;
+      const uint4 c = fp8_block16(v, scale);
+      if (u < blocks * (int)m) {
+        *reinterpret_cast<uint4*>(xq + u * kFp8Block + 16 * (lane & 7)) = c;
+        if ((lane & 7) == 0) xs[u] = scale;
+      }
+    }
+    lds_order();
+    const int row = min(r, (int)m - 1);   // rows past the last repeat it and are not written
+    const uint8_t* xr = xq + row * blocks * kFp8Block + 16 * g;
+    for (int kb = kb0; kb < kb1; kb += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int8v w = fw[d];
+        fw[d] = load32(wbuf, wrow, kb + d + kDepth);
+        if (kb + d < kb1) {
+          const uint8_t* p = xr + (kb + d - kb0) * kFp8Block;
+          const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(p), hi = *reinterpret_cast<const u32x4_t*>(p + 64);
+          const int8v fx = int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+          add_scaled(acc[0], xs[row * blocks + kb + d - kb0] * ws[kb + d], block_mfma(w, fx));
+        }
+      }
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t xbuf = rsrc_of(x, (uint32_t)(m * k));
+    const __amdgpu_buffer_rsrc_t sbuf = rsrc_of(x_scales, (uint32_t)(m * kb_all * 4));
+    uint32_t xrow[kTA];
+    int8v fx[kDepth][kTA];
+    float sx[kDepth][kTA];
+#pragma unroll
+    for (int i = 0; i < kTA; ++i) xrow[i] = 16 * i + r < m ? (uint32_t)((16 * i + r) * k) : kOutside;
+    auto load_x = [&](int d, int kb) {
+#pragma unroll
+      for (int i = 0; i < kTA; ++i) {
+        fx[d][i] = load32(xbuf, xrow[i], kb);
+        const bool in = 16 * i + r < m && kb < kb1;
+        sx[d][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, (int)(in ? (uint32_t)((kb * m + 16 * i + r) * 4) : kOutside), 0, 0));
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load_x(d, kb0 + d);
+    for (int kb = kb0; kb < kb1; kb += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const float sw = ws[min(kb + d, kb_all - 1)];
+#pragma unroll
+        for (int i = 0; i < kTA; ++i) add_scaled(acc[i], sx[d][i] * sw, block_mfma(fw[d], fx[d][i]));
+        fw[d] = load32(wbuf, wrow, kb + d + kDepth);
+        load_x(d, kb + d + kDepth);
+      }
+    }
+  }
+
+  // The waves' sums, added in wave order; a thread finishes four columns of one row.
+  __syncthreads();
+  float4v* red = reinterpret_cast<float4v*>(lds);
+#pragma unroll
+  for (int i = 0; i < kTA; ++i) red[(wave * kTA + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  for (int u = t; u < kTA * 64; u += 64 * kWaves) {
+    float4v z = red[u];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) z += red[w * kTA * 64 + u];
+    const int64_t row = 16 * (u >> 6) + (u & 15), col = n0 + 4 * ((u & 63) >> 4);
+    if (row >= m) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) out[row * n + col + e] = (uint16_t)finish_bf16(z[e], bias, col + e, ep, row * n + col + e);
+  }
+}
+
+// How a product runs: streamed, or in tiles of Large or Small, `full` of them in whole rounds of
+// what the GPU holds at once and the rest split along K.
+enum Kind { kSkinny, kLargeTiles, kSmallTiles };
+struct Plan {
+  Kind kind;
+  int64_t tiles_m, tiles_n, full, rest;
+  int splits;
+  size_t bytes;
+};
+
+template <class G>
+Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t slots) {
+  Plan p{};
+  p.kind = kind;
+  p.tiles_m = (m + G::kBM - 1) / G::kBM;
+  p.tiles_n = (n + G::kBN - 1) / G::kBN;
+  const int64_t tiles = p.tiles_m * p.tiles_n;
+  p.full = tiles / slots * slots;
+  p.rest = tiles - p.full;
+  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
+  int64_t sp = p.rest > 0 ? std::min<int64_t>(slots / p.rest, kb / 4) : 1;
+  p.splits = (int)std::max<int64_t>(sp, 1);
+  p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)p.rest * G::kBM * G::kBN * sizeof(float) : 0;
+  return p;
+}
+
+// Rounds of blocks of K that a plan takes, in units of one block of a Large tile.
+double plan_cost(const Plan& p, int64_t k, int64_t slots, double block_cost) {
+  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
+  double c = (double)(p.full / slots) * kb;
+  if (p.rest > 0) c += (double)((kb + p.splits - 1) / p.splits);
+  return c * block_cost + (p.splits > 1 ? 6.0 : 0.0);
+}
+
+Plan plan_of(int64_t m, int64_t k, int64_t n, int cus) {
+  if (m <= 64 && m * k < (int64_t)kOutside) {
+    Plan p{};
+    p.kind = kSkinny;
+    return p;
+  }
+  const Plan l = tile_plan<Large>(kLargeTiles, m, k, n, cus), s = tile_plan<Small>(kSmallTiles, m, k, n, 2 * cus);
+  return plan_cost(l, k, cus, 1.0) <= plan_cost(s, k, 2 * cus, 0.7) ? l : s;
+}
+
+template <class G>
+hipError_t launch_tiles(const Plan& p, const uint8_t* a_codes, const float* a_scales, int64_t m, int64_t k,
+                        const uint8_t* b_codes, const float* b_scales, int64_t n, const uint16_t* bias,
+                        const Epilogue& ep, uint16_t* out, float* partial, hipStream_t s) {
+  using Fn = decltype(&gemm_fp8_kernel<G, false, 0>);
+  static constexpr Fn f[5] = {gemm_fp8_kernel<G, false, NVFP4_ACT_NONE>, gemm_fp8_kernel<G, false, NVFP4_ACT_SILU>,
+                              gemm_fp8_kernel<G, false, NVFP4_ACT_GELU>,
+                              gemm_fp8_kernel<G, false, NVFP4_ACT_GELU_TANH>, gemm_fp8_kernel<G, true, 0>};
+  static_assert(NVFP4_ACT_NONE == 0 && NVFP4_ACT_SILU == 1 && NVFP4_ACT_GELU == 2 && NVFP4_ACT_GELU_TANH == 3, "");
+  static bool attr_set[5][kMaxDevices] = {};
+  auto launch = [&](int which, int64_t blocks, int64_t tile0, int splits) {
+    if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(f[which]), G::kLds, attr_set[which]);
+        e != hipSuccess)
+      return e;
+    hipLaunchKernelGGL(f[which], dim3((uint32_t)blocks), dim3(G::kThreads), G::kLds, s, a_codes, a_scales, m, k, b_codes,
+                       b_scales, n, bias, out, (int)p.tiles_m, (int)p.tiles_n, (int)tile0, splits, partial, ep);
+    return hipGetLastError();
+  };
+  if (p.full > 0)
+    if (hipError_t e = launch(ep.act, p.full, 0, 1); e != hipSuccess) return e;
+  if (p.rest == 0) return hipSuccess;
+  if (p.splits == 1) return launch(ep.act, p.rest, p.full, 1);
+  if (hipError_t e = launch(4, p.rest * p.splits, p.full, p.splits); e != hipSuccess) return e;
+  hipLaunchKernelGGL(gemm_fp8_reduce<G>, dim3((uint32_t)(p.rest * (G::kBM * G::kBN / 8 / 256))), dim3(256), 0, s, partial,
+                     p.splits, (int)p.rest, (int)p.full, (int)p.tiles_m, (int)p.tiles_n, m, n, bias, out, ep);
+  return hipGetLastError();
+}
+
+template <int kTA, bool kFused>
+hipError_t launch_skinny(const void* x, const uint16_t* up, const float* x_scales, int64_t m, int64_t k,
+                         const uint8_t* b_codes, const float* b_scales, int64_t n, const uint16_t* bias,
+                         const Epilogue& ep, uint16_t* out, hipStream_t s) {
+  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
+  const dim3 grid((uint32_t)((n + 15) / 16));
+  auto lds = [&](int waves) {
+    const size_t x_bytes = kFused ? (size_t)kb * (size_t)m * (kFp8Block + 4) : 0;
+    return (uint32_t)std::max<size_t>(x_bytes, (size_t)waves * kTA * 1024);
+  };
+  if (kb >= 16)
+    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kTA, 8, kFused>), grid, dim3(512), lds(8), s, x, up, x_scales, m, k,
+                       b_codes, b_scales, n, bias, out, ep);
+  else
+    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kTA, 4, kFused>), grid, dim3(256), lds(4), s, x, up, x_scales, m, k,
+                       b_codes, b_scales, n, bias, out, ep);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gemm_fp8_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus) { return plan_of(m, k, n, cus).bytes; }
+
+hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
+                           const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep, uint16_t* out,
+                           void* workspace, size_t workspace_bytes, int cus, hipStream_t s) {
+  Plan p = plan_of(m, k, n, cus);
+  if (p.kind == kSkinny) {
+    const auto fn = m <= 16 ? launch_skinny<1, false> : m <= 32 ? launch_skinny<2, false> : launch_skinny<4, false>;
+    return fn(a_codes, nullptr, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, s);
+  }
+  if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes)) p.splits = 1;
+  return (p.kind == kLargeTiles ? launch_tiles<Large> : launch_tiles<Small>)(
+      p, a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), s);
+}
+
+bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n) {
+  (void)n;
+  return m <= kFusedRows && (k + kFp8Block - 1) / kFp8Block * m * (kFp8Block + 4) <= kFusedLds;
+}
+
+hipError_t launch_linear_fp8_fused(const uint16_t* x, const uint16_t* up, int64_t m, int64_t k, const uint8_t* b_codes,
+                                   const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep,
+                                   uint16_t* out, hipStream_t s) {
+  return launch_skinny<1, true>(x, up, nullptr, m, k, b_codes, b_scales, n, bias, ep, out, s);
+}
+
+}  // namespace nvfp4

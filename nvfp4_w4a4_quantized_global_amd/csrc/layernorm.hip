@@ -1,0 +1,500 @@
+// Layer norm with the residual's addition, on gfx950: its output as bf16 (with or without an
+// 8-bit checkpoint), as 8-bit block codes or as NVFP4 codes, and its gradient; and the RMS
+// norm's output as 8-bit block codes.
+//
+//   r = x + residual                      (rounded to the stream's type, stored)
+//   mu = mean(r),  s = fp32(1 / sqrt(mean((r - mu)^2) + eps))
+//   y = bf16(fp32(fp32(fp32(r - mu) * s) * w) + b)
+//
+// Mean and variance come from one pass over the row, which stays in registers: with the
+// row's first value p as a pivot, S1 = sum(r - p) and S2 = sum((r - p)^2) in fp64 give
+// mu = p + S1 / K and the variance S2 / K - (S1 / K)^2.  p is one of the K values, so
+// (p - mu)^2 is at most K times the variance: the subtraction costs 14 of fp64's 53 bits at
+// most, where sums without a pivot lose as many bits as the mean is larger than the spread.
+//
+// The layout is the RMS norm's (norm_device.h): a lane owns 16 consecutive values, a row a
+// power-of-two group of lanes or a workgroup of its own; one read, one write.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "checkpoint_device.h"
+#include "fp8_device.h"
+#include "norm_device.h"
+#include "nvfp4_device.h"
+#include "nvfp4_launch.h"
+#include "quantize_device.h"
+
+namespace nvfp4 {
+namespace {
+
+// Value i of a row's stream, rounded as it is stored.
+template <bool kXF32, int kRes>
+__device__ __forceinline__ float stream_value(const void* x, const void* residual, int64_t i) {
+  float v = kXF32 ? static_cast<const float*>(x)[i] : bf16_to_f32(static_cast<const uint16_t*>(x)[i]);
+  if constexpr (kRes == 1)
+    v = bf16_to_f32(gemm::pack_bf16x2(__fadd_rn(v, bf16_to_f32(static_cast<const uint16_t*>(residual)[i])), 0.0f) & 0xFFFFu);
+  if constexpr (kRes == 2) v = __fadd_rn(v, static_cast<const float*>(residual)[i]);
+  return v;
+}
+
+// Sums of d = v - p and d^2 over a lane's 16 values.
+__device__ __forceinline__ void pivot_sums(const float (&v)[16], float p, double& s1, double& s2) {
+  double a1 = 0.0, b1 = 0.0, a2 = 0.0, b2 = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const double d = (double)v[i] - (double)p, e = (double)v[i + 1] - (double)p;
+    a1 += d;
+    b1 += e;
+    a2 = fma(d, d, a2);
+    b2 = fma(e, e, b2);
+  }
+  s1 = a1 + b1;
+  s2 = a2 + b2;
+}
+
+// Mean and scale from the row's sums.  The variance's last bits may fall below zero; NaN stays.
+__device__ __forceinline__ float row_statistics(double s1, double s2, float p, int64_t k, double eps, double& mu) {
+  const double m = s1 / (double)k;
+  double var = s2 / (double)k - m * m;
+  var = var < 0.0 ? 0.0 : var;
+  mu = (double)p + m;
+  return (float)(1.0 / sqrt(var + eps));
+}
+
+// y = bf16(fp32(fp32(fp32(r - mu) * s) * w) + b), over r.
+template <bool kWF32>
+__device__ __forceinline__ void layernorm16(float (&v)[16], double mu, float s, const Raw16<kWF32>& w,
+                                            const Raw16<kWF32>& b, bool has_bias) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn((float)((double)v[i] - mu), s), w.get(i));
+  if (has_bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], b.get(i));
+  }
+  round_bf16(v);
+}
+
+// kRes: no residual, one in bf16, one in fp32 (the stream's type is the residual's, or x's
+// without one).  kMean: the layer norm; otherwise the RMS norm, whose row sum is added as in
+// norm.hip, so that its y has the same bits.  What becomes of y is a.mode: bf16 with an optional
+// checkpoint, 8-bit block codes, NVFP4 codes under a static scale, those of a single row under
+// its own dynamic scale, or (first pass of a dynamic scale over many rows) only the statistics
+// and the abs-max of y.
+template <bool kXF32, int kRes, bool kWF32, bool kMean>
+__global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
+  constexpr bool kSF32 = kRes == 0 ? kXF32 : kRes == 2;
+  __shared__ double part[2][16];
+  __shared__ float pmax[16];
+  const int t = threadIdx.x;
+  const int rows_here = blockDim.x / a.lanes;
+  const int sub = rows_here == 1 ? 0 : t / a.lanes;
+  const int c = t - sub * a.lanes;
+  const int64_t k = a.k;
+  const bool in_k = c < k / kBlock;
+  const bool has_bias = kMean && a.b != nullptr;
+  Raw16<kWF32> w, b;
+  if (in_k) w.load(a.w, (int64_t)c * kBlock);
+  else w.zero();
+  if (in_k && has_bias) b.load(a.b, (int64_t)c * kBlock);
+  else b.zero();
+  const float gsf_static = a.mode == kNormStatic ? *a.gsf : 0.0f;
+  if (a.mode == kNormStatic && a.gsf_out != nullptr && blockIdx.x == 0 && t == 0) *a.gsf_out = gsf_static;
+  float mx = 0.0f;
+
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_here) {
+    const int64_t row = row0 + sub;
+    const bool valid = row < a.rows && in_k;
+    const int64_t off = row * k + (int64_t)c * kBlock;
+    float v[16];
+    float p = 0.0f;
+    if (valid) {
+      load_stream16<kXF32>(a.x, off, v);
+      if constexpr (kRes != 0) {
+        float q[16];
+        load_stream16<kRes == 2>(a.residual, off, q);
+        // the pivot before r is written: r may be the residual or x
+        if constexpr (kMean) p = stream_value<kXF32, kRes>(a.x, a.residual, row * k);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], q[i]);
+        if constexpr (!kSF32) round_bf16(v);
+      } else if constexpr (kMean) {
+        p = stream_value<kXF32, kRes>(a.x, nullptr, row * k);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+    const int lanes = a.lanes < 64 ? a.lanes : 64;
+    double s1 = 0.0, s2;
+    if constexpr (kMean) pivot_sums(v, p, s1, s2);   // lanes without values: all zero
+    else s2 = sum_squares(v);
+    if constexpr (kMean) s1 = group_sum(s1, lanes);
+    s2 = group_sum(s2, lanes);
+    if (a.lanes > 64) {
+      if ((t & 63) == 0) {
+        part[0][t >> 6] = s1;
+        part[1][t >> 6] = s2;
+      }
+      __syncthreads();
+      s1 = 0.0;
+      s2 = 0.0;
+      for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
+        if constexpr (kMean) s1 += part[0][i];
+        s2 += part[1][i];
+      }
+      __syncthreads();
+    }
+    // behind the barrier (or, inside a wave, behind the sums): every lane of the row has its pivot
+    if constexpr (kRes != 0)
+      if (valid) store_stream16<kSF32>(a.r, off, v);
+    float s;
+    double mu = 0.0;
+    if constexpr (kMean) {
+      s = row_statistics(s1, s2, p, k, a.eps, mu);
+      layernorm16<kWF32>(v, mu, s, w, b, has_bias);
+      if (!valid) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      }
+    } else {
+      s = row_scale(s2, k, a.eps);
+      normalize16<kWF32>(v, s, w);
+    }
+
+    if (a.mode == kNormFp8) {
+      float scale;
+      const uint4 code = fp8_block16(v, scale);
+      if (valid) {
+        *reinterpret_cast<uint4*>(a.codes + off) = code;
+        if ((c & 7) == 0) a.block_scales[(int64_t)(c >> 3) * a.rows + row] = scale;
+      }
+      continue;
+    }
+    if constexpr (kMean) {
+      if (a.mode == kNormOut) {
+        if (valid) store16_bf16(a.y + off, v);
+        if (a.codes != nullptr) {
+          uint32_t sb;
+          const uint4 code = ck_pack16(v, sb);
+          if (valid) {
+            *reinterpret_cast<uint4*>(a.codes + off) = code;
+            if ((c & 1) == 0) a.scales[row * ((k + kCkBlock - 1) / kCkBlock) + (c >> 1)] = (uint8_t)sb;
+          }
+        }
+        continue;
+      }
+      float gsf = gsf_static;
+      if (a.mode != kNormStatic) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
+        if (a.mode == kNormStats) {
+          if (c == 0 && row < a.rows) {
+            a.rstd[row] = s;
+            a.mean[row] = mu;
+          }
+          continue;
+        }
+        // the one row: its abs-max over the workgroup (rows beyond it are zeros)
+        mx = wave_max(mx);
+        if ((t & 63) == 0) pmax[t >> 6] = mx;
+        __syncthreads();
+        for (int i = 0; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
+        gsf = global_scale_from_amax(mx);
+        if (t == 0 && a.gsf_out != nullptr) *a.gsf_out = gsf;
+      }
+      // lanes past the row's last 128-wide tile hold no unit of this row
+      const int64_t urow = c < (k + kScaleTileK - 1) / kScaleTileK * 8 ? row : a.rows;
+      quantize_unit<false>(v, urow, c >> 3, c & 7, a.rows, k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
+    }
+  }
+  if constexpr (kMean) {
+    if (a.mode == kNormStats) {
+      mx = wave_max(mx);
+      if ((t & 63) == 0) pmax[t >> 6] = mx;
+      __syncthreads();
+      if (t == 0) {
+        for (int i = 1; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
+        a.partials[blockIdx.x] = mx;
+      }
+    }
+  }
+}
+
+// Second pass of a dynamic scale: y again from r and the row's statistics, then its codes, as
+// the RMS norm's second pass does (norm.hip).
+template <bool kSF32, bool kWF32>
+__global__ void __launch_bounds__(kNormQThreads) layernorm_quantize_kernel(const NormForward a, int n_partials) {
+  __shared__ float lds[kNormQThreads / 64];
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < n_partials; i += kNormQThreads) m = fmaxf(m, a.partials[i]);
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kNormQThreads / 64; ++i) m = fmaxf(m, lds[i]);
+  const float gsf = global_scale_from_amax(m);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.gsf_out != nullptr) *a.gsf_out = gsf;
+
+  const int kt_count = (int)((a.k + kScaleTileK - 1) / kScaleTileK);
+  const int j = threadIdx.x & 7;
+  const uint32_t unit = blockIdx.x * (kNormQThreads / 8) + (threadIdx.x >> 3);
+  const int kt = (int)(unit % (uint32_t)kt_count);
+  const int64_t stride = gridDim.x * (kNormQThreads / 8) / (uint32_t)kt_count;   // rows
+  const int64_t first = unit / (uint32_t)kt_count;
+  const int blk = kt * 8 + j;
+  const bool in_k = blk < a.k / kBlock;
+  const bool has_bias = a.b != nullptr;
+  const void* r = a.r != nullptr ? a.r : a.x;
+  Raw16<kWF32> w, b;
+  if (in_k) w.load(a.w, (int64_t)blk * kBlock);
+  else w.zero();
+  if (in_k && has_bias) b.load(a.b, (int64_t)blk * kBlock);
+  else b.zero();
+  Raw16<kSF32> cur;
+  float s = 0.0f;
+  double mu = 0.0;
+  auto fetch = [&](int64_t row) {
+    if (row < a.rows && in_k) {
+      cur.load(r, row * a.k + (int64_t)blk * kBlock);
+      s = a.rstd[row];
+      mu = a.mean[row];
+    } else {
+      cur.zero();
+      s = 0.0f;
+      mu = 0.0;
+    }
+  };
+  fetch(first);
+  // the wave loops while any of its rows is left: quantize_unit shuffles across its lanes
+  for (int64_t row = first; __any(row < a.rows); row += stride) {
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = cur.get(i);
+    const float sr = s;
+    const double mr = mu;
+    fetch(row + stride);
+    layernorm16<kWF32>(y, mr, sr, w, b, has_bias);
+    quantize_unit<false>(y, row, kt, j, a.rows, a.k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
+  }
+}
+
+// Gradient.  With n = (r - mu) s and g = gy w:
+//   grad_r = s (g - mean(g) - n mean(g n)) + grad_residual,
+//   grad_w = sum over rows of gy n,   grad_b = sum over rows of gy
+// (the rounding of y taken as the identity).  One reduction gives all four row sums: those of
+// the pivot's distances d = r - p in fp64, and sum(g), sum(g d) from a lane's 16 products in
+// fp32, added in fp64: mean(g n) = s (sum(g d) - (mu - p) sum(g)) / K.
+//
+// Each workgroup walks its rows with its lanes' 16 columns of grad_w and grad_b in registers and
+// writes one partial row of both; layernorm_weight_grad_kernel adds the partials in a fixed order.
+template <bool kSF32, bool kWF32, bool kRes>
+__global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBackward a) {
+  __shared__ double part[2][4][16];
+  __shared__ float colsum[kGroupThreads * 16];
+  const int t = threadIdx.x;
+  const int rows_here = blockDim.x / a.lanes;
+  const int sub = rows_here == 1 ? 0 : t / a.lanes;
+  const int c = t - sub * a.lanes;
+  const int64_t k = a.k;
+  const bool in_k = c < k / kBlock;
+  Raw16<kWF32> w;
+  if (in_k) w.load(a.w, (int64_t)c * kBlock);
+  else w.zero();
+  float gw[16], gb[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) gw[i] = gb[i] = 0.0f;
+
+  const int64_t stride = (int64_t)gridDim.x * rows_here;
+  const double inv_k = 1.0 / (double)k;
+  int parity = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += stride, parity ^= 1) {
+    const int64_t row = row0 + sub;
+    const int64_t off = row * k + (int64_t)c * kBlock;
+    const bool valid = row < a.rows && in_k;
+    Raw16<kSF32> rr, gres;
+    Raw16<false> gy;
+    float p = 0.0f;
+    if (valid) {
+      rr.load(a.r, off);
+      p = stream_value<kSF32, 0>(a.r, nullptr, row * k);
+      gy.load(a.gy, off);
+      if constexpr (kRes) gres.load(a.grad_residual, off);
+    } else {
+      rr.zero();
+      gy.zero();
+      if constexpr (kRes) gres.zero();
+    }
+    float r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = rr.get(i);
+    double sum[4];
+    pivot_sums(r, p, sum[0], sum[1]);
+    float sg = 0.0f, sgd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float g = gy.get(i) * w.get(i);
+      sg += g;
+      sgd = fmaf(g, r[i] - p, sgd);
+    }
+    sum[2] = (double)sg;
+    sum[3] = (double)sgd;
+    const int lanes = a.lanes < 64 ? a.lanes : 64;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] = group_sum(sum[q], lanes);
+    if (a.lanes > 64) {
+      // the other parity's slots may still be read by slower waves; these are free
+      if ((t & 63) == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[parity][q][t >> 6] = sum[q];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[q] = 0.0;
+      for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[q] += part[parity][q][i];
+      }
+    }
+    // 0 for lanes without values: with eps = 0 a row beyond the last would have an infinite scale,
+    // and its part of grad_w (0 times it) would be NaN
+    double mu;
+    float s = row_statistics(sum[0], sum[1], p, k, a.eps, mu);
+    if (!valid) {
+      s = 0.0f;
+      mu = 0.0;
+    }
+    const float f1 = (float)(sum[2] * inv_k);
+    const float f2 = s * (float)((sum[3] - (mu - (double)p) * sum[2]) * inv_k);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float n = (float)((double)r[i] - mu) * s, g = gy.get(i);
+      gw[i] = fmaf(g, n, gw[i]);
+      gb[i] += g;
+      const float x = s * (fmaf(g, w.get(i), -f1) - n * f2);
+      r[i] = kRes ? x + gres.get(i) : x;
+    }
+    if (valid) {
+      if constexpr (!kSF32) round_bf16(r);
+      store_stream16<kSF32>(a.grad_r, off, r);
+    }
+  }
+  if (a.partials == nullptr) return;
+  float* const row_out = a.partials + (int64_t)blockIdx.x * 2 * k + (int64_t)c * kBlock;
+  if (rows_here == 1) {
+    if (in_k) {
+      store_stream16<true>(row_out, 0, gw);
+      store_stream16<true>(row_out, k, gb);
+    }
+    return;
+  }
+  // the workgroup's rows side by side in LDS, added in row order
+  auto join = [&](float (&g)[16], int64_t at) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) colsum[t * 16 + i] = g[i];
+    __syncthreads();
+    if (sub == 0 && in_k) {
+      for (int s = 1; s < rows_here; ++s)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] += colsum[(s * a.lanes + c) * 16 + i];
+      store_stream16<true>(row_out, at, g);
+    }
+  };
+  join(gw, 0);
+  __syncthreads();
+  join(gb, k);
+}
+
+// grad_w[j], then grad_b[j - k], = sum of n partial rows of 2 k: 32 columns per workgroup, 32
+// interleaved row sets added in order.
+__global__ void __launch_bounds__(1024) layernorm_weight_grad_kernel(const float* __restrict__ partials, int n,
+                                                                     int64_t k, float* __restrict__ grad_w,
+                                                                     float* __restrict__ grad_b) {
+  __shared__ float lds[32][33];
+  const int x = threadIdx.x & 31, set = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + x;
+  float a = 0.0f;
+  if (col < 2 * k) {
+#pragma unroll 8
+    for (int i = set; i < n; i += 32) a += partials[(int64_t)i * 2 * k + col];
+  }
+  lds[set][x] = a;
+  __syncthreads();
+  if (set == 0 && col < 2 * k) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) a += lds[i][x];
+    if (col < k) grad_w[col] = a;
+    else grad_b[col - k] = a;
+  }
+}
+
+using ForwardFn = void (*)(const NormForward);
+
+template <bool kMean>
+ForwardFn forward_kernel(const NormForward& a) {
+  const int w = a.w_f32 ? 1 : 0;
+  if (a.residual == nullptr) {
+    static constexpr ForwardFn f[2][2] = {
+        {layernorm_kernel<false, 0, false, kMean>, layernorm_kernel<false, 0, true, kMean>},
+        {layernorm_kernel<true, 0, false, kMean>, layernorm_kernel<true, 0, true, kMean>}};
+    return f[a.x_f32 ? 1 : 0][w];
+  }
+  static constexpr ForwardFn f[3][2] = {
+      {layernorm_kernel<false, 1, false, kMean>, layernorm_kernel<false, 1, true, kMean>},
+      {layernorm_kernel<false, 2, false, kMean>, layernorm_kernel<false, 2, true, kMean>},
+      {layernorm_kernel<true, 2, false, kMean>, layernorm_kernel<true, 2, true, kMean>}};
+  return f[!a.stream_f32 ? 0 : !a.x_f32 ? 1 : 2][w];
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(NormForward a, bool mean, hipStream_t s) {
+  const RowShape shape = row_shape(a.k);
+  a.lanes = shape.lanes;
+  const int64_t per = shape.threads / shape.lanes;
+  int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, 1 << 20);   // the rest by the row loop
+  if (a.mode == kNormDynamic) {
+    // one row needs no second pass: its workgroup knows the whole abs-max
+    a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
+    blocks = walking_blocks(a.rows, shape);
+  }
+  const ForwardFn fn = mean ? forward_kernel<true>(a) : forward_kernel<false>(a);
+  hipLaunchKernelGGL(fn, dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.mode != kNormStats) return e;
+  using QuantFn = void (*)(const NormForward, int);
+  static constexpr QuantFn q[2][2] = {{layernorm_quantize_kernel<false, false>, layernorm_quantize_kernel<false, true>},
+                                      {layernorm_quantize_kernel<true, false>, layernorm_quantize_kernel<true, true>}};
+  const int64_t grid = quantize_blocks(a.rows, a.k);
+  const bool sf32 = a.residual != nullptr ? a.stream_f32 : a.x_f32;
+  hipLaunchKernelGGL(q[sf32 ? 1 : 0][a.w_f32 ? 1 : 0], dim3((uint32_t)grid), dim3(kNormQThreads), 0, s, a, (int)blocks);
+  return hipGetLastError();
+}
+
+size_t layernorm_backward_partial_floats(int64_t rows, int64_t k) {
+  return (size_t)walking_blocks(rows, row_shape(k)) * 2 * (size_t)k;
+}
+
+hipError_t launch_layernorm_backward(NormBackward a, hipStream_t s) {
+  const RowShape shape = row_shape(a.k);
+  a.lanes = shape.lanes;
+  const int64_t blocks = walking_blocks(a.rows, shape);
+  if (a.grad_w == nullptr) a.partials = nullptr;
+  using Fn = void (*)(const NormBackward);
+  static constexpr Fn f[2][2][2] = {
+      {{layernorm_backward_kernel<false, false, false>, layernorm_backward_kernel<false, false, true>},
+       {layernorm_backward_kernel<false, true, false>, layernorm_backward_kernel<false, true, true>}},
+      {{layernorm_backward_kernel<true, false, false>, layernorm_backward_kernel<true, false, true>},
+       {layernorm_backward_kernel<true, true, false>, layernorm_backward_kernel<true, true, true>}}};
+  if (blocks > 0)
+    hipLaunchKernelGGL(f[a.stream_f32 ? 1 : 0][a.w_f32 ? 1 : 0][a.grad_residual != nullptr ? 1 : 0],
+                       dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.grad_w == nullptr) return e;
+  hipLaunchKernelGGL(layernorm_weight_grad_kernel, dim3((uint32_t)((2 * a.k + 31) / 32)), dim3(1024), 0, s, a.partials,
+                     (int)blocks, a.k, a.grad_w, a.grad_b);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

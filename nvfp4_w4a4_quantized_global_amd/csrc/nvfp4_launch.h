@@ -146,7 +146,7 @@ hipError_t launch_linear_decode_fused(const uint16_t* x, int64_t k, const uint8_
 // scale (gsf_out: the scale used); dynamic takes rstd [rows] and partials [kNormPartials].
 constexpr int64_t kNormMaxK = 16384;
 constexpr int kNormPartials = 1280;   // workgroups of the statistics pass at most
-enum NormMode { kNormOut, kNormStatic, kNormDynamic, kNormOneRow, kNormStats };   // the last two: internal
+enum NormMode { kNormOut, kNormStatic, kNormDynamic, kNormOneRow, kNormStats, kNormFp8 };   // OneRow, Stats: internal
 struct NormForward {
   const void* x;
   const void* residual;
@@ -160,7 +160,11 @@ struct NormForward {
   uint8_t *codes, *scales;
   const float* gsf;
   float *gsf_out, *rstd, *partials;
-  int lanes;   // set by the launcher
+  int lanes;             // set by the launcher
+  // the layer norm's:
+  const void* b;         // bias of the weight's type, or NULL
+  double* mean;          // [rows], beside rstd
+  float* block_scales;   // kNormFp8: [ceil(k / 128)][rows]
 };
 hipError_t launch_rmsnorm(NormForward a, hipStream_t s);
 
@@ -174,10 +178,17 @@ struct NormBackward {
   bool stream_f32, w_f32;
   void* grad_r;
   float *grad_w, *partials;
-  int lanes;   // set by the launcher
+  int lanes;       // set by the launcher
+  float* grad_b;   // the layer norm's
 };
 size_t rmsnorm_backward_partial_floats(int64_t rows, int64_t k);
 hipError_t launch_rmsnorm_backward(NormBackward a, hipStream_t s);
+
+// Layer norm (layernorm.hip), same arguments and modes, and kNormFp8: 8-bit block codes.
+// mean false: the RMS norm, kNormFp8 only.  Its gradient writes grad_w and grad_b, or neither.
+hipError_t launch_layernorm(NormForward a, bool mean, hipStream_t s);
+size_t layernorm_backward_partial_floats(int64_t rows, int64_t k);
+hipError_t launch_layernorm_backward(NormBackward a, hipStream_t s);
 
 // 8-bit checkpoints (checkpoint.hip): codes [rows][k], scales [rows][ceil(k / 32)].
 hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t rows, int64_t k, int group, float inv_sqrt_g,
@@ -193,6 +204,34 @@ hipError_t launch_swiglu_backward(const uint16_t* gy, const void* gate, const ui
                                   uint16_t* grad_up, hipStream_t s);
 hipError_t launch_activation_backward(const uint16_t* gy, const void* z, const uint8_t* z_scales, int64_t rows,
                                       int64_t k, int act, uint16_t* grad_z, hipStream_t s);
+
+// 8-bit block codes (fp8.hip): activations [rows][k] with scales [ceil(k / 128)][rows], of x or
+// (up not NULL) of the SwiGLU product of x and up; column_sum [k], when not NULL, receives the
+// sums of x over its rows (not with up; partials: fp8_column_sum_floats).  Weights [n][k] with
+// scales [ceil(n / 128)][ceil(k / 128)] and, when codes_t is not NULL, both transposed.
+size_t fp8_column_sum_floats(int64_t rows, int64_t k);
+hipError_t launch_fp8_quantize(const uint16_t* x, const uint16_t* up, int64_t rows, int64_t k, uint8_t* codes,
+                               float* scales, float* column_sum, float* partials, hipStream_t s);
+hipError_t launch_fp8_quantize_weight(const void* w, bool w_f32, int64_t n, int64_t k, uint8_t* codes, float* scales,
+                                      uint8_t* codes_t, float* scales_t, hipStream_t s);
+hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t k, bool weight,
+                                 void* out, bool out_bf16, hipStream_t s);
+
+// The product of 8-bit block codes, a [m][k] with a_scales [ceil(k / 128)][m] and b [n][k] with
+// b_scales [ceil(n / 128)][ceil(k / 128)] (gemm_fp8.hip): tiles for many rows, a weight-streaming
+// kernel for few.  The workspace (gemm_fp8_workspace_bytes) holds the fp32 sums of tiles split
+// along k; without it they run unsplit.
+constexpr int64_t kFp8MaxK = 1 << 22;
+size_t gemm_fp8_workspace_bytes(int64_t m, int64_t k, int64_t n, int cus);
+hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_t m, int64_t k, const uint8_t* b_codes,
+                           const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep, uint16_t* out,
+                           void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
+// The same for one or a few bf16 rows x (or the SwiGLU product of x and up), which each workgroup
+// quantizes for itself: one launch.
+bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n);
+hipError_t launch_linear_fp8_fused(const uint16_t* x, const uint16_t* up, int64_t m, int64_t k, const uint8_t* b_codes,
+                                   const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep,
+                                   uint16_t* out, hipStream_t s);
 
 // grad_w [n][k] (fp32, or bf16) = sum over rows of gy [rows][n] x checkpoint [rows][k]
 // (weight_grad.hip).  partial: fp32 split sums, weight_grad_workspace_bytes of them, or
