@@ -42,8 +42,10 @@ __device__ __forceinline__ uint4 fp8_encode16(const float (&v)[16], float factor
 // codes of this lane's values and the block's scale.  Every lane of the wave takes part.
 __device__ __forceinline__ uint4 fp8_block16(const float (&v)[16], float& scale) {
   uint32_t m = ck_amax_bits(v);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+  // lane ^ 1, lane ^ 2, and 7 - lane of the eight, by the vector unit's lane moves
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, true));
   float factor;
   scale = fp8_scale(m, factor);
   return fp8_encode16(v, factor);

@@ -39,6 +39,11 @@ __device__ __forceinline__ float stream_value(const void* x, const void* residua
   return v;
 }
 
+// Four values at a time: the scheduler would convert all 16 to fp64 at once (32 registers more).
+__device__ __forceinline__ void by_four(int i) {
+  if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+}
+
 // Sums of d = v - p and d^2 over a lane's 16 values.
 __device__ __forceinline__ void pivot_sums(const float (&v)[16], float p, double& s1, double& s2) {
   double a1 = 0.0, b1 = 0.0, a2 = 0.0, b2 = 0.0;
@@ -49,9 +54,51 @@ __device__ __forceinline__ void pivot_sums(const float (&v)[16], float p, double
     b1 += e;
     a2 = fma(d, d, a2);
     b2 = fma(e, e, b2);
+    by_four(i + 1);
   }
   s1 = a1 + b1;
   s2 = a2 + b2;
+}
+
+// Ends what the compiler knows of v: it would keep its 16 fp64 conversions (32 registers) from the
+// sums to the output, which spills; converting again costs less.
+__device__ __forceinline__ void forget(float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm("" : "+v"(v[i]));
+}
+
+template <bool kF32>
+__device__ __forceinline__ void forget(Raw16<kF32>& v) {
+#pragma unroll
+  for (int i = 0; i < (kF32 ? 4 : 2); ++i) asm("" : "+v"(v.raw[i].x), "+v"(v.raw[i].y), "+v"(v.raw[i].z), "+v"(v.raw[i].w));
+}
+
+// Sum over the `lanes` lanes of a row (a power of two from 8 to 64), the same bits in each: by the
+// vector unit's own lane moves, where shuffles through LDS (two for each fp64 step) cost the
+// gradient's four sums more than its memory traffic.
+template <int kCtrl>
+__device__ __forceinline__ double lane_move(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <bool k32>
+__device__ __forceinline__ double swap_sum(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t l = (uint32_t)u, h = (uint32_t)(u >> 32);
+  const auto lo = k32 ? __builtin_amdgcn_permlane32_swap(l, l, false, false) : __builtin_amdgcn_permlane16_swap(l, l, false, false);
+  const auto hi = k32 ? __builtin_amdgcn_permlane32_swap(h, h, false, false) : __builtin_amdgcn_permlane16_swap(h, h, false, false);
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+}
+__device__ __forceinline__ double lanes_sum(double v, int lanes) {
+  v += lane_move<0xB1>(v);                     // lane ^ 1
+  v += lane_move<0x4E>(v);                     // lane ^ 2
+  v += lane_move<0x141>(v);                    // 7 - lane of eight: the other four
+  if (lanes >= 16) v += lane_move<0x140>(v);   // 15 - lane of 16: the other eight
+  if (lanes >= 32) v = swap_sum<false>(v);
+  if (lanes >= 64) v = swap_sum<true>(v);
+  return v;
 }
 
 // Mean and scale from the row's sums.  The variance's last bits may fall below zero; NaN stays.
@@ -68,7 +115,10 @@ template <bool kWF32>
 __device__ __forceinline__ void layernorm16(float (&v)[16], double mu, float s, const Raw16<kWF32>& w,
                                             const Raw16<kWF32>& b, bool has_bias) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(__fmul_rn((float)((double)v[i] - mu), s), w.get(i));
+  for (int i = 0; i < 16; ++i) {
+    v[i] = __fmul_rn(__fmul_rn((float)((double)v[i] - mu), s), w.get(i));
+    by_four(i);
+  }
   if (has_bias) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], b.get(i));
@@ -78,11 +128,11 @@ __device__ __forceinline__ void layernorm16(float (&v)[16], double mu, float s, 
 
 // kRes: no residual, one in bf16, one in fp32 (the stream's type is the residual's, or x's
 // without one).  kMean: the layer norm; otherwise the RMS norm, whose row sum is added as in
-// norm.hip, so that its y has the same bits.  What becomes of y is a.mode: bf16 with an optional
+// norm.hip, so that its y has the same bits.  What becomes of y is kMode: bf16 with an optional
 // checkpoint, 8-bit block codes, NVFP4 codes under a static scale, those of a single row under
 // its own dynamic scale, or (first pass of a dynamic scale over many rows) only the statistics
 // and the abs-max of y.
-template <bool kXF32, int kRes, bool kWF32, bool kMean>
+template <bool kXF32, int kRes, bool kWF32, bool kMean, int kMode>
 __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
   constexpr bool kSF32 = kRes == 0 ? kXF32 : kRes == 2;
   __shared__ double part[2][16];
@@ -99,8 +149,8 @@ __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
   else w.zero();
   if (in_k && has_bias) b.load(a.b, (int64_t)c * kBlock);
   else b.zero();
-  const float gsf_static = a.mode == kNormStatic ? *a.gsf : 0.0f;
-  if (a.mode == kNormStatic && a.gsf_out != nullptr && blockIdx.x == 0 && t == 0) *a.gsf_out = gsf_static;
+  const float gsf_static = kMode == kNormStatic ? *a.gsf : 0.0f;
+  if (kMode == kNormStatic && a.gsf_out != nullptr && blockIdx.x == 0 && t == 0) *a.gsf_out = gsf_static;
   float mx = 0.0f;
 
   for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < a.rows; row0 += (int64_t)gridDim.x * rows_here) {
@@ -130,8 +180,12 @@ __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
     double s1 = 0.0, s2;
     if constexpr (kMean) pivot_sums(v, p, s1, s2);   // lanes without values: all zero
     else s2 = sum_squares(v);
-    if constexpr (kMean) s1 = group_sum(s1, lanes);
-    s2 = group_sum(s2, lanes);
+    if constexpr (kMean) {
+      s1 = lanes_sum(s1, lanes);
+      s2 = lanes_sum(s2, lanes);
+    } else {
+      s2 = group_sum(s2, lanes);
+    }
     if (a.lanes > 64) {
       if ((t & 63) == 0) {
         part[0][t >> 6] = s1;
@@ -151,6 +205,7 @@ __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
       if (valid) store_stream16<kSF32>(a.r, off, v);
     float s;
     double mu = 0.0;
+    forget(v);
     if constexpr (kMean) {
       s = row_statistics(s1, s2, p, k, a.eps, mu);
       layernorm16<kWF32>(v, mu, s, w, b, has_bias);
@@ -163,40 +218,36 @@ __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
       normalize16<kWF32>(v, s, w);
     }
 
-    if (a.mode == kNormFp8) {
+    if constexpr (kMode == kNormFp8) {
       float scale;
       const uint4 code = fp8_block16(v, scale);
       if (valid) {
         *reinterpret_cast<uint4*>(a.codes + off) = code;
         if ((c & 7) == 0) a.block_scales[(int64_t)(c >> 3) * a.rows + row] = scale;
       }
-      continue;
-    }
-    if constexpr (kMean) {
-      if (a.mode == kNormOut) {
-        if (valid) store16_bf16(a.y + off, v);
-        if (a.codes != nullptr) {
-          uint32_t sb;
-          const uint4 code = ck_pack16(v, sb);
-          if (valid) {
-            *reinterpret_cast<uint4*>(a.codes + off) = code;
-            if ((c & 1) == 0) a.scales[row * ((k + kCkBlock - 1) / kCkBlock) + (c >> 1)] = (uint8_t)sb;
-          }
+    } else if constexpr (kMode == kNormOut) {
+      if (valid) store16_bf16(a.y + off, v);
+      if (a.codes != nullptr) {
+        uint32_t sb;
+        const uint4 code = ck_pack16(v, sb);
+        if (valid) {
+          *reinterpret_cast<uint4*>(a.codes + off) = code;
+          if ((c & 1) == 0) a.scales[row * ((k + kCkBlock - 1) / kCkBlock) + (c >> 1)] = (uint8_t)sb;
         }
-        continue;
       }
+    } else if constexpr (kMode == kNormStats) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      if (c == 0 && row < a.rows) {
+        a.rstd[row] = s;
+        a.mean[row] = mu;
+      }
+    } else {
       float gsf = gsf_static;
-      if (a.mode != kNormStatic) {
+      if constexpr (kMode == kNormOneRow) {
+        // the one row: its abs-max over the workgroup (rows beyond it are zeros)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
-        if (a.mode == kNormStats) {
-          if (c == 0 && row < a.rows) {
-            a.rstd[row] = s;
-            a.mean[row] = mu;
-          }
-          continue;
-        }
-        // the one row: its abs-max over the workgroup (rows beyond it are zeros)
         mx = wave_max(mx);
         if ((t & 63) == 0) pmax[t >> 6] = mx;
         __syncthreads();
@@ -209,15 +260,13 @@ __global__ void __launch_bounds__(1024) layernorm_kernel(const NormForward a) {
       quantize_unit<false>(v, urow, c >> 3, c & 7, a.rows, k, 0, 1.0f, gsf, a.codes, a.scales, nullptr);
     }
   }
-  if constexpr (kMean) {
-    if (a.mode == kNormStats) {
-      mx = wave_max(mx);
-      if ((t & 63) == 0) pmax[t >> 6] = mx;
-      __syncthreads();
-      if (t == 0) {
-        for (int i = 1; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
-        a.partials[blockIdx.x] = mx;
-      }
+  if constexpr (kMode == kNormStats) {
+    mx = wave_max(mx);
+    if ((t & 63) == 0) pmax[t >> 6] = mx;
+    __syncthreads();
+    if (t == 0) {
+      for (int i = 1; i < (int)(blockDim.x >> 6); ++i) mx = fmaxf(mx, pmax[i]);
+      a.partials[blockIdx.x] = mx;
     }
   }
 }
@@ -289,6 +338,9 @@ __global__ void __launch_bounds__(kNormQThreads) layernorm_quantize_kernel(const
 //
 // Each workgroup walks its rows with its lanes' 16 columns of grad_w and grad_b in registers and
 // writes one partial row of both; layernorm_weight_grad_kernel adds the partials in a fixed order.
+//
+// (Eight values a lane, in half the registers, take twice the waves per row and as many sums for
+// half the work: 16384 x 1024 61 us against 45, 4091 x 5120 with an fp32 stream 93 against 75.)
 template <bool kSF32, bool kWF32, bool kRes>
 __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBackward a) {
   __shared__ double part[2][4][16];
@@ -300,8 +352,8 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
   const int64_t k = a.k;
   const bool in_k = c < k / kBlock;
   Raw16<kWF32> w;
+  w.zero();
   if (in_k) w.load(a.w, (int64_t)c * kBlock);
-  else w.zero();
   float gw[16], gb[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) gw[i] = gb[i] = 0.0f;
@@ -316,33 +368,28 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
     Raw16<kSF32> rr, gres;
     Raw16<false> gy;
     float p = 0.0f;
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
     if (valid) {
       rr.load(a.r, off);
       p = stream_value<kSF32, 0>(a.r, nullptr, row * k);
       gy.load(a.gy, off);
       if constexpr (kRes) gres.load(a.grad_residual, off);
-    } else {
-      rr.zero();
-      gy.zero();
-      if constexpr (kRes) gres.zero();
-    }
-    float r[16];
+      float sg = 0.0f, sgd = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = rr.get(i);
-    double sum[4];
-    pivot_sums(r, p, sum[0], sum[1]);
-    float sg = 0.0f, sgd = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float g = gy.get(i) * w.get(i);
-      sg += g;
-      sgd = fmaf(g, r[i] - p, sgd);
+      for (int i = 0; i < 16; ++i) {
+        const double d = (double)rr.get(i) - (double)p;
+        sum[0] += d;
+        sum[1] = fma(d, d, sum[1]);
+        const float g = gy.get(i) * w.get(i);
+        sg += g;
+        sgd = fmaf(g, rr.get(i) - p, sgd);
+      }
+      sum[2] = (double)sg;
+      sum[3] = (double)sgd;
     }
-    sum[2] = (double)sg;
-    sum[3] = (double)sgd;
     const int lanes = a.lanes < 64 ? a.lanes : 64;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum[q] = group_sum(sum[q], lanes);
+    for (int q = 0; q < 4; ++q) sum[q] = lanes_sum(sum[q], lanes);
     if (a.lanes > 64) {
       // the other parity's slots may still be read by slower waves; these are free
       if ((t & 63) == 0) {
@@ -357,35 +404,48 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
         for (int q = 0; q < 4; ++q) sum[q] += part[parity][q][i];
       }
     }
-    // 0 for lanes without values: with eps = 0 a row beyond the last would have an infinite scale,
-    // and its part of grad_w (0 times it) would be NaN
+    // lanes without values add nothing: with eps = 0 the scale of a row beyond the last would be
+    // infinite, and its part of grad_w (0 times it) NaN
+    if (!valid) continue;
     double mu;
-    float s = row_statistics(sum[0], sum[1], p, k, a.eps, mu);
-    if (!valid) {
-      s = 0.0f;
-      mu = 0.0;
-    }
+    const float s = row_statistics(sum[0], sum[1], p, k, a.eps, mu);
     const float f1 = (float)(sum[2] * inv_k);
     const float f2 = s * (float)((sum[3] - (mu - (double)p) * sum[2]) * inv_k);
+    forget(rr);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float n = (float)((double)r[i] - mu) * s, g = gy.get(i);
-      gw[i] = fmaf(g, n, gw[i]);
-      gb[i] += g;
-      const float x = s * (fmaf(g, w.get(i), -f1) - n * f2);
-      r[i] = kRes ? x + gres.get(i) : x;
-    }
-    if (valid) {
-      if constexpr (!kSF32) round_bf16(r);
-      store_stream16<kSF32>(a.grad_r, off, r);
+    for (int h = 0; h < 16; h += 8) {
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = h + q;
+        const float n = (float)((double)rr.get(i) - mu) * s, g = gy.get(i);
+        gw[i] = fmaf(g, n, gw[i]);
+        gb[i] += g;
+        x[q] = s * (fmaf(g, w.get(i), -f1) - n * f2);
+        if constexpr (kRes) x[q] += gres.get(i);
+      }
+      if constexpr (kSF32) {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.grad_r) + off + h);
+        d[0] = make_float4(x[0], x[1], x[2], x[3]);
+        d[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_r) + off + h) =
+            make_uint4(gemm::pack_bf16x2(x[0], x[1]), gemm::pack_bf16x2(x[2], x[3]), gemm::pack_bf16x2(x[4], x[5]),
+                       gemm::pack_bf16x2(x[6], x[7]));
+      }
     }
   }
   if (a.partials == nullptr) return;
   float* const row_out = a.partials + (int64_t)blockIdx.x * 2 * k + (int64_t)c * kBlock;
+  auto store = [&](const float (&g)[16], int64_t at) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<float4*>(row_out + at + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+  };
   if (rows_here == 1) {
     if (in_k) {
-      store_stream16<true>(row_out, 0, gw);
-      store_stream16<true>(row_out, k, gb);
+      store(gw, 0);
+      store(gb, k);
     }
     return;
   }
@@ -398,7 +458,7 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
       for (int s = 1; s < rows_here; ++s)
 #pragma unroll
         for (int i = 0; i < 16; ++i) g[i] += colsum[(s * a.lanes + c) * 16 + i];
-      store_stream16<true>(row_out, at, g);
+      store(g, at);
     }
   };
   join(gw, 0);
@@ -431,20 +491,31 @@ __global__ void __launch_bounds__(1024) layernorm_weight_grad_kernel(const float
 
 using ForwardFn = void (*)(const NormForward);
 
-template <bool kMean>
-ForwardFn forward_kernel(const NormForward& a) {
+template <bool kMean, int kMode>
+ForwardFn forward_of(const NormForward& a) {
   const int w = a.w_f32 ? 1 : 0;
   if (a.residual == nullptr) {
     static constexpr ForwardFn f[2][2] = {
-        {layernorm_kernel<false, 0, false, kMean>, layernorm_kernel<false, 0, true, kMean>},
-        {layernorm_kernel<true, 0, false, kMean>, layernorm_kernel<true, 0, true, kMean>}};
+        {layernorm_kernel<false, 0, false, kMean, kMode>, layernorm_kernel<false, 0, true, kMean, kMode>},
+        {layernorm_kernel<true, 0, false, kMean, kMode>, layernorm_kernel<true, 0, true, kMean, kMode>}};
     return f[a.x_f32 ? 1 : 0][w];
   }
   static constexpr ForwardFn f[3][2] = {
-      {layernorm_kernel<false, 1, false, kMean>, layernorm_kernel<false, 1, true, kMean>},
-      {layernorm_kernel<false, 2, false, kMean>, layernorm_kernel<false, 2, true, kMean>},
-      {layernorm_kernel<true, 2, false, kMean>, layernorm_kernel<true, 2, true, kMean>}};
+      {layernorm_kernel<false, 1, false, kMean, kMode>, layernorm_kernel<false, 1, true, kMean, kMode>},
+      {layernorm_kernel<false, 2, false, kMean, kMode>, layernorm_kernel<false, 2, true, kMean, kMode>},
+      {layernorm_kernel<true, 2, false, kMean, kMode>, layernorm_kernel<true, 2, true, kMean, kMode>}};
   return f[!a.stream_f32 ? 0 : !a.x_f32 ? 1 : 2][w];
+}
+
+ForwardFn forward_kernel(const NormForward& a, bool mean) {
+  if (!mean) return forward_of<false, kNormFp8>(a);
+  switch (a.mode) {
+    case kNormFp8: return forward_of<true, kNormFp8>(a);
+    case kNormOut: return forward_of<true, kNormOut>(a);
+    case kNormStatic: return forward_of<true, kNormStatic>(a);
+    case kNormOneRow: return forward_of<true, kNormOneRow>(a);
+    default: return forward_of<true, kNormStats>(a);
+  }
 }
 
 }  // namespace
@@ -459,8 +530,7 @@ hipError_t launch_layernorm(NormForward a, bool mean, hipStream_t s) {
     a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
     blocks = walking_blocks(a.rows, shape);
   }
-  const ForwardFn fn = mean ? forward_kernel<true>(a) : forward_kernel<false>(a);
-  hipLaunchKernelGGL(fn, dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
+  hipLaunchKernelGGL(forward_kernel(a, mean), dim3((uint32_t)blocks), dim3((uint32_t)shape.threads), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.mode != kNormStats) return e;
   using QuantFn = void (*)(const NormForward, int);
