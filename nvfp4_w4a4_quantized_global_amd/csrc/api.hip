@@ -1223,7 +1223,7 @@ int nvfp4_fp8_linear(const void* x, const void* up, int64_t m, int64_t k, const 
   if (nvfp4::linear_fp8_fused_supported(m, k, n)) {
     Range stage("nvfp4.quantize+gemm");
     return hip_status(nvfp4::launch_linear_fp8_fused(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up),
-                                                     m, k, w_codes, w_scales, n, b, ep, o, s),
+                                                     m, k, w_codes, w_scales, n, b, ep, o, nvfp4::compute_units(), s),
                       fn);
   }
   uint8_t* codes = static_cast<uint8_t*>(workspace);

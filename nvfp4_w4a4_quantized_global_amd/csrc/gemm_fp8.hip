@@ -307,54 +307,79 @@ __global__ void __launch_bounds__(256) gemm_fp8_reduce(const float* __restrict__
 
 // ---- few rows: the weight is streamed once ----
 
-// A workgroup owns 16 weight rows, its waves a K range each; a wave multiplies every block of its
-// rows with kTA tiles of 16 activation rows, several blocks' loads in flight, and the waves' sums
-// meet in LDS.  kFused (one tile): x is bf16 (or gate, with up), and each wave first quantizes its
-// own K range of the m rows into LDS.
+// A workgroup owns `nrows` weight rows (a multiple of 4), up to kTB MFMA tiles of 16: an equal
+// share for every compute unit, so that none streams twice what another does.  Its waves take the
+// blocks of K in turn, so that together they read runs of kWaves * 128 bytes of each row; each
+// multiplies its blocks with kTA tiles of 16 activation rows, several blocks' loads in flight, and
+// the waves' sums meet in LDS.  kFused (one activation tile): x is bf16 (or gate, with up), and
+// each wave first quantizes its own blocks of the m rows into LDS.
+constexpr int kWaves = 8;
 constexpr int kFusedRows = 4;
 constexpr int kFusedLds = 60 * 1024;
 
-template <int kTA, int kWaves, bool kFused>
+// Blocks of K in flight per wave.  Measured with the first figure 3, 4 and 6 (and the others in
+// proportion): one row, 5120 -> 25600 26.7, 28.3, 30.9 us; 16 rows, 25600 -> 5120 39.6, 41.2, 41.8;
+// 64 rows, 25600 -> 5120 with one block in flight 89, with two 73.
+constexpr int skinny_depth(int ta, int tb) { return ta + tb <= 2 ? 3 : ta + tb <= 3 || ta + tb == 6 ? 2 : 1; }
+
+template <int kTA, int kTB, bool kFused>
 __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
     const void* __restrict__ x, const uint16_t* __restrict__ up, const float* __restrict__ x_scales, int64_t m,
-    int64_t k, const uint8_t* __restrict__ w_codes, const float* __restrict__ w_scales, int64_t n,
+    int64_t k, const uint8_t* __restrict__ w_codes, const float* __restrict__ w_scales, int64_t n, int nrows,
     const uint16_t* __restrict__ bias, uint16_t* out, const Epilogue ep) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int kDepth = kTA == 1 ? 4 : 2;   // blocks in flight
+  constexpr int kDepth = skinny_depth(kTA, kTB);   // blocks in flight
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * nrows;
+  const int here = (int)min(n - n0, (int64_t)nrows);
   const int kb_all = (int)((k + kFp8Block - 1) / kFp8Block);
-  const int kb0 = (int)((int64_t)kb_all * wave / kWaves), kb1 = (int)((int64_t)kb_all * (wave + 1) / kWaves);
   const int r = lane & 15, g = lane >> 4;
-
-  const __amdgpu_buffer_rsrc_t wbuf = rsrc_of(w_codes + n0 * k, (uint32_t)(min(n - n0, (int64_t)16) * k));
-  const uint32_t wrow = (uint32_t)(r * k);
+  // blocks that hold this lane's first and second chunk: the last may be short
+  const int lim0 = (int)((k - 16 * g + kFp8Block - 1) / kFp8Block), lim1 = (int)((k - 64 - 16 * g + kFp8Block - 1) / kFp8Block);
   auto load32 = [&](__amdgpu_buffer_rsrc_t buf, uint32_t row, int kb) {
-    const int64_t c0 = (int64_t)kb * kFp8Block + 16 * g, c1 = c0 + 64;
-    const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(c0 < k && kb < kb1 ? row + (uint32_t)c0 : kOutside), 0, 0);
-    const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(c1 < k && kb < kb1 ? row + (uint32_t)c1 : kOutside), 0, 0);
+    const uint32_t off = row + (uint32_t)kb * kFp8Block;
+    const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(kb < lim0 ? off : kOutside), 0, 0);
+    const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(buf, (int)(kb < lim1 ? off + 64 : kOutside), 0, 0);
     return int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
-  int8v fw[kDepth];
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) fw[d] = load32(wbuf, wrow, kb0 + d);
-  const float* ws = w_scales + (n0 / kFp8Block) * kb_all;
 
-  float4v acc[kTA];
+  const __amdgpu_buffer_rsrc_t wbuf = rsrc_of(w_codes + n0 * k, (uint32_t)((int64_t)here * k));
+  uint32_t wrow[kTB];
+  int8v fw[kDepth][kTB];
 #pragma unroll
-  for (int i = 0; i < kTA; ++i) acc[i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < kTB; ++j) wrow[j] = 16 * j + r < here ? (uint32_t)((16 * j + r) * k + 16 * g) : kOutside;
+  auto load_w = [&](int d, int kb) {
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) fw[d][j] = load32(wbuf, wrow[j], kb);
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load_w(d, wave + kWaves * d);
+  // The rows meet two of the weight's 128-row scale blocks at most; a lane's results are four rows
+  // of one of them.
+  const int64_t nb0 = n0 / kFp8Block, nb1 = (n0 + here - 1) / kFp8Block;
+  const float *ws0 = w_scales + nb0 * kb_all, *ws1 = w_scales + nb1 * kb_all;
+  bool second[kTB];
+#pragma unroll
+  for (int j = 0; j < kTB; ++j) second[j] = (n0 + 16 * j + 4 * g) / kFp8Block != nb0;
+
+  float4v acc[kTA][kTB];
+#pragma unroll
+  for (int i = 0; i < kTA; ++i)
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 
   if constexpr (kFused) {
     // this wave's [m][blocks] codes, and behind all waves' codes its scales; eight lanes own a block
-    const int blocks = kb1 - kb0;
-    uint8_t* xq = lds + kb0 * (int)m * kFp8Block;
-    float* xs = reinterpret_cast<float*>(lds + kb_all * (int)m * kFp8Block) + kb0 * (int)m;
+    const int blocks = (kb_all - wave + kWaves - 1) / kWaves;
+    const int before = wave * (kb_all / kWaves) + min(wave, kb_all % kWaves);   // blocks of the waves before
+    uint8_t* xq = lds + before * (int)m * kFp8Block;
+    float* xs = reinterpret_cast<float*>(lds + kb_all * (int)m * kFp8Block) + before * (int)m;
     const uint16_t* xb = static_cast<const uint16_t*>(x);
     for (int u0 = 0; u0 < blocks * (int)m; u0 += 8) {
       const int u = u0 + (lane >> 3);
       const int row = u / blocks, b = u - row * blocks;
-      const int64_t col = (int64_t)(kb0 + b) * kFp8Block + 16 * (lane & 7);
+      const int64_t col = (int64_t)(wave + kWaves * b) * kFp8Block + 16 * (lane & 7);
       float v[16];
       if (u < blocks * (int)m && col < k) {
         load16_bf16(xb + row * k + col, v);
@@ -378,45 +403,54 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
     lds_order();
     const int row = min(r, (int)m - 1);   // rows past the last repeat it and are not written
     const uint8_t* xr = xq + row * blocks * kFp8Block + 16 * g;
-    for (int kb = kb0; kb < kb1; kb += kDepth) {
+    const float* xsr = xs + row * blocks;
+    for (int b = 0; b < blocks; b += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        const int8v w = fw[d];
-        fw[d] = load32(wbuf, wrow, kb + d + kDepth);
-        if (kb + d < kb1) {
-          const uint8_t* p = xr + (kb + d - kb0) * kFp8Block;
+        if (b + d < blocks) {
+          const uint8_t* p = xr + (b + d) * kFp8Block;
           const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(p), hi = *reinterpret_cast<const u32x4_t*>(p + 64);
           const int8v fx = int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-          add_scaled(acc[0], xs[row * blocks + kb + d - kb0] * ws[kb + d], block_mfma(w, fx));
+          const float sx = xsr[b + d];
+          const float s0 = ws0[wave + kWaves * (b + d)], s1 = ws1[wave + kWaves * (b + d)];
+#pragma unroll
+          for (int j = 0; j < kTB; ++j) add_scaled(acc[0][j], sx * (second[j] ? s1 : s0), block_mfma(fw[d][j], fx));
         }
+        load_w(d, wave + kWaves * (b + d + kDepth));
       }
     }
   } else {
     const __amdgpu_buffer_rsrc_t xbuf = rsrc_of(x, (uint32_t)(m * k));
     const __amdgpu_buffer_rsrc_t sbuf = rsrc_of(x_scales, (uint32_t)(m * kb_all * 4));
-    uint32_t xrow[kTA];
+    uint32_t xrow[kTA], srow[kTA];
     int8v fx[kDepth][kTA];
     float sx[kDepth][kTA];
 #pragma unroll
-    for (int i = 0; i < kTA; ++i) xrow[i] = 16 * i + r < m ? (uint32_t)((16 * i + r) * k) : kOutside;
+    for (int i = 0; i < kTA; ++i) {
+      xrow[i] = 16 * i + r < m ? (uint32_t)((16 * i + r) * k + 16 * g) : kOutside;
+      srow[i] = 16 * i + r < m ? (uint32_t)((16 * i + r) * 4) : kOutside;
+    }
     auto load_x = [&](int d, int kb) {
 #pragma unroll
       for (int i = 0; i < kTA; ++i) {
         fx[d][i] = load32(xbuf, xrow[i], kb);
-        const bool in = 16 * i + r < m && kb < kb1;
-        sx[d][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, (int)(in ? (uint32_t)((kb * m + 16 * i + r) * 4) : kOutside), 0, 0));
+        sx[d][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, (int)(kb < kb_all ? srow[i] + (uint32_t)(kb * m * 4) : kOutside), 0, 0));
       }
     };
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load_x(d, kb0 + d);
-    for (int kb = kb0; kb < kb1; kb += kDepth) {
+    for (int d = 0; d < kDepth; ++d) load_x(d, wave + kWaves * d);
+    for (int kb = wave; kb < kb_all; kb += kWaves * kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        const float sw = ws[min(kb + d, kb_all - 1)];
+        const int kc = min(kb + kWaves * d, kb_all - 1);   // past the last block the codes are zeros
+        const float s0 = ws0[kc], s1 = ws1[kc];
 #pragma unroll
-        for (int i = 0; i < kTA; ++i) add_scaled(acc[i], sx[d][i] * sw, block_mfma(fw[d], fx[d][i]));
-        fw[d] = load32(wbuf, wrow, kb + d + kDepth);
-        load_x(d, kb + d + kDepth);
+        for (int i = 0; i < kTA; ++i)
+#pragma unroll
+          for (int j = 0; j < kTB; ++j)
+            add_scaled(acc[i][j], sx[d][i] * (second[j] ? s1 : s0), block_mfma(fw[d][j], fx[d][i]));
+        load_w(d, kb + kWaves * (d + kDepth));
+        load_x(d, kb + kWaves * (d + kDepth));
       }
     }
   }
@@ -425,17 +459,22 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
   __syncthreads();
   float4v* red = reinterpret_cast<float4v*>(lds);
 #pragma unroll
-  for (int i = 0; i < kTA; ++i) red[(wave * kTA + i) * 64 + lane] = acc[i];
+  for (int i = 0; i < kTA; ++i)
+#pragma unroll
+    for (int j = 0; j < kTB; ++j) red[((wave * kTA + i) * kTB + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  for (int u = t; u < kTA * 64; u += 64 * kWaves) {
+  for (int u = t; u < kTA * kTB * 64; u += 64 * kWaves) {
+    const int tile = u >> 6, j = tile % kTB;
+    const int64_t row = 16 * (tile / kTB) + (u & 15);
+    const int c = 16 * j + 4 * ((u & 63) >> 4);
+    if (row >= m || c >= here) continue;
     float4v z = red[u];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) z += red[w * kTA * 64 + u];
-    const int64_t row = 16 * (u >> 6) + (u & 15), col = n0 + 4 * ((u & 63) >> 4);
-    if (row >= m) continue;
+    for (int w = 1; w < kWaves; ++w) z += red[w * kTA * kTB * 64 + u];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (col + e < n) out[row * n + col + e] = (uint16_t)finish_bf16(z[e], bias, col + e, ep, row * n + col + e);
+      if (c + e < here)
+        out[row * n + n0 + c + e] = (uint16_t)finish_bf16(z[e], bias, n0 + c + e, ep, row * n + n0 + c + e);
   }
 }
 
@@ -511,22 +550,33 @@ hipError_t launch_tiles(const Plan& p, const uint8_t* a_codes, const float* a_sc
   return hipGetLastError();
 }
 
+// Tiles of weight rows per workgroup, and rows: an equal share (a multiple of 4) for each of a
+// whole number of workgroups per compute unit.
+struct Rows {
+  int tiles, rows;
+};
+Rows skinny_rows(int64_t n, int cus, int most) {
+  int tiles = 1;
+  while (tiles < most && n > (int64_t)cus * 16 * tiles) tiles *= 2;
+  const int64_t rounds = (n + (int64_t)cus * 16 * tiles - 1) / ((int64_t)cus * 16 * tiles);
+  const int64_t share = (n + cus * rounds - 1) / (cus * rounds);
+  return {tiles, (int)((share + 3) / 4 * 4)};
+}
+
 template <int kTA, bool kFused>
 hipError_t launch_skinny(const void* x, const uint16_t* up, const float* x_scales, int64_t m, int64_t k,
                          const uint8_t* b_codes, const float* b_scales, int64_t n, const uint16_t* bias,
-                         const Epilogue& ep, uint16_t* out, hipStream_t s) {
+                         const Epilogue& ep, uint16_t* out, int cus, hipStream_t s) {
+  constexpr int kMost = kTA == 4 ? 2 : 4;
+  const Rows p = skinny_rows(n, cus, kMost);
   const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
-  const dim3 grid((uint32_t)((n + 15) / 16));
-  auto lds = [&](int waves) {
-    const size_t x_bytes = kFused ? (size_t)kb * (size_t)m * (kFp8Block + 4) : 0;
-    return (uint32_t)std::max<size_t>(x_bytes, (size_t)waves * kTA * 1024);
-  };
-  if (kb >= 16)
-    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kTA, 8, kFused>), grid, dim3(512), lds(8), s, x, up, x_scales, m, k,
-                       b_codes, b_scales, n, bias, out, ep);
-  else
-    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kTA, 4, kFused>), grid, dim3(256), lds(4), s, x, up, x_scales, m, k,
-                       b_codes, b_scales, n, bias, out, ep);
+  const size_t x_bytes = kFused ? (size_t)kb * (size_t)m * (kFp8Block + 4) : 0;
+  const uint32_t lds = (uint32_t)std::max<size_t>(x_bytes, (size_t)kWaves * kTA * p.tiles * 1024);
+  const auto fn = p.tiles == 1   ? gemm_fp8_skinny_kernel<kTA, 1, kFused>
+                  : p.tiles == 2 ? gemm_fp8_skinny_kernel<kTA, 2, kFused>
+                                 : gemm_fp8_skinny_kernel<kTA, kMost, kFused>;
+  hipLaunchKernelGGL(fn, dim3((uint32_t)((n + p.rows - 1) / p.rows)), dim3(64 * kWaves), lds, s, x, up, x_scales, m, k,
+                     b_codes, b_scales, n, p.rows, bias, out, ep);
   return hipGetLastError();
 }
 
@@ -540,7 +590,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
   Plan p = plan_of(m, k, n, cus);
   if (p.kind == kSkinny) {
     const auto fn = m <= 16 ? launch_skinny<1, false> : m <= 32 ? launch_skinny<2, false> : launch_skinny<4, false>;
-    return fn(a_codes, nullptr, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, s);
+    return fn(a_codes, nullptr, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, cus, s);
   }
   if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes)) p.splits = 1;
   return (p.kind == kLargeTiles ? launch_tiles<Large> : launch_tiles<Small>)(
@@ -554,8 +604,8 @@ bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n) {
 
 hipError_t launch_linear_fp8_fused(const uint16_t* x, const uint16_t* up, int64_t m, int64_t k, const uint8_t* b_codes,
                                    const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep,
-                                   uint16_t* out, hipStream_t s) {
-  return launch_skinny<1, true>(x, up, nullptr, m, k, b_codes, b_scales, n, bias, ep, out, s);
+                                   uint16_t* out, int cus, hipStream_t s) {
+  return launch_skinny<1, true>(x, up, nullptr, m, k, b_codes, b_scales, n, bias, ep, out, cus, s);
 }
 
 }  // namespace nvfp4

@@ -231,7 +231,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
 bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n);
 hipError_t launch_linear_fp8_fused(const uint16_t* x, const uint16_t* up, int64_t m, int64_t k, const uint8_t* b_codes,
                                    const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep,
-                                   uint16_t* out, hipStream_t s);
+                                   uint16_t* out, int cus, hipStream_t s);
 
 // grad_w [n][k] (fp32, or bf16) = sum over rows of gy [rows][n] x checkpoint [rows][k]
 // (weight_grad.hip).  partial: fp32 split sums, weight_grad_workspace_bytes of them, or
