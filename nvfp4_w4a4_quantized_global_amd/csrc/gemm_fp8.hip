@@ -39,6 +39,10 @@ __device__ __forceinline__ void add_scaled(float4v& acc, float s, const float4v&
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(s, t[e], acc[e]);
 }
 
+// Keeps a sum's additions in front of this point: free to move, they gather behind the MFMAs of a
+// whole block of K, whose results then need more registers than there are.
+__device__ __forceinline__ void pin(float4v& acc) { asm volatile("" : "+v"(acc)); }
+
 // A buffer of `bytes` bytes from p (wave-uniform): loads past them return zero.
 __device__ __forceinline__ u32x4_t buffer_of(const void* p, uint32_t bytes) {
   const uint64_t a = (uint64_t)p;
@@ -79,12 +83,16 @@ struct Geo {
   static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_;
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
   static constexpr int kBM = 16 * kWM * kTM, kBN = 16 * kWN * kTN;
-  static constexpr int kOffB = 128 * kBM, kOffS = kOffB + 128 * kBN, kStage = kOffS + 4 * kBM;
+  static constexpr int kOffSB = 4 * kBM;                     // the weight's scales, behind the rows'
+  static constexpr int kOffA = (kOffSB + 4 * (kBN / 128) + 1023) / 1024 * 1024;
+  static constexpr int kOffB = kOffA + 128 * kBM, kStage = kOffB + 128 * kBN;
   static constexpr int kLds = 2 * kStage;
   static constexpr int kCopyA = kBM / 8 / kWaves, kCopyB = kBN / 8 / kWaves;   // copy instructions of a wave
   static constexpr int kEpiRow = 16 * kTN + 4;                                  // words per staged output row
   static constexpr int kEpiWave = 16 * kEpiRow * 4;
   static_assert(kTN == 4, "a wave's 64 columns: eight lanes a row in the epilogue, one weight scale");
+  static_assert(kTM % 2 == 0, "the first and the last tile of a block in different registers");
+  static_assert(kWaves > kBM / 64, "a wave for the weight's scales");
   static_assert(kCopyA * 8 * kWaves == kBM && kCopyB * 8 * kWaves == kBN && kBM % 64 == 0, "whole copies");
   static_assert(kWaves * kEpiWave <= kLds, "epilogue staging fits in the stages");
 };
@@ -145,17 +153,23 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   const uint32_t brow = (uint32_t)((8 * G::kCopyB * wave + (lane >> 3)) * k);
   const uint32_t step8 = (uint32_t)(8 * k);
   const uint32_t srows = (uint32_t)min(m - row0, (int64_t)G::kBM) * 4;
-  auto fetch = [&](int kt) {
+  // the scales of this tile's 128-row blocks of the weight, one row of kb_all each
+  const int64_t nb0 = col0 / kFp8Block, nblocks = (n + kFp8Block - 1) / kFp8Block;
+  const u32x4_t sbuf = buffer_of(b_scales + nb0 * kb_all, (uint32_t)((nblocks - nb0) * kb_all * 4));
+  // Part q of block kt's copies into its stage; blocks past the last are zeros.
+  constexpr int kParts = G::kCopyA + G::kCopyB + 1;
+  auto fetch = [&](int kt, int q) {
     uint8_t* st = lds + (kt & 1) * G::kStage;
-    const uint32_t koff = (int64_t)kt * kFp8Block + chunk < k ? (uint32_t)(kt * kFp8Block + chunk) : kOutside;
-#pragma unroll
-    for (int i = 0; i < G::kCopyA; ++i)
-      copy16_to_lds(abuf, arow + i * step8 + koff, st + (G::kCopyA * wave + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < G::kCopyB; ++i)
-      copy16_to_lds(bbuf, brow + i * step8 + koff, st + G::kOffB + (G::kCopyB * wave + i) * 1024);
-    if (wave < G::kBM / 64)
-      copy4_to_lds(buffer_of(a_scales + (int64_t)kt * m + row0, srows), (uint32_t)t * 4, st + G::kOffS + wave * 256);
+    const uint32_t koff = kt < kt_end && (int64_t)kt * kFp8Block + chunk < k ? (uint32_t)(kt * kFp8Block + chunk) : kOutside;
+    if (q < G::kCopyA) {
+      copy16_to_lds(abuf, arow + q * step8 + koff, st + G::kOffA + (G::kCopyA * wave + q) * 1024);
+    } else if (q < G::kCopyA + G::kCopyB) {
+      copy16_to_lds(bbuf, brow + (q - G::kCopyA) * step8 + koff, st + G::kOffB + (G::kCopyB * wave + q - G::kCopyA) * 1024);
+    } else if (wave < G::kBM / 64) {
+      copy4_to_lds(buffer_of(a_scales + (int64_t)min(kt, kb_all - 1) * m + row0, srows), (uint32_t)t * 4, st + wave * 256);
+    } else if (wave == G::kWaves - 1) {
+      copy4_to_lds(sbuf, lane < G::kBN / 128 && kt < kb_all ? (uint32_t)((lane * kb_all + kt) * 4) : kOutside, st + G::kOffSB);
+    }
   };
 
   // Fragment reads: lane l takes chunks l / 16 and l / 16 + 4 of row l % 16.
@@ -172,35 +186,99 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
 #pragma unroll
     for (int j = 0; j < kTN; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int64_t nblocks = (n + kFp8Block - 1) / kFp8Block;
-  const float* bs = b_scales + min((col0 + wn * 16 * kTN) / kFp8Block, nblocks - 1) * kb_all;
+  const int abase = G::kOffA + wm * 16 * kTM * 128, bbase = G::kOffB + wn * 16 * kTN * 128;
+  const int sa_at = (wm * 16 * kTM + (lane & 15)) * 4, sb_at = G::kOffSB + wn * 16 * kTN / kFp8Block * 4;
+  int8v fb[kTN], fa[2], last;
+  float s[kTM];
+  auto read_scales = [&](const uint8_t* st) {
+    const float sb = *reinterpret_cast<const float*>(st + sb_at);
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) s[i] = sb * *reinterpret_cast<const float*>(st + sa_at + 64 * i);
+  };
 
-  fetch(kt_begin);
+  // A block of K: the tiles of A pass one after the other, each against the wave's kTN tiles of B,
+  // the next tile's fragment in flight and the results of the tile before added beside the MFMAs.
+  // The barrier stands before the last two tiles: their fragments are in registers by then, and the
+  // next stage is complete, so that the 512 cycles of their MFMAs (two waves to a SIMD) cover the
+  // reads of the next block's first fragments.  Copies into the freed stage start behind them and go
+  // on behind the next block's first tiles: in front of MFMAs they hold those up, since a compute
+  // unit takes 16 cycles for each of its 72.  (8192 x 8192 -> 8192, matrix cores busy: barrier before
+  // the last tile, copies in front 55 % of the cycles, 451 us; so 64 %, 428 us.  The clock falls from
+  // 2.0 to 1.9 GHz with it, and is 2.4 on zeros, where the times are 397 and 352 us: the card's power
+  // takes half of what a better schedule gains.)  v_mfma_f32_32x32x64 instead needs 256 registers
+  // and spills (612 us).
+  constexpr int kFirst = 3;                                          // parts beside the last two tiles
+  constexpr int kEach = (kParts - kFirst + kTM - 3) / (kTM - 2) + 1;   // and behind each of the first others
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) fetch(kt_begin, q);
+  stage_barrier();
+#pragma unroll
+  for (int q = 0; q < kFirst; ++q) fetch(kt_begin + 1, q);
+  {
+    const uint8_t* st = lds + (kt_begin & 1) * G::kStage;
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) fb[j] = fragment(st + bbase + j * 2048);
+    fa[0] = fragment(st + abase);
+    read_scales(st);
+  }
 #pragma clang loop unroll(disable)
   for (int kt = kt_begin; kt < kt_end; ++kt) {
-    stage_barrier();   // block kt is in its stage, the other stage is read
-    if (kt + 1 < kt_end) fetch(kt + 1);
     const uint8_t* st = lds + (kt & 1) * G::kStage;
-    const uint8_t* ap = st + wm * 16 * kTM * 128;
-    const uint8_t* bp = st + G::kOffB + wn * 16 * kTN * 128;
-    const float sb = bs[kt];
-    int8v fb[kTN], fa[2];
+    const uint8_t* nx = lds + ((kt + 1) & 1) * G::kStage;   // past the last block: read, not used
+    float4v p[2][kTN];
+    // tiles 0 .. kTM - 3
 #pragma unroll
-    for (int j = 0; j < kTN; ++j) fb[j] = fragment(bp + j * 2048);
-    fa[0] = fragment(ap);
-    float s[kTM];
+    for (int i = 0; i < kTM - 2; ++i) {
+      fa[(i + 1) & 1] = fragment(st + abase + (i + 1) * 2048);
+      if (i == kTM - 3) last = fragment(st + abase + (kTM - 1) * 2048);
 #pragma unroll
-    for (int i = 0; i < kTM; ++i)
-      s[i] = sb * *reinterpret_cast<const float*>(st + G::kOffS + (wm * 16 * kTM + 16 * i + (lane & 15)) * 4);
+      for (int j = 0; j < kTN; ++j) {
+        p[i & 1][j] = block_mfma(fb[j], fa[i & 1]);
+        if (i > 0) add_scaled(acc[i - 1][j], s[i - 1], p[(i - 1) & 1][j]);
+      }
+      if (i > 0) {
 #pragma unroll
-    for (int i = 0; i < kTM; ++i) {
-      if (i + 1 < kTM) fa[(i + 1) & 1] = fragment(ap + (i + 1) * 2048);
-      float4v p[kTN];
+        for (int j = 0; j < kTN; ++j) pin(acc[i - 1][j]);
+      }
 #pragma unroll
-      for (int j = 0; j < kTN; ++j) p[j] = block_mfma(fb[j], fa[i & 1]);
+      for (int j = 0; j < kTN; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < kTN; ++j) add_scaled(acc[i][j], s[i], p[j]);
+      for (int q = 0; q < kEach; ++q)
+        if (kFirst + i * kEach + q < kParts) fetch(kt + 1, kFirst + i * kEach + q);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    stage_barrier();
+    // the last two tiles, a tile of B at a time, which makes room for the next block's
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) {
+      p[0][j] = block_mfma(fb[j], fa[0]);
+      add_scaled(acc[kTM - 3][j], s[kTM - 3], p[1][j]);
+      pin(acc[kTM - 3][j]);
+      p[1][j] = block_mfma(fb[j], last);
+      fb[j] = fragment(nx + bbase + j * 2048);
+      if (j == 0) __builtin_amdgcn_sched_barrier(0);
+    }
+    fa[0] = fragment(nx + abase);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < kFirst; ++q) fetch(kt + 2, q);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) {
+      add_scaled(acc[kTM - 2][j], s[kTM - 2], p[0][j]);
+      pin(acc[kTM - 2][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) {
+      add_scaled(acc[kTM - 1][j], s[kTM - 1], p[1][j]);
+      pin(acc[kTM - 1][j]);
+    }
+    read_scales(nx);
   }
   stage_barrier();   // every wave is done with the stages
 
@@ -479,17 +557,27 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
 }
 
 // How a product runs: streamed, or in tiles of Large or Small, `full` of them in whole rounds of
-// what the GPU holds at once and the rest split along K.
+// what the GPU holds at once and the rest split along K into `splits` workgroups each.
 enum Kind { kSkinny, kLargeTiles, kSmallTiles };
 struct Plan {
   Kind kind;
   int64_t tiles_m, tiles_n, full, rest;
   int splits;
-  size_t bytes;
+  size_t bytes;   // partial tiles
+  double cost;
 };
 
+// Time in us as measured over shapes from 48 x 1024 -> 4096 to 4096 x 8192 -> 5120 (within 15 % of
+// most): a round of tiles takes its prologue and epilogue, and its blocks of K, 1.45 us of a Large
+// tile, 1.1 of two Small ones on a compute unit and 0.87 of one alone; a split adds a launch and
+// 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Small tiles whole 38.9 us,
+// in three splits 28.9, in six 37.8, in Large ones split eight ways 36.8; 2048 x 1024 -> 1024 whole
+// 11.4, in two splits 20.7; 4096 x 5120 -> 5120 in Large ones 116, in Small 136.)
 template <class G>
-Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t slots) {
+Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
+  constexpr bool kLarge = G::kBM == 256;
+  const int64_t slots = kLarge ? cus : 2 * cus;
+  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
   Plan p{};
   p.kind = kind;
   p.tiles_m = (m + G::kBM - 1) / G::kBM;
@@ -497,29 +585,33 @@ Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t slots) {
   const int64_t tiles = p.tiles_m * p.tiles_n;
   p.full = tiles / slots * slots;
   p.rest = tiles - p.full;
-  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
-  int64_t sp = p.rest > 0 ? std::min<int64_t>(slots / p.rest, kb / 4) : 1;
-  p.splits = (int)std::max<int64_t>(sp, 1);
-  p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)p.rest * G::kBM * G::kBN * sizeof(float) : 0;
+  p.splits = 1;
+  const double round = kLarge ? 6.0 : 4.0;
+  const double whole = 2.0 + (double)(p.full / slots) * (round + (double)kb * (kLarge ? 1.45 : 1.1));
+  p.cost = whole;
+  if (p.rest == 0) return p;
+  for (int64_t sp = 1; sp <= 32 && sp * p.rest <= slots && (sp == 1 || kb >= 2 * sp); ++sp) {
+    const double block = kLarge ? 1.45 : sp * p.rest <= cus ? 0.87 : 1.1;
+    const size_t bytes = sp > 1 ? (size_t)sp * (size_t)p.rest * G::kBM * G::kBN * sizeof(float) : 0;
+    const double cost = whole + round + (double)((kb + sp - 1) / sp) * block + (sp > 1 ? 2.5 + 0.45e-6 * (double)bytes : 0.0);
+    if (sp > 1 && cost >= p.cost) continue;
+    p.splits = (int)sp;
+    p.bytes = bytes;
+    p.cost = cost;
+  }
   return p;
 }
 
-// Rounds of blocks of K that a plan takes, in units of one block of a Large tile.
-double plan_cost(const Plan& p, int64_t k, int64_t slots, double block_cost) {
-  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
-  double c = (double)(p.full / slots) * kb;
-  if (p.rest > 0) c += (double)((kb + p.splits - 1) / p.splits);
-  return c * block_cost + (p.splits > 1 ? 6.0 : 0.0);
-}
-
+// Up to 32 rows the streaming kernel wins wherever it was measured (32 x 5120 -> 1024 10.5 us, Small
+// tiles 11.1; 24 x 5120 -> 5120 11.6 and 17.9); to 64 its time goes with K (64 x 25600 -> 5120 67
+// us, tiles 35; 48 x 1024 -> 4096 6.5 and 10.4).
 Plan plan_of(int64_t m, int64_t k, int64_t n, int cus) {
-  if (m <= 64 && m * k < (int64_t)kOutside) {
-    Plan p{};
-    p.kind = kSkinny;
-    return p;
-  }
-  const Plan l = tile_plan<Large>(kLargeTiles, m, k, n, cus), s = tile_plan<Small>(kSmallTiles, m, k, n, 2 * cus);
-  return plan_cost(l, k, cus, 1.0) <= plan_cost(s, k, 2 * cus, 0.7) ? l : s;
+  const bool streams = m <= 64 && m * k < (int64_t)kOutside;
+  if (m <= 32 && streams) return Plan{};
+  const Plan l = tile_plan<Large>(kLargeTiles, m, k, n, cus), s = tile_plan<Small>(kSmallTiles, m, k, n, cus);
+  const Plan& best = l.cost <= s.cost ? l : s;
+  if (streams && 4.5 + 0.32 * (double)((k + kFp8Block - 1) / kFp8Block) <= best.cost) return Plan{};
+  return best;
 }
 
 template <class G>
