@@ -111,13 +111,22 @@ __device__ __forceinline__ void tile_coords(int tile, int tiles_m, int tiles_n, 
   tn = in_band / rows;
 }
 
+// Tile u of a launch: part u % sub^2 of tile tile0 + u / sub^2.
+__device__ __forceinline__ void sub_tile_coords(int u, int tile0, int tiles_m, int tiles_n, int sub, int& tm, int& tn) {
+  const int q = sub * sub, part = u % q;
+  tile_coords(tile0 + u / q, tiles_m, tiles_n, tm, tn);
+  tm = tm * sub + part / sub;
+  tn = tn * sub + part % sub;
+}
+
 // kSplit: the tiles from tile0 on, each split along K into `splits` workgroups that write fp32
-// partial tiles; otherwise whole tiles with the epilogue of activation kAct.
+// partial tiles; otherwise whole tiles with the epilogue of activation kAct.  With sub = 2 the
+// indices count tiles of twice the height and width (tiles_m, tiles_n of those), each cut into four.
 template <class G, bool kSplit, int kAct>
 __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     const uint8_t* __restrict__ a_codes, const float* __restrict__ a_scales, int64_t m, int64_t k,
     const uint8_t* __restrict__ b_codes, const float* __restrict__ b_scales, int64_t n,
-    const uint16_t* __restrict__ bias, uint16_t* out, int tiles_m, int tiles_n, int tile0, int splits,
+    const uint16_t* __restrict__ bias, uint16_t* out, int tiles_m, int tiles_n, int tile0, int splits, int sub,
     float* __restrict__ partial, const Epilogue ep) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int kTM = G::kTM, kTN = G::kTN;
@@ -132,8 +141,9 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     bid = (bid & 7) * (nblk >> 3) + (bid >> 3);
   }
   int tm, tn;
-  tile_coords(bid + tile0, tiles_m, tiles_n, tm, tn);
+  sub_tile_coords(bid, tile0, tiles_m, tiles_n, sub, tm, tn);
   const int64_t row0 = (int64_t)tm * G::kBM, col0 = (int64_t)tn * G::kBN;
+  if (row0 >= m || col0 >= n) return;   // a quarter outside the output
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -200,20 +210,18 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   // the next tile's fragment in flight and the results of the tile before added beside the MFMAs.
   // The barrier stands before the last two tiles: their fragments are in registers by then, and the
   // next stage is complete, so that the 512 cycles of their MFMAs (two waves to a SIMD) cover the
-  // reads of the next block's first fragments.  Copies into the freed stage start behind them and go
-  // on behind the next block's first tiles: in front of MFMAs they hold those up, since a compute
-  // unit takes 16 cycles for each of its 72.  (8192 x 8192 -> 8192, matrix cores busy: barrier before
-  // the last tile, copies in front 55 % of the cycles, 451 us; so 64 %, 428 us.  The clock falls from
-  // 2.0 to 1.9 GHz with it, and is 2.4 on zeros, where the times are 397 and 352 us: the card's power
-  // takes half of what a better schedule gains.)  v_mfma_f32_32x32x64 instead needs 256 registers
-  // and spills (612 us).
-  constexpr int kFirst = 3;                                          // parts beside the last two tiles
-  constexpr int kEach = (kParts - kFirst + kTM - 3) / (kTM - 2) + 1;   // and behind each of the first others
+  // reads of the next block's first fragments.  Copies into the freed stage follow behind them: in
+  // front of MFMAs they hold those up, since a compute unit takes 16 cycles for each of its 72.
+  // (8192 x 8192 -> 8192, matrix cores busy: barrier before the last tile, copies in front 55 % of
+  // the cycles, 451 us; so 64 %, 428 us.  The clock falls from 2.0 to 1.9 GHz with it, and is 2.4 on
+  // zeros, where the times are 397 and 352 us: the card's power takes half of what a better schedule
+  // gains.  Copies spread over the next block's tiles: 5120 -> 25600 over 4096 rows 531 us, together
+  // 518.)  v_mfma_f32_32x32x64 instead needs 256 registers and spills (612 us).
 #pragma unroll
   for (int q = 0; q < kParts; ++q) fetch(kt_begin, q);
   stage_barrier();
 #pragma unroll
-  for (int q = 0; q < kFirst; ++q) fetch(kt_begin + 1, q);
+  for (int q = 0; q < kParts; ++q) fetch(kt_begin + 1, q);
   {
     const uint8_t* st = lds + (kt_begin & 1) * G::kStage;
 #pragma unroll
@@ -247,10 +255,6 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = 0; q < kEach; ++q)
-        if (kFirst + i * kEach + q < kParts) fetch(kt + 1, kFirst + i * kEach + q);
-      __builtin_amdgcn_sched_barrier(0);
     }
     stage_barrier();
     // the last two tiles, a tile of B at a time, which makes room for the next block's
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     fa[0] = fragment(nx + abase);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < kFirst; ++q) fetch(kt + 2, q);
+    for (int q = 0; q < kParts; ++q) fetch(kt + 2, q);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kTN; ++j) {
@@ -349,14 +353,14 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
 // columns per thread.
 template <class G>
 __global__ void __launch_bounds__(256) gemm_fp8_reduce(const float* __restrict__ partial, int splits, int tiles,
-                                                       int tile0, int tiles_m, int tiles_n, int64_t m, int64_t n,
-                                                       const uint16_t* __restrict__ bias, uint16_t* out,
+                                                       int tile0, int tiles_m, int tiles_n, int sub, int64_t m,
+                                                       int64_t n, const uint16_t* __restrict__ bias, uint16_t* out,
                                                        const Epilogue ep) {
   constexpr int kPerTile = G::kBM * G::kBN / 8;
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int tl = (int)(gid / kPerTile), u = (int)(gid % kPerTile);
   int tm, tn;
-  tile_coords(tile0 + tl, tiles_m, tiles_n, tm, tn);
+  sub_tile_coords(tl, tile0, tiles_m, tiles_n, sub, tm, tn);
   const int64_t row = (int64_t)tm * G::kBM + u / (G::kBN / 8), col = (int64_t)tn * G::kBN + 8 * (u % (G::kBN / 8));
   if (row >= m || col >= n) return;
   const float4v* src = reinterpret_cast<const float4v*>(partial + (int64_t)tl * (G::kBM * G::kBN) + 8 * u);
@@ -556,13 +560,14 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
   }
 }
 
-// How a product runs: streamed, or in tiles of Large or Small, `full` of them in whole rounds of
-// what the GPU holds at once and the rest split along K into `splits` workgroups each.
+// How a product runs: streamed, or in tiles: `full` of them in whole rounds of what the GPU holds
+// at once, and the rest cut into `sub` x `sub` smaller ones (1 or 2), each split along K into
+// `splits` workgroups.
 enum Kind { kSkinny, kLargeTiles, kSmallTiles };
 struct Plan {
   Kind kind;
   int64_t tiles_m, tiles_n, full, rest;
-  int splits;
+  int sub, splits;
   size_t bytes;   // partial tiles
   double cost;
 };
@@ -573,9 +578,24 @@ struct Plan {
 // 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Small tiles whole 38.9 us,
 // in three splits 28.9, in six 37.8, in Large ones split eight ways 36.8; 2048 x 1024 -> 1024 whole
 // 11.4, in two splits 20.7; 4096 x 5120 -> 5120 in Large ones 116, in Small 136.)
+// The cheapest number of splits of `units` tiles of this size, at most one round of them.
+void plan_rest(Plan& p, int64_t units, int64_t kb, int64_t cus, bool large, int sub, double before) {
+  const int64_t slots = large ? cus : 2 * cus, tile = large ? Large::kBM * Large::kBN : Small::kBM * Small::kBN;
+  for (int64_t sp = 1; sp <= 32 && sp * units <= slots && (sp == 1 || kb >= 2 * sp); ++sp) {
+    const double block = large ? 1.45 : sp * units <= cus ? 0.87 : 1.1;
+    const size_t bytes = sp > 1 ? (size_t)sp * (size_t)units * (size_t)tile * sizeof(float) : 0;
+    const double cost = before + (large ? 6.0 : 4.0) + (double)((kb + sp - 1) / sp) * block +
+                        (sp > 1 ? 2.5 + 0.45e-6 * (double)bytes : 0.0);
+    if (p.splits > 0 && cost >= p.cost) continue;
+    p.sub = sub;
+    p.splits = (int)sp;
+    p.bytes = bytes;
+    p.cost = cost;
+  }
+}
 template <class G>
 Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
-  constexpr bool kLarge = G::kBM == 256;
+  constexpr bool kLarge = G::kBM == Large::kBM;
   const int64_t slots = kLarge ? cus : 2 * cus;
   const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
   Plan p{};
@@ -585,20 +605,12 @@ Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
   const int64_t tiles = p.tiles_m * p.tiles_n;
   p.full = tiles / slots * slots;
   p.rest = tiles - p.full;
-  p.splits = 1;
-  const double round = kLarge ? 6.0 : 4.0;
-  const double whole = 2.0 + (double)(p.full / slots) * (round + (double)kb * (kLarge ? 1.45 : 1.1));
-  p.cost = whole;
+  p.cost = 2.0 + (double)(p.full / slots) * ((kLarge ? 6.0 : 4.0) + (double)kb * (kLarge ? 1.45 : 1.1));
   if (p.rest == 0) return p;
-  for (int64_t sp = 1; sp <= 32 && sp * p.rest <= slots && (sp == 1 || kb >= 2 * sp); ++sp) {
-    const double block = kLarge ? 1.45 : sp * p.rest <= cus ? 0.87 : 1.1;
-    const size_t bytes = sp > 1 ? (size_t)sp * (size_t)p.rest * G::kBM * G::kBN * sizeof(float) : 0;
-    const double cost = whole + round + (double)((kb + sp - 1) / sp) * block + (sp > 1 ? 2.5 + 0.45e-6 * (double)bytes : 0.0);
-    if (sp > 1 && cost >= p.cost) continue;
-    p.splits = (int)sp;
-    p.bytes = bytes;
-    p.cost = cost;
-  }
+  const double before = p.cost;
+  plan_rest(p, p.rest, kb, cus, kLarge, 1, before);
+  // four Small tiles for a Large one, after whole rounds
+  if (kLarge && p.full > 0) plan_rest(p, 4 * p.rest, kb, cus, false, 2, before);
   return p;
 }
 
@@ -614,32 +626,52 @@ Plan plan_of(int64_t m, int64_t k, int64_t n, int cus) {
   return best;
 }
 
+struct Args {
+  const uint8_t* a_codes;
+  const float* a_scales;
+  int64_t m, k;
+  const uint8_t* b_codes;
+  const float* b_scales;
+  int64_t n;
+  const uint16_t* bias;
+  Epilogue ep;
+  uint16_t* out;
+  float* partial;
+  hipStream_t s;
+};
+
+// `tiles` tiles from tile0 on, split or whole.
 template <class G>
-hipError_t launch_tiles(const Plan& p, const uint8_t* a_codes, const float* a_scales, int64_t m, int64_t k,
-                        const uint8_t* b_codes, const float* b_scales, int64_t n, const uint16_t* bias,
-                        const Epilogue& ep, uint16_t* out, float* partial, hipStream_t s) {
+hipError_t launch_tiles(const Args& a, const Plan& p, int64_t tiles, int64_t tile0, int sub, int splits) {
   using Fn = decltype(&gemm_fp8_kernel<G, false, 0>);
   static constexpr Fn f[5] = {gemm_fp8_kernel<G, false, NVFP4_ACT_NONE>, gemm_fp8_kernel<G, false, NVFP4_ACT_SILU>,
                               gemm_fp8_kernel<G, false, NVFP4_ACT_GELU>,
                               gemm_fp8_kernel<G, false, NVFP4_ACT_GELU_TANH>, gemm_fp8_kernel<G, true, 0>};
   static_assert(NVFP4_ACT_NONE == 0 && NVFP4_ACT_SILU == 1 && NVFP4_ACT_GELU == 2 && NVFP4_ACT_GELU_TANH == 3, "");
   static bool attr_set[5][kMaxDevices] = {};
-  auto launch = [&](int which, int64_t blocks, int64_t tile0, int splits) {
-    if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(f[which]), G::kLds, attr_set[which]);
-        e != hipSuccess)
-      return e;
-    hipLaunchKernelGGL(f[which], dim3((uint32_t)blocks), dim3(G::kThreads), G::kLds, s, a_codes, a_scales, m, k, b_codes,
-                       b_scales, n, bias, out, (int)p.tiles_m, (int)p.tiles_n, (int)tile0, splits, partial, ep);
-    return hipGetLastError();
-  };
-  if (p.full > 0)
-    if (hipError_t e = launch(ep.act, p.full, 0, 1); e != hipSuccess) return e;
-  if (p.rest == 0) return hipSuccess;
-  if (p.splits == 1) return launch(ep.act, p.rest, p.full, 1);
-  if (hipError_t e = launch(4, p.rest * p.splits, p.full, p.splits); e != hipSuccess) return e;
-  hipLaunchKernelGGL(gemm_fp8_reduce<G>, dim3((uint32_t)(p.rest * (G::kBM * G::kBN / 8 / 256))), dim3(256), 0, s, partial,
-                     p.splits, (int)p.rest, (int)p.full, (int)p.tiles_m, (int)p.tiles_n, m, n, bias, out, ep);
+  const int which = splits > 1 ? 4 : a.ep.act;
+  if (hipError_t e = set_dynamic_lds_once(reinterpret_cast<const void*>(f[which]), G::kLds, attr_set[which]);
+      e != hipSuccess)
+    return e;
+  hipLaunchKernelGGL(f[which], dim3((uint32_t)(tiles * splits)), dim3(G::kThreads), G::kLds, a.s, a.a_codes, a.a_scales,
+                     a.m, a.k, a.b_codes, a.b_scales, a.n, a.bias, a.out, (int)p.tiles_m, (int)p.tiles_n, (int)tile0,
+                     splits, sub, a.partial, a.ep);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  hipLaunchKernelGGL(gemm_fp8_reduce<G>, dim3((uint32_t)(tiles * (G::kBM * G::kBN / 8 / 256))), dim3(256), 0, a.s,
+                     a.partial, splits, (int)tiles, (int)tile0, (int)p.tiles_m, (int)p.tiles_n, sub, a.m, a.n, a.bias,
+                     a.out, a.ep);
   return hipGetLastError();
+}
+
+hipError_t launch_plan(const Args& a, const Plan& p) {
+  const bool large = p.kind == kLargeTiles;
+  if (p.full > 0)
+    if (hipError_t e = (large ? launch_tiles<Large> : launch_tiles<Small>)(a, p, p.full, 0, 1, 1); e != hipSuccess)
+      return e;
+  if (p.rest == 0) return hipSuccess;
+  if (large && p.sub == 1) return launch_tiles<Large>(a, p, p.rest, p.full, 1, p.splits);
+  return launch_tiles<Small>(a, p, p.rest * p.sub * p.sub, p.full, p.sub, p.splits);
 }
 
 // Tiles of weight rows per workgroup, and rows: an equal share (a multiple of 4) for each of a
@@ -685,8 +717,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
     return fn(a_codes, nullptr, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, cus, s);
   }
   if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes)) p.splits = 1;
-  return (p.kind == kLargeTiles ? launch_tiles<Large> : launch_tiles<Small>)(
-      p, a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), s);
+  return launch_plan({a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), s}, p);
 }
 
 bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n) {
