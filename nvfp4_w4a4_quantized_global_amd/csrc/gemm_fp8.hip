@@ -67,9 +67,11 @@ __device__ __forceinline__ void copy4_to_lds(u32x4_t rsrc, uint32_t offset, uint
   asm volatile("buffer_load_dword %1, %2, 0 offen lds"
                :: "{m0}"((uint32_t)(uintptr_t)dst), "v"(offset), "s"(rsrc) : "memory");
 }
-// Waits for this wave's copies and LDS accesses, then the workgroup barrier.
+// Waits for this wave's copies, except the last kFlying, and LDS accesses, then the workgroup barrier.
+template <int kFlying>
 __device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  static_assert(kFlying < 64, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kFlying) : "memory");
 }
 // Orders this wave's LDS accesses around a point.
 __device__ __forceinline__ void lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -78,26 +80,29 @@ __device__ __forceinline__ void lds_order() { asm volatile("s_waitcnt lgkmcnt(0)
 
 // kWM x kWN waves, each kTM x kTN MFMA tiles of 16 x 16.  A stage holds one block of K of both
 // operands (128 bytes a row) and the activations' scales.
-template <int kWM_, int kWN_, int kTM_, int kTN_>
+template <int kWM_, int kWN_, int kTM_, int kTN_, int kStages_>
 struct Geo {
-  static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_;
+  static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_, kStages = kStages_;
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
   static constexpr int kBM = 16 * kWM * kTM, kBN = 16 * kWN * kTN;
   static constexpr int kOffSB = 4 * kBM;                     // the weight's scales, behind the rows'
   static constexpr int kOffA = (kOffSB + 4 * (kBN / 128) + 1023) / 1024 * 1024;
   static constexpr int kOffB = kOffA + 128 * kBM, kStage = kOffB + 128 * kBN;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLds = kStages * kStage;
   static constexpr int kCopyA = kBM / 8 / kWaves, kCopyB = kBN / 8 / kWaves;   // copy instructions of a wave
   static constexpr int kEpiRow = 16 * kTN + 4;                                  // words per staged output row
   static constexpr int kEpiWave = 16 * kEpiRow * 4;
   static_assert(kTN == 4, "a wave's 64 columns: eight lanes a row in the epilogue, one weight scale");
   static_assert(kTM % 2 == 0, "the first and the last tile of a block in different registers");
   static_assert(kWaves > kBM / 64, "a wave for the weight's scales");
+  static_assert(kOffSB + 512 <= kOffA, "room for the other waves' copies of nothing");
+  static_assert((kStages & (kStages - 1)) == 0, "stages by a mask");
   static_assert(kCopyA * 8 * kWaves == kBM && kCopyB * 8 * kWaves == kBN && kBM % 64 == 0, "whole copies");
   static_assert(kWaves * kEpiWave <= kLds, "epilogue staging fits in the stages");
 };
-using Large = Geo<2, 4, 8, 4>;   // 256 x 256, one workgroup of eight waves per compute unit
-using Small = Geo<2, 2, 4, 4>;   // 128 x 128, two workgroups of four
+using Large = Geo<2, 4, 8, 4, 2>;   // 256 x 256, one workgroup of eight waves per compute unit
+using Small = Geo<2, 2, 4, 4, 2>;   // 128 x 128, two workgroups of four
+using Deep = Geo<2, 2, 4, 4, 4>;    // the same, one workgroup with three blocks of K in flight
 
 // Tile index -> (tile row, tile column): bands of kGroupM tile rows, column-major inside a band,
 // so that the tiles resident on one XCD share operand panels in its L2.
@@ -166,10 +171,11 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   // the scales of this tile's 128-row blocks of the weight, one row of kb_all each
   const int64_t nb0 = col0 / kFp8Block, nblocks = (n + kFp8Block - 1) / kFp8Block;
   const u32x4_t sbuf = buffer_of(b_scales + nb0 * kb_all, (uint32_t)((nblocks - nb0) * kb_all * 4));
-  // Part q of block kt's copies into its stage; blocks past the last are zeros.
+  // Part q of block kt's copies into its stage; blocks past the last are zeros.  Every wave has
+  // kParts of them, so that the waits can count.
   constexpr int kParts = G::kCopyA + G::kCopyB + 1;
   auto fetch = [&](int kt, int q) {
-    uint8_t* st = lds + (kt & 1) * G::kStage;
+    uint8_t* st = lds + (kt & (G::kStages - 1)) * G::kStage;
     const uint32_t koff = kt < kt_end && (int64_t)kt * kFp8Block + chunk < k ? (uint32_t)(kt * kFp8Block + chunk) : kOutside;
     if (q < G::kCopyA) {
       copy16_to_lds(abuf, arow + q * step8 + koff, st + G::kOffA + (G::kCopyA * wave + q) * 1024);
@@ -177,8 +183,10 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
       copy16_to_lds(bbuf, brow + (q - G::kCopyA) * step8 + koff, st + G::kOffB + (G::kCopyB * wave + q - G::kCopyA) * 1024);
     } else if (wave < G::kBM / 64) {
       copy4_to_lds(buffer_of(a_scales + (int64_t)min(kt, kb_all - 1) * m + row0, srows), (uint32_t)t * 4, st + wave * 256);
-    } else if (wave == G::kWaves - 1) {
-      copy4_to_lds(sbuf, lane < G::kBN / 128 && kt < kb_all ? (uint32_t)((lane * kb_all + kt) * 4) : kOutside, st + G::kOffSB);
+    } else {
+      const bool mine = wave == G::kWaves - 1 && lane < G::kBN / 128 && kt < kb_all;
+      copy4_to_lds(sbuf, mine ? (uint32_t)((lane * kb_all + kt) * 4) : kOutside,
+                   st + G::kOffSB + (wave == G::kWaves - 1 ? 0 : 256));
     }
   };
 
@@ -217,13 +225,12 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   // zeros, where the times are 397 and 352 us: the card's power takes half of what a better schedule
   // gains.  Copies spread over the next block's tiles: 5120 -> 25600 over 4096 rows 531 us, together
   // 518.)  v_mfma_f32_32x32x64 instead needs 256 registers and spills (612 us).
+  for (int d = 0; d < G::kStages; ++d)
 #pragma unroll
-  for (int q = 0; q < kParts; ++q) fetch(kt_begin, q);
-  stage_barrier();
-#pragma unroll
-  for (int q = 0; q < kParts; ++q) fetch(kt_begin + 1, q);
+    for (int q = 0; q < kParts; ++q) fetch(kt_begin + d, q);
+  stage_barrier<(G::kStages - 1) * kParts>();
   {
-    const uint8_t* st = lds + (kt_begin & 1) * G::kStage;
+    const uint8_t* st = lds + (kt_begin & (G::kStages - 1)) * G::kStage;
 #pragma unroll
     for (int j = 0; j < kTN; ++j) fb[j] = fragment(st + bbase + j * 2048);
     fa[0] = fragment(st + abase);
@@ -231,8 +238,8 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   }
 #pragma clang loop unroll(disable)
   for (int kt = kt_begin; kt < kt_end; ++kt) {
-    const uint8_t* st = lds + (kt & 1) * G::kStage;
-    const uint8_t* nx = lds + ((kt + 1) & 1) * G::kStage;   // past the last block: read, not used
+    const uint8_t* st = lds + (kt & (G::kStages - 1)) * G::kStage;
+    const uint8_t* nx = lds + ((kt + 1) & (G::kStages - 1)) * G::kStage;   // past the last block: read, not used
     float4v p[2][kTN];
     // tiles 0 .. kTM - 3
 #pragma unroll
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    stage_barrier();
+    stage_barrier<(G::kStages - 2) * kParts>();
     // the last two tiles, a tile of B at a time, which makes room for the next block's
 #pragma unroll
     for (int j = 0; j < kTN; ++j) {
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     fa[0] = fragment(nx + abase);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) fetch(kt + 2, q);
+    for (int q = 0; q < kParts; ++q) fetch(kt + G::kStages, q);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kTN; ++j) {
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     }
     read_scales(nx);
   }
-  stage_barrier();   // every wave is done with the stages
+  stage_barrier<0>();   // every wave is done with the stages
 
   // 16 rows at a time pass through the wave's own LDS region: lane l writes four columns of row
   // l % 16, and reads back eight columns of row 8 p + l / 8.
@@ -351,20 +358,20 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
 
 // Adds the partial tiles of `tiles` tiles from tile0 in split order and finishes them: eight
 // columns per thread.
-template <class G>
+template <int kBM, int kBN>
 __global__ void __launch_bounds__(256) gemm_fp8_reduce(const float* __restrict__ partial, int splits, int tiles,
                                                        int tile0, int tiles_m, int tiles_n, int sub, int64_t m,
                                                        int64_t n, const uint16_t* __restrict__ bias, uint16_t* out,
                                                        const Epilogue ep) {
-  constexpr int kPerTile = G::kBM * G::kBN / 8;
+  constexpr int kPerTile = kBM * kBN / 8;
   const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int tl = (int)(gid / kPerTile), u = (int)(gid % kPerTile);
   int tm, tn;
   sub_tile_coords(tl, tile0, tiles_m, tiles_n, sub, tm, tn);
-  const int64_t row = (int64_t)tm * G::kBM + u / (G::kBN / 8), col = (int64_t)tn * G::kBN + 8 * (u % (G::kBN / 8));
+  const int64_t row = (int64_t)tm * kBM + u / (kBN / 8), col = (int64_t)tn * kBN + 8 * (u % (kBN / 8));
   if (row >= m || col >= n) return;
-  const float4v* src = reinterpret_cast<const float4v*>(partial + (int64_t)tl * (G::kBM * G::kBN) + 8 * u);
-  const int64_t stride = (int64_t)tiles * (G::kBM * G::kBN / 4);
+  const float4v* src = reinterpret_cast<const float4v*>(partial + (int64_t)tl * (kBM * kBN) + 8 * u);
+  const int64_t stride = (int64_t)tiles * (kBM * kBN / 4);
   float4v a = src[0], b = src[1];
 #pragma unroll 4
   for (int s = 1; s < splits; ++s) {
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
 
 // How a product runs: streamed, or in tiles: `full` of them in whole rounds of what the GPU holds
 // at once, and the rest cut into `sub` x `sub` smaller ones (1 or 2), each split along K into
-// `splits` workgroups.
+// `splits` workgroups.  Small tiles that leave no compute unit with two run as Deep.
 enum Kind { kSkinny, kLargeTiles, kSmallTiles };
 struct Plan {
   Kind kind;
@@ -574,17 +581,19 @@ struct Plan {
 
 // Time in us as measured over shapes from 48 x 1024 -> 4096 to 4096 x 8192 -> 5120 (within 15 % of
 // most): a round of tiles takes its prologue and epilogue, and its blocks of K, 1.45 us of a Large
-// tile, 1.1 of two Small ones on a compute unit and 0.87 of one alone; a split adds a launch and
-// 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Small tiles whole 38.9 us,
-// in three splits 28.9, in six 37.8, in Large ones split eight ways 36.8; 2048 x 1024 -> 1024 whole
-// 11.4, in two splits 20.7; 4096 x 5120 -> 5120 in Large ones 116, in Small 136.)
+// tile, 1.05 of two Small ones on a compute unit and 0.6 of a Deep one; a split adds a launch and
+// 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Deep tiles whole 31.0 us, in
+// two splits 27.6, in six 37.1, in Large ones split eight ways 37.7; 2048 x 1024 -> 1024 whole 11.9,
+// in two splits 21.2; 4096 x 5120 -> 5120 in Large ones 107, in Small 118; 4096 x 5120 -> 1024, one
+// tile a compute unit, with one block of K in flight 40.1, with three 31.8.)
+constexpr double kLargeRound = 6.0, kSmallRound = 4.9, kLargeBlock = 1.45, kSmallBlock = 1.05, kDeepBlock = 0.6;
 // The cheapest number of splits of `units` tiles of this size, at most one round of them.
 void plan_rest(Plan& p, int64_t units, int64_t kb, int64_t cus, bool large, int sub, double before) {
   const int64_t slots = large ? cus : 2 * cus, tile = large ? Large::kBM * Large::kBN : Small::kBM * Small::kBN;
   for (int64_t sp = 1; sp <= 32 && sp * units <= slots && (sp == 1 || kb >= 2 * sp); ++sp) {
-    const double block = large ? 1.45 : sp * units <= cus ? 0.87 : 1.1;
+    const double block = large ? kLargeBlock : sp * units <= cus ? kDeepBlock : kSmallBlock;
     const size_t bytes = sp > 1 ? (size_t)sp * (size_t)units * (size_t)tile * sizeof(float) : 0;
-    const double cost = before + (large ? 6.0 : 4.0) + (double)((kb + sp - 1) / sp) * block +
+    const double cost = before + (large ? kLargeRound : kSmallRound) + (double)((kb + sp - 1) / sp) * block +
                         (sp > 1 ? 2.5 + 0.45e-6 * (double)bytes : 0.0);
     if (p.splits > 0 && cost >= p.cost) continue;
     p.sub = sub;
@@ -605,7 +614,7 @@ Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
   const int64_t tiles = p.tiles_m * p.tiles_n;
   p.full = tiles / slots * slots;
   p.rest = tiles - p.full;
-  p.cost = 2.0 + (double)(p.full / slots) * ((kLarge ? 6.0 : 4.0) + (double)kb * (kLarge ? 1.45 : 1.1));
+  p.cost = 2.0 + (double)(p.full / slots) * ((kLarge ? kLargeRound : kSmallRound) + (double)kb * (kLarge ? kLargeBlock : kSmallBlock));
   if (p.rest == 0) return p;
   const double before = p.cost;
   plan_rest(p, p.rest, kb, cus, kLarge, 1, before);
@@ -615,14 +624,16 @@ Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
 }
 
 // Up to 32 rows the streaming kernel wins wherever it was measured (32 x 5120 -> 1024 10.5 us, Small
-// tiles 11.1; 24 x 5120 -> 5120 11.6 and 17.9); to 64 its time goes with K (64 x 25600 -> 5120 67
-// us, tiles 35; 48 x 1024 -> 4096 6.5 and 10.4).
+// tiles 11.1; 24 x 5120 -> 5120 11.6 and 17.9); to 64 its time goes with K, and with N beyond one
+// round of it (64 x 25600 -> 5120 67 us, tiles 35; 64 x 5120 -> 25600 75 and 39; 48 x 1024 -> 4096
+// 6.5 and 10.4).
 Plan plan_of(int64_t m, int64_t k, int64_t n, int cus) {
   const bool streams = m <= 64 && m * k < (int64_t)kOutside;
   if (m <= 32 && streams) return Plan{};
   const Plan l = tile_plan<Large>(kLargeTiles, m, k, n, cus), s = tile_plan<Small>(kSmallTiles, m, k, n, cus);
   const Plan& best = l.cost <= s.cost ? l : s;
-  if (streams && 4.5 + 0.32 * (double)((k + kFp8Block - 1) / kFp8Block) <= best.cost) return Plan{};
+  const double rounds = std::max(1.0, (double)n / (32.0 * cus));   // two tiles of 16 weight rows a workgroup
+  if (streams && 4.5 + 0.32 * rounds * (double)((k + kFp8Block - 1) / kFp8Block) <= best.cost) return Plan{};
   return best;
 }
 
@@ -637,6 +648,7 @@ struct Args {
   Epilogue ep;
   uint16_t* out;
   float* partial;
+  int cus;
   hipStream_t s;
 };
 
@@ -658,7 +670,7 @@ hipError_t launch_tiles(const Args& a, const Plan& p, int64_t tiles, int64_t til
                      splits, sub, a.partial, a.ep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(gemm_fp8_reduce<G>, dim3((uint32_t)(tiles * (G::kBM * G::kBN / 8 / 256))), dim3(256), 0, a.s,
+  hipLaunchKernelGGL((gemm_fp8_reduce<G::kBM, G::kBN>), dim3((uint32_t)(tiles * (G::kBM * G::kBN / 8 / 256))), dim3(256), 0, a.s,
                      a.partial, splits, (int)tiles, (int)tile0, (int)p.tiles_m, (int)p.tiles_n, sub, a.m, a.n, a.bias,
                      a.out, a.ep);
   return hipGetLastError();
@@ -671,7 +683,8 @@ hipError_t launch_plan(const Args& a, const Plan& p) {
       return e;
   if (p.rest == 0) return hipSuccess;
   if (large && p.sub == 1) return launch_tiles<Large>(a, p, p.rest, p.full, 1, p.splits);
-  return launch_tiles<Small>(a, p, p.rest * p.sub * p.sub, p.full, p.sub, p.splits);
+  const int64_t units = p.rest * p.sub * p.sub;
+  return (units * p.splits <= a.cus ? launch_tiles<Deep> : launch_tiles<Small>)(a, p, units, p.full, p.sub, p.splits);
 }
 
 // Tiles of weight rows per workgroup, and rows: an equal share (a multiple of 4) for each of a
@@ -717,7 +730,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
     return fn(a_codes, nullptr, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, cus, s);
   }
   if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes)) p.splits = 1;
-  return launch_plan({a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), s}, p);
+  return launch_plan({a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), cus, s}, p);
 }
 
 bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n) {
