@@ -85,9 +85,9 @@ def fp8_quantize_swiglu(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Ten
     """fp8_quantize_activation(swiglu(gate, up)) without writing the product."""
     g2, u2 = _gate_up(gate, up)
     rows, k = g2.shape
-    codes, scales = _empty_codes(rows, k, g2.device)
+    codes, scales = _empty_codes(rows, k, gate.device)
     check(lib().nvfp4_fp8_quantize_activation(_ptr(g2), _ptr(u2), rows, k, _ptr(codes), _ptr(scales), None, None, 0,
-                                              _stream(g2.device)))
+                                              _stream(gate.device)))
     return codes, scales
 
 
@@ -165,14 +165,14 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
     return out
 
 
-def _linear(x2, up, m, k, codes, scales, bias, lead, workspace, out, activation, residual, preact):
-    """fp8_linear on checked contiguous rows; the result in the leading dimensions ``lead``."""
+def _linear(x, x2, up, m, k, codes, scales, bias, workspace, out, activation, residual, preact):
+    """fp8_linear of ``x`` (or gate), ``x2`` its checked contiguous rows."""
     n, wk = _weight(codes, scales)
     if wk != k:
         raise ValueError(f"codes must be uint8 [{n}, {k}], got {list(codes.shape)}")
     _bias(bias, n)
-    _operands(x2, codes=codes, scales=scales, bias=bias)
-    dev = x2.device
+    _operands(x, codes=codes, scales=scales, bias=bias)
+    dev = x.device
     act = _activation_code(activation)
     given = out
     if residual is not None or preact is not None or given is not None:
@@ -190,9 +190,9 @@ def _linear(x2, up, m, k, codes, scales, bias, lead, workspace, out, activation,
                                  _stream(dev)))
     if given is not None or preact is not None:
         _written(given, preact)
-    if len(lead) == 1 and (given is None or given.shape == (m, n)):
+    if x.dim() == 2 and (given is None or given.shape == (m, n)):
         return out
-    return out.reshape(*lead, n)
+    return out.reshape(*x.shape[:-1], n)
 
 
 @_on_device
@@ -204,7 +204,7 @@ def fp8_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias:
 
     ``out``, ``activation``, ``residual`` and ``preact`` as for :func:`nvfp4_linear`."""
     x2, m, k = _rows("x", x)
-    return _linear(x2, None, m, k, codes, scales, bias, x.shape[:-1], workspace, out, activation, residual, preact)
+    return _linear(x, x2, None, m, k, codes, scales, bias, workspace, out, activation, residual, preact)
 
 
 @_on_device
@@ -214,7 +214,7 @@ def fp8_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, codes: torch.Tensor,
                       residual: torch.Tensor | None = None, preact: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`fp8_linear` on silu(gate) * up, the product never written (down_proj)."""
     g2, u2 = _gate_up(gate, up)
-    return _linear(g2, u2, *g2.shape, codes, scales, bias, gate.shape[:-1], workspace, out, activation, residual, preact)
+    return _linear(gate, g2, u2, *g2.shape, codes, scales, bias, workspace, out, activation, residual, preact)
 
 
 class _FP8Fn(torch.autograd.Function):

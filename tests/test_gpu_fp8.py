@@ -163,7 +163,15 @@ def _case(m, k, n, seed=0):
     return x, nv().fp8_quantize_weight(w.to(DEV)), b, res
 
 
-@pytest.mark.parametrize("m,k,n", PATHS)
+# every count of activation and weight tiles of the streaming kernel (the weight's width decides the
+# latter), rows that straddle the weight's scale blocks, quarter tiles after a whole round (some of
+# them outside the output), two whole rounds, splits of quarter tiles
+WIDTHS = [(1, 144, 5000), (3, 272, 9001), (16, 144, 5001), (9, 272, 12000), (20, 144, 300), (30, 144, 5000), (32, 272, 9000),
+          (40, 144, 1000), (64, 144, 6000), (50, 272, 9003), (4100, 144, 5000), (4091, 272, 8200), (4352, 2064, 4096),
+          (8300, 16, 8001)]
+
+
+@pytest.mark.parametrize("m,k,n", PATHS + WIDTHS)
 def test_linear(m, k, n):
     x, (wc, ws), b, res = _case(m, k, n)
     xc, xs = nv().fp8_quantize_activation(x)
@@ -175,7 +183,7 @@ def test_linear(m, k, n):
     _check(g, xv, wv)
     # the same inputs give the same bits; without a workspace for the splits the same function
     assert torch.equal(nv().fp8_linear(x, wc, ws), y)
-    for act in ("gelu", "silu", "gelu_tanh"):
+    for act in ("gelu", "silu", "gelu_tanh") if m * n < 1 << 21 else ("silu",):
         pre = torch.empty(m, n, device=DEV, dtype=BF)
         _check(nv().fp8_linear(x, wc, ws, b, activation=act, residual=res, preact=pre), xv, wv, b, act, res, pre)
     _check(nv().fp8_gemm(xc, xs, wc, ws, b, residual=res), xv, wv, b, None, res)
@@ -183,6 +191,36 @@ def test_linear(m, k, n):
     h = res.clone()
     assert nv().fp8_linear(x, wc, ws, b, out=h, residual=h).data_ptr() == h.data_ptr()
     _check(h, xv, wv, b, None, res)
+
+
+def test_block():
+    """A pre-norm block as it is used: the norm writes codes, two projections read them, and the down
+    projection of their SwiGLU product is added to the residual stream in place."""
+    for m, k, f in [(1, 512, 1040), (7, 272, 528), (300, 512, 1040)]:
+        x, h = workloads.draw("normal", (m, k), 260, m).to(DEV), workloads.draw("t3", (m, k), 261, m).to(DEV)
+        lw, lb = (1 + 0.1 * torch.randn(k)).to(DEV), (0.1 * torch.randn(k)).to(DEV)
+        gate, up, down = (nv().fp8_quantize_weight(0.05 * torch.randn(s, device=DEV)) for s in ((f, k), (f, k), (k, f)))
+        for norm in ("layer", "rms"):
+            if norm == "layer":
+                codes, scales, r = nv().fp8_quantize_layernorm(x, lw, lb, 1e-6, h)
+                y, r2 = nv().layernorm(x, lw, lb, 1e-6, h)
+            else:
+                codes, scales, r = nv().fp8_quantize_rmsnorm(x, lw, 1e-6, h)
+                y, r2 = nv().rmsnorm(x, lw, 1e-6, h)
+            assert torch.equal(r, r2)
+            g, u = nv().fp8_gemm(codes, scales, *gate), nv().fp8_gemm(codes, scales, *up)
+            yv = _values(*nv().fp8_quantize_activation(y), False)
+            _check(g, yv, _values(*gate, True))
+            _check(u, yv, _values(*up, True))
+            out = nv().fp8_linear_swiglu(g, u, *down, out=r, residual=r)
+            assert out.data_ptr() == r.data_ptr()
+            p = nv().swiglu(g, u)
+            _check(out, _values(*nv().fp8_quantize_activation(p), False), _values(*down, True), None, None, r2)
+    # the same norm in front of 4-bit projections
+    codes, scales, gsf = nv().quantize_layernorm(x, lw, lb)
+    packed = nv().quantize_weight((0.05 * torch.randn(96, k, device=DEV)).to(BF))
+    got = nv().nvfp4_gemm(codes, scales, packed[0], packed[1], gsf, packed[2])
+    assert torch.equal(got, nv().nvfp4_linear(nv().layernorm(x, lw, lb), *packed, None, 96))
 
 
 @pytest.mark.parametrize("m,k,n", [(1, 25600, 400), (3, 1040, 96), (16, 2064, 333), (300, 1280, 520)])
