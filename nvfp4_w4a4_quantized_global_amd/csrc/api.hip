@@ -1196,7 +1196,7 @@ int nvfp4_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t m, int
 
 size_t nvfp4_fp8_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
   if (m <= 0 || k <= 0 || n <= 0) return 0;
-  if (nvfp4::linear_fp8_fused_supported(m, k, n)) return 0;
+  if (nvfp4::linear_fp8_fused_supported(m, k)) return 0;
   return align_up((size_t)m * (size_t)k) + fp8_scale_bytes(m, k) + nvfp4_fp8_gemm_workspace_bytes(m, k, n);
 }
 
@@ -1220,7 +1220,7 @@ int nvfp4_fp8_linear(const void* x, const void* up, int64_t m, int64_t k, const 
   const uint16_t* b = static_cast<const uint16_t*>(bias);
   uint16_t* o = static_cast<uint16_t*>(out);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (nvfp4::linear_fp8_fused_supported(m, k, n)) {
+  if (nvfp4::linear_fp8_fused_supported(m, k)) {
     Range stage("nvfp4.quantize+gemm");
     return hip_status(nvfp4::launch_linear_fp8_fused(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up),
                                                      m, k, w_codes, w_scales, n, b, ep, o, nvfp4::compute_units(), s),

@@ -655,12 +655,12 @@ Plan tile_plan(Kind kind, int64_t m, int64_t k, int64_t n, int64_t cus) {
 // round of it (64 x 25600 -> 5120 67 us, tiles 35; 64 x 5120 -> 25600 75 and 39; 48 x 1024 -> 4096
 // 6.5 and 10.4).
 Plan plan_of(int64_t m, int64_t k, int64_t n, int cus) {
-  const bool streams = m <= 64 && m * k < (int64_t)kOutside;
-  if (m <= 32 && streams) return Plan{};
+  static_assert(64 * kFp8MaxK < (int64_t)kOutside, "64 rows fit 31-bit offsets");
+  if (m <= 32) return Plan{};
   const Plan l = tile_plan<Large>(kLargeTiles, m, k, n, cus), s = tile_plan<Small>(kSmallTiles, m, k, n, cus);
   const Plan& best = l.cost <= s.cost ? l : s;
   const double rounds = std::max(1.0, (double)n / (32.0 * cus));   // two tiles of 16 weight rows a workgroup
-  if (streams && 4.5 + 0.32 * rounds * (double)((k + kFp8Block - 1) / kFp8Block) <= best.cost) return Plan{};
+  if (m <= 64 && 4.5 + 0.32 * rounds * (double)((k + kFp8Block - 1) / kFp8Block) <= best.cost) return Plan{};
   return best;
 }
 
@@ -760,8 +760,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
   return launch_plan({a_codes, a_scales, m, k, b_codes, b_scales, n, bias, ep, out, static_cast<float*>(workspace), cus, s}, p);
 }
 
-bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n) {
-  (void)n;
+bool linear_fp8_fused_supported(int64_t m, int64_t k) {
   return m <= kFusedRows && (k + kFp8Block - 1) / kFp8Block * m * (kFp8Block + 4) <= kFusedLds;
 }
 

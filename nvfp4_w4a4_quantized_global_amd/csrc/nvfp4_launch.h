@@ -228,7 +228,7 @@ hipError_t launch_gemm_fp8(const uint8_t* a_codes, const float* a_scales, int64_
                            void* workspace, size_t workspace_bytes, int cus, hipStream_t s);
 // The same for one or a few bf16 rows x (or the SwiGLU product of x and up), which each workgroup
 // quantizes for itself: one launch.
-bool linear_fp8_fused_supported(int64_t m, int64_t k, int64_t n);
+bool linear_fp8_fused_supported(int64_t m, int64_t k);
 hipError_t launch_linear_fp8_fused(const uint16_t* x, const uint16_t* up, int64_t m, int64_t k, const uint8_t* b_codes,
                                    const float* b_scales, int64_t n, const uint16_t* bias, const Epilogue& ep,
                                    uint16_t* out, int cus, hipStream_t s);

@@ -135,8 +135,9 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
              activation: str | None = None, residual: torch.Tensor | None = None,
              preact: torch.Tensor | None = None) -> torch.Tensor:
     """The product of an activation's codes [M, K] and a weight's [N, K]: bf16(act(z) + residual)
-    from z = product + bias, in fp32 with that one rounding; [M, N].  ``out``, ``activation``,
-    ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
+    from z = product + bias, in fp32 with that one rounding; [M, N].  (The matrix cores add eight
+    products at a time, cut below 2^-13 of the largest: about 1e-4 of an output.)  ``out``,
+    ``activation``, ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
     fp8_gemm_workspace_bytes is allocated here if not given."""
     _require_cuda("x_codes", x_codes, torch.uint8, 2)
     m, k = x_codes.shape
@@ -286,7 +287,11 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
     is all that is kept of it: ``checkpoint`` shares one (of :func:`layernorm_train`,
     :func:`rmsnorm_train` or :func:`checkpoint_pack`), None packs it here.  ``activation`` and
     ``residual`` (bf16, gets its gradient too) as for :func:`nvfp4_linear_train`, the activation's
-    gradient at z in 8 bits."""
+    gradient at z in 8 bits.
+
+    A backward pass that fills ``.grad`` is captured into a graph only while no eager graph of the
+    same leaves is alive: autograd would add on that one's stream, which a capture must not wait for.
+    ``torch.autograd.grad`` has no such limit."""
     x = x.to(torch.bfloat16)
     if x.dim() < 1 or not x.is_contiguous():
         x = x.contiguous()
@@ -310,15 +315,17 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
 
 class FP8Linear:
     """An inference linear over a weight in 8-bit blocks, beside :class:`NVFP4Linear`: for the layers
-    that keep more than 4 bits.  ``codes`` uint8 [out, in] and ``scales`` fp32
-    [ceil(out/128), ceil(in/128)] are E4M3 codes and the factors they are multiplied by."""
+    that keep more than 4 bits.  ``codes`` uint8 (or float8_e4m3fn) [out, in] and ``scales``
+    fp32 [ceil(out/128), ceil(in/128)] are E4M3 codes and the factors they are multiplied by."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None):
         if codes.dim() != 2 or codes.shape[1] % 16:
             raise ValueError(f"codes must be [out_features, in_features], in_features a multiple of 16, got "
                              f"{list(codes.shape)}")
-        if codes.dtype != torch.uint8:
+        if codes.dtype == torch.float8_e4m3fn:
             codes = codes.view(torch.uint8)
+        elif codes.dtype != torch.uint8:
+            raise ValueError(f"codes must be uint8 or float8_e4m3fn, got {codes.dtype}")
         self.codes, self.scales, self.bias = codes, scales, bias
         self.out_features, self.in_features = codes.shape
         if tuple(scales.shape) != (_blocks(self.out_features), _blocks(self.in_features)):

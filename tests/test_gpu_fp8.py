@@ -285,6 +285,19 @@ def test_untouched_around_the_output():
         assert torch.equal(nv().fp8_linear(x, wc, ws, b, out=odd), nv().fp8_linear(x, wc, ws, b))
 
 
+@pytest.mark.parametrize("m,k,n", [(1, 272, 77), (20, 272, 77), (48, 1024, 528), (300, 1040, 528), (4096, 272, 2048)])
+@pytest.mark.parametrize("act", [None, "gelu_tanh"])
+def test_residual_in_place(m, k, n, act):
+    # a residual stream updated where it lies, over every kind of kernel
+    x, (wc, ws), b, res = _case(m, k, n)
+    want = nv().fp8_linear(x, wc, ws, b, residual=res, activation=act)
+    pre, want_pre = torch.empty_like(res), torch.empty_like(res)
+    assert torch.equal(nv().fp8_linear(x, wc, ws, b, residual=res, activation=act, preact=want_pre), want)
+    stream = res.clone()
+    got = nv().fp8_linear(x, wc, ws, b, residual=stream, out=stream, activation=act, preact=pre)
+    assert got.data_ptr() == stream.data_ptr() and torch.equal(stream, want) and torch.equal(pre, want_pre)
+
+
 def test_long_offsets():
     # outputs and codes past 2^31
     m, k, n = 70000, 32, 32768
@@ -348,7 +361,8 @@ def test_refusals():
                 lambda: nv().fp8_linear_train(x, torch.ones(20, 144, device=DEV)),
                 lambda: nv().fp8_linear_train(x, torch.ones(32, 128, device=DEV)),
                 lambda: nv().fp8_linear_train(x, torch.ones(32, 144, device=DEV), checkpoint=nv().checkpoint_pack(x[:2])),
-                lambda: nv().FP8Linear(wc, ws.t().contiguous())):
+                lambda: nv().FP8Linear(wc, ws.t().contiguous()),
+                lambda: nv().FP8Linear(wc.view(torch.float8_e4m3fnuz), ws), lambda: nv().FP8Linear(x[:, :80], ws)):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(TypeError):
@@ -444,6 +458,29 @@ def test_shared_checkpoint_and_partial_gradients():
     with pytest.raises(RuntimeError):
         g, = torch.autograd.grad(nv().fp8_linear_train(x3, w3).float().square().sum(), x3, create_graph=True)
         g.sum().backward()
+
+
+def test_training_of_an_empty_batch_and_expanded_gradients():
+    w, b = (torch.randn(48, 272, device=DEV) * 0.05).requires_grad_(), torch.zeros(48, device=DEV, requires_grad=True)
+    lw, lb = torch.ones(272, device=DEV, requires_grad=True), torch.zeros(272, device=DEV, requires_grad=True)
+    x = torch.empty(0, 272, device=DEV, dtype=BF, requires_grad=True)
+    y, ck = nv().layernorm_train(x, lw, lb, checkpoint=True)
+    nv().fp8_linear_train(y, w, b, checkpoint=ck, activation="gelu").sum().backward()
+    assert x.grad.shape == (0, 272)
+    for p in (w, b, lw, lb):
+        assert p.grad.shape == p.shape and not p.grad.any()
+        p.grad = None
+    # sum's gradient is one value seen everywhere, through strides of zero
+    x = torch.randn(2, 3, 272, device=DEV).to(BF).requires_grad_()
+    leaves = (x, w, b, lw, lb)
+
+    def grads(gy):
+        y, ck = nv().layernorm_train(x, lw, lb, checkpoint=True)
+        return torch.autograd.grad(nv().fp8_linear_train(y, w, b, checkpoint=ck), leaves, gy)
+
+    one = torch.ones(1, device=DEV, dtype=BF).expand(2, 3, 48)
+    for got, want in zip(grads(one), grads(one.contiguous())):
+        assert torch.equal(got, want)
 
 
 # ---- streams and graphs ----

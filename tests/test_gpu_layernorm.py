@@ -303,3 +303,24 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(got, want)), i
+
+
+@pytest.mark.parametrize("m,k", [(5, 64), (9, 1040), (600, 1040), (7, 5120), (1100, 5120), (2, 16384)])
+def test_residual_sum_in_place(m, k):
+    # the C calls may write r over the residual, or over x of its type: the pivot is read before
+    import nvfp4_w4a4_quantized_global_amd._lib as L
+    x, res, w, b = _dev(*_inputs(m, k, BF, BF, F))
+    y, r = nv().layernorm(x, w, b, 1e-6, res)
+    codes, scales, _ = nv().fp8_quantize_layernorm(x, w, b, 1e-6, res)
+    s = torch.cuda.current_stream().cuda_stream
+    for over in (0, 1):
+        a = [x.clone(), res.clone()]
+        got = torch.empty_like(y)
+        L.check(L.lib().nvfp4_layernorm(a[0].data_ptr(), 0, a[1].data_ptr(), 0, w.data_ptr(), b.data_ptr(), 1, m, k, 1e-6,
+                                        a[over].data_ptr(), got.data_ptr(), None, None, s))
+        assert torch.equal(got, y) and torch.equal(a[over], r) and torch.equal(a[1 - over], (x, res)[1 - over])
+        a = [x.clone(), res.clone()]
+        c, sc = torch.empty_like(codes), torch.empty_like(scales)
+        L.check(L.lib().nvfp4_fp8_quantize_layernorm(a[0].data_ptr(), 0, a[1].data_ptr(), 0, w.data_ptr(), b.data_ptr(), 1, m,
+                                                     k, 1e-6, a[over].data_ptr(), c.data_ptr(), sc.data_ptr(), s))
+        assert torch.equal(c, codes) and torch.equal(sc, scales) and torch.equal(a[over], r)
