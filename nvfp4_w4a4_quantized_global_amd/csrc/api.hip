@@ -349,6 +349,10 @@ int check_fp8_shape(const char* fn, int64_t rows, int64_t k) {
     return fail(NVFP4_ERR_SHAPE, "%s: K must be at most %lld, got %lld", fn, (long long)NVFP4_FP8_MAX_DIM, (long long)k);
   return NVFP4_OK;
 }
+// Whether workspace sizes are defined for a product of these dimensions.
+bool fp8_dims(int64_t m, int64_t k, int64_t n) {
+  return m > 0 && m < kMaxDim && k > 0 && k <= NVFP4_FP8_MAX_DIM && n > 0 && n <= NVFP4_FP8_MAX_DIM;
+}
 int check_fp8_out_features(const char* fn, int64_t n) {
   if (n <= 0 || n > NVFP4_FP8_MAX_DIM)
     return fail(NVFP4_ERR_SHAPE, "%s: out_features must be in [1, %lld], got %lld", fn, (long long)NVFP4_FP8_MAX_DIM,
@@ -979,7 +983,7 @@ int nvfp4_layernorm(const void* x, int x_dtype, const void* residual, int residu
 }
 
 size_t nvfp4_quantize_layernorm_workspace_bytes(int64_t rows) {
-  if (rows <= 1) return 0;   // one row is one workgroup's: nothing to hand over
+  if (rows <= 1 || rows >= kMaxDim) return 0;   // one row is one workgroup's: nothing to hand over
   return align_up(sizeof(float) * nvfp4::kNormPartials) + align_up(sizeof(float) * (size_t)rows) +
          align_up(sizeof(double) * (size_t)rows);
 }
@@ -1017,7 +1021,7 @@ int nvfp4_quantize_layernorm(const void* x, int x_dtype, const void* residual, i
 }
 
 size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t k) {
-  if (rows < 0 || k <= 0 || k > nvfp4::kNormMaxK || k % NVFP4_BLOCK_SIZE) return 0;
+  if (rows < 0 || rows >= kMaxDim || k <= 0 || k > nvfp4::kNormMaxK || k % NVFP4_BLOCK_SIZE) return 0;
   return align_up(sizeof(float) * nvfp4::layernorm_backward_partial_floats(rows, k));
 }
 
@@ -1062,7 +1066,7 @@ int nvfp4_layernorm_backward(const void* grad_y, const void* r, int r_dtype, con
 }
 
 size_t nvfp4_fp8_quantize_workspace_bytes(int64_t rows, int64_t k) {
-  if (rows < 0 || k <= 0) return 0;
+  if (rows < 0 || rows >= kMaxDim || k <= 0 || k > NVFP4_FP8_MAX_DIM) return 0;
   return align_up(sizeof(float) * nvfp4::fp8_column_sum_floats(rows, k));
 }
 
@@ -1167,7 +1171,7 @@ int nvfp4_fp8_quantize_layernorm(const void* x, int x_dtype, const void* residua
 }
 
 size_t nvfp4_fp8_gemm_workspace_bytes(int64_t m, int64_t k, int64_t n) {
-  if (m <= 0 || k <= 0 || n <= 0) return 0;
+  if (!fp8_dims(m, k, n)) return 0;
   return align_up(nvfp4::gemm_fp8_workspace_bytes(m, k, n, nvfp4::compute_units()));
 }
 
@@ -1195,7 +1199,7 @@ int nvfp4_fp8_gemm(const uint8_t* x_codes, const float* x_scales, int64_t m, int
 }
 
 size_t nvfp4_fp8_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
-  if (m <= 0 || k <= 0 || n <= 0) return 0;
+  if (!fp8_dims(m, k, n)) return 0;
   if (nvfp4::linear_fp8_fused_supported(m, k)) return 0;
   return align_up((size_t)m * (size_t)k) + fp8_scale_bytes(m, k) + nvfp4_fp8_gemm_workspace_bytes(m, k, n);
 }

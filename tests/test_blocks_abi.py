@@ -157,3 +157,16 @@ def test_fp8_sizes():
     # partials never exceed one round of tiles: 256 of 256 x 256, or 512 of 128 x 128
     for m, k, n in ((33, 1 << 20, 16), (4096, 25600, 5120), (100, 8192, 8192), (1000, 16, 1000)):
         assert L.nvfp4_fp8_gemm_workspace_bytes(m, k, n) <= 256 * 256 * 256 * 4
+
+
+def test_sizes_outside_the_calls_limits():
+    L = lib()
+    most, wide = (1 << 31) - 1, 1 << 22
+    assert L.nvfp4_fp8_linear_workspace_bytes(most, wide, wide) > most * wide
+    assert L.nvfp4_layernorm_backward_workspace_bytes(most, 16384) > 0 < L.nvfp4_quantize_layernorm_workspace_bytes(most)
+    assert L.nvfp4_fp8_quantize_workspace_bytes(most, wide) > 0
+    for big in (1 << 31, (1 << 63) - 1, -1):
+        assert L.nvfp4_layernorm_backward_workspace_bytes(big, 5120) == 0 == L.nvfp4_quantize_layernorm_workspace_bytes(big)
+        assert L.nvfp4_fp8_quantize_workspace_bytes(big, 5120) == 0 == L.nvfp4_fp8_quantize_workspace_bytes(16, big)
+        for f in (L.nvfp4_fp8_gemm_workspace_bytes, L.nvfp4_fp8_linear_workspace_bytes):
+            assert f(big, 512, 512) == 0 == f(300, big, 512) == f(300, 512, big)

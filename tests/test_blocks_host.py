@@ -150,3 +150,15 @@ def test_launches_on_the_tensors_device(name, monkeypatch):
     launches = [(n, d) for n, d in seen if not n.endswith("_bytes") or "workspace" in n]
     assert launches and all(d == 1 for _, d in launches), launches
     assert current == [0]
+
+
+def test_layer_takes_its_codes_types_only():
+    scales = torch.ones(1, 2)
+    for dt in (torch.uint8, torch.float8_e4m3fn):
+        layer = fp8.FP8Linear(torch.zeros(N, K, dtype=U8).view(dt), scales)
+        assert layer.codes.dtype == U8 and (layer.out_features, layer.in_features) == (N, K)
+    for bad in (torch.zeros(N, K, dtype=U8).view(torch.float8_e4m3fnuz), torch.zeros(N, K, dtype=U8).view(torch.float8_e5m2),
+                torch.zeros(N, K, dtype=torch.int8), torch.zeros(N, K // 2, dtype=BF), torch.zeros(N, 20, dtype=U8),
+                torch.zeros(N * K, dtype=U8)):
+        with pytest.raises(ValueError):
+            fp8.FP8Linear(bad, scales)
