@@ -509,6 +509,11 @@ int nvfp4_fp8_quantize_activation(const void* x_dev, const void* up_dev, int64_t
                                   float* scales_dev, float* column_sum_dev, void* workspace_dev,
                                   size_t workspace_bytes, void* stream);
 
+/* nvfp4_fp8_quantize_checkpoint: nvfp4_fp8_quantize_activation and nvfp4_checkpoint_pack (no rotation)
+ * of one read of x_dev, the same bits (a training step's two forms of a linear's input). */
+int nvfp4_fp8_quantize_checkpoint(const void* x_dev, int64_t rows, int64_t k, uint8_t* codes_dev, float* scales_dev,
+                                  uint8_t* ck_codes_dev, uint8_t* ck_scales_dev, void* stream);
+
 /* nvfp4_fp8_quantize_weight: w_dev [n][k] of w_dtype.  codes_t_dev / scales_t_dev: both NULL, or the
  * transposed codes [k][n] and scales [ceil(k / 128)][ceil(n / 128)], the same values (a weight for
  * the input's gradient; n a multiple of 16 then). */

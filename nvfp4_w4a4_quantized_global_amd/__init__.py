@@ -11,7 +11,8 @@ from .checkpoint import (  # noqa: F401
 )
 from .fp8 import (  # noqa: F401
     FP8_BLOCK, FP8_MAX_DIM, FP8Linear, fp8_dequantize, fp8_gemm, fp8_gemm_workspace_bytes, fp8_linear, fp8_linear_swiglu,
-    fp8_linear_train, fp8_linear_workspace_bytes, fp8_quantize_activation, fp8_quantize_swiglu, fp8_quantize_weight,
+    fp8_linear_train, fp8_linear_workspace_bytes, fp8_quantize_activation, fp8_quantize_checkpoint, fp8_quantize_swiglu,
+    fp8_quantize_weight,
 )
 from .layer_norm import (  # noqa: F401
     fp8_quantize_layernorm, fp8_quantize_rmsnorm, layernorm, layernorm_backward, layernorm_checkpoint, layernorm_train,

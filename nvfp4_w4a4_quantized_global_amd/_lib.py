@@ -81,6 +81,7 @@ SIGNATURES = {
     "nvfp4_layernorm_backward": (_int, [_vp, _vp, _int, _vp, _int, _vp, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "nvfp4_fp8_quantize_workspace_bytes": (_sz, [_i64, _i64]),
     "nvfp4_fp8_quantize_activation": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "nvfp4_fp8_quantize_checkpoint": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "nvfp4_fp8_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "nvfp4_fp8_dequantize": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _int, _vp]),
     "nvfp4_fp8_quantize_rmsnorm": (_int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp]),

@@ -1089,8 +1089,24 @@ int nvfp4_fp8_quantize_activation(const void* x, const void* up, int64_t rows, i
                                column_sum != nullptr ? nvfp4_fp8_quantize_workspace_bytes(rows, k) : 0))
     return rc;
   return hip_status(nvfp4::launch_fp8_quantize(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(up), rows,
-                                               k, codes, scales, column_sum, static_cast<float*>(workspace),
-                                               static_cast<hipStream_t>(stream)),
+                                               k, codes, scales, column_sum, static_cast<float*>(workspace), nullptr,
+                                               nullptr, static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int nvfp4_fp8_quantize_checkpoint(const void* x, int64_t rows, int64_t k, uint8_t* codes, float* scales,
+                                  uint8_t* ck_codes, uint8_t* ck_scales, void* stream) {
+  const char* fn = "nvfp4_fp8_quantize_checkpoint";
+  Range call(fn);
+  g_err[0] = 0;
+  if (int rc = check_fp8_shape(fn, rows, k)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!x || !ck_codes || !ck_scales) return fail(NVFP4_ERR_ARG, "%s: NULL tensor argument", fn);
+  if (int rc = check_aligned(fn, "x", x)) return rc;
+  if (int rc = check_fp8_operand(fn, "codes", codes, "scales", scales)) return rc;
+  if (int rc = check_aligned(fn, "ck_codes", ck_codes)) return rc;
+  return hip_status(nvfp4::launch_fp8_quantize(static_cast<const uint16_t*>(x), nullptr, rows, k, codes, scales, nullptr,
+                                               nullptr, ck_codes, ck_scales, static_cast<hipStream_t>(stream)),
                     fn);
 }
 
@@ -1237,7 +1253,7 @@ int nvfp4_fp8_linear(const void* x, const void* up, int64_t m, int64_t k, const 
     Range stage("nvfp4.quantize");
     if (int rc = hip_status(nvfp4::launch_fp8_quantize(static_cast<const uint16_t*>(x),
                                                        static_cast<const uint16_t*>(up), m, k, codes, scales, nullptr,
-                                                       nullptr, s),
+                                                       nullptr, nullptr, nullptr, s),
                             fn))
       return rc;
   }

@@ -25,13 +25,15 @@ constexpr int kQBlocks = 4, kQRows = 8;   // blocks of a row, and rows, a workgr
 // a workgroup takes four neighbouring blocks (1 KB of bf16) of eight rows, so that loads come in
 // long runs and the scales of a block in runs of eight rows.  kSwiglu: the input is the SwiGLU
 // product of x (gate) and up.  kSum: the workgroup walks down the rows and writes one partial row
-// of column sums (partials [gridDim.y][k]).
-template <bool kSwiglu, bool kSum>
+// of column sums (partials [gridDim.y][k]).  kCheckpoint: x's 8-bit checkpoint from the same read.
+template <bool kSwiglu, bool kSum, bool kCheckpoint>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const uint16_t* __restrict__ x,
                                                                 const uint16_t* __restrict__ up, int64_t rows,
                                                                 int64_t k, uint8_t* __restrict__ codes,
                                                                 float* __restrict__ scales,
-                                                                float* __restrict__ partials) {
+                                                                float* __restrict__ partials,
+                                                                uint8_t* __restrict__ ck_codes,
+                                                                uint8_t* __restrict__ ck_scales) {
   __shared__ float sums[kSum ? kThreads * 16 : 1];
   const int t = threadIdx.x;
   const int unit = t >> 3, j = t & 7;
@@ -67,6 +69,14 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const uint16_t* 
     if (valid) {
       *reinterpret_cast<uint4*>(codes + row * k + col) = c;
       if (j == 0) scales[blk * rows + row] = scale;
+    }
+    if constexpr (kCheckpoint) {
+      uint32_t byte;
+      const uint4 q = ck_pack16(v, byte);
+      if (valid) {
+        *reinterpret_cast<uint4*>(ck_codes + row * k + col) = q;
+        if ((j & 1) == 0) ck_scales[row * ((k + kCkBlock - 1) / kCkBlock) + col / kCkBlock] = (uint8_t)byte;
+      }
     }
   }
   if constexpr (kSum) {
@@ -242,25 +252,24 @@ int64_t sum_walkers(int64_t rows, int64_t k) {
 size_t fp8_column_sum_floats(int64_t rows, int64_t k) { return (size_t)sum_walkers(rows, k) * (size_t)k; }
 
 hipError_t launch_fp8_quantize(const uint16_t* x, const uint16_t* up, int64_t rows, int64_t k, uint8_t* codes,
-                               float* scales, float* column_sum, float* partials, hipStream_t s) {
+                               float* scales, float* column_sum, float* partials, uint8_t* ck_codes, uint8_t* ck_scales,
+                               hipStream_t s) {
   const int64_t groups = column_groups(k);
   if (column_sum != nullptr) {
     const int64_t walkers = sum_walkers(rows, k);
     if (walkers > 0)
-      hipLaunchKernelGGL((fp8_quantize_kernel<false, true>), dim3((uint32_t)groups, (uint32_t)walkers), dim3(kThreads), 0,
-                         s, x, up, rows, k, codes, scales, partials);
+      hipLaunchKernelGGL((fp8_quantize_kernel<false, true, false>), dim3((uint32_t)groups, (uint32_t)walkers),
+                         dim3(kThreads), 0, s, x, up, rows, k, codes, scales, partials, nullptr, nullptr);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     hipLaunchKernelGGL(fp8_column_sum_kernel, dim3((uint32_t)((k + 31) / 32)), dim3(1024), 0, s, partials, (int)walkers, k,
                        column_sum);
     return hipGetLastError();
   }
+  const auto fn = up != nullptr ? fp8_quantize_kernel<true, false, false>
+                  : ck_codes != nullptr ? fp8_quantize_kernel<false, false, true>
+                                        : fp8_quantize_kernel<false, false, false>;
   const dim3 grid((uint32_t)groups, (uint32_t)std::min<int64_t>((rows + kQRows - 1) / kQRows, 65535));
-  if (up != nullptr)
-    hipLaunchKernelGGL((fp8_quantize_kernel<true, false>), grid, dim3(kThreads), 0, s, x, up, rows, k, codes, scales,
-                       partials);
-  else
-    hipLaunchKernelGGL((fp8_quantize_kernel<false, false>), grid, dim3(kThreads), 0, s, x, up, rows, k, codes, scales,
-                       partials);
+  hipLaunchKernelGGL(fn, grid, dim3(kThreads), 0, s, x, up, rows, k, codes, scales, partials, ck_codes, ck_scales);
   return hipGetLastError();
 }
 

@@ -207,11 +207,13 @@ hipError_t launch_activation_backward(const uint16_t* gy, const void* z, const u
 
 // 8-bit block codes (fp8.hip): activations [rows][k] with scales [ceil(k / 128)][rows], of x or
 // (up not NULL) of the SwiGLU product of x and up; column_sum [k], when not NULL, receives the
-// sums of x over its rows (not with up; partials: fp8_column_sum_floats).  Weights [n][k] with
+// sums of x over its rows (not with up; partials: fp8_column_sum_floats); ck_codes and ck_scales, when
+// not NULL, its 8-bit checkpoint (with neither).  Weights [n][k] with
 // scales [ceil(n / 128)][ceil(k / 128)] and, when codes_t is not NULL, both transposed.
 size_t fp8_column_sum_floats(int64_t rows, int64_t k);
 hipError_t launch_fp8_quantize(const uint16_t* x, const uint16_t* up, int64_t rows, int64_t k, uint8_t* codes,
-                               float* scales, float* column_sum, float* partials, hipStream_t s);
+                               float* scales, float* column_sum, float* partials, uint8_t* ck_codes, uint8_t* ck_scales,
+                               hipStream_t s);
 hipError_t launch_fp8_quantize_weight(const void* w, bool w_f32, int64_t n, int64_t k, uint8_t* codes, float* scales,
                                       uint8_t* codes_t, float* scales_t, hipStream_t s);
 hipError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t k, bool weight,

@@ -81,6 +81,17 @@ def fp8_quantize_activation(x: torch.Tensor, column_sum: bool = False):
 
 
 @_on_device
+def fp8_quantize_checkpoint(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, ck.Checkpoint]:
+    """(codes, scales) of fp8_quantize_activation and checkpoint_pack(x), from one read of x."""
+    x2, rows, k = _rows("x", x)
+    codes, scales = _empty_codes(rows, k, x2.device)
+    held = ck._empty_checkpoint(x2)
+    check(lib().nvfp4_fp8_quantize_checkpoint(_ptr(x2), rows, k, _ptr(codes), _ptr(scales), _ptr(held.codes),
+                                              _ptr(held.scales), _stream(x2.device)))
+    return codes, scales, held
+
+
+@_on_device
 def fp8_quantize_swiglu(gate: torch.Tensor, up: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """fp8_quantize_activation(swiglu(gate, up)) without writing the product."""
     g2, u2 = _gate_up(gate, up)
@@ -239,10 +250,17 @@ class _FP8Fn(torch.autograd.Function):
         z = z_scales = None
         if activation is not None:
             z = torch.empty(x.numel() // x.shape[-1], n, dtype=torch.bfloat16, device=x.device)
-        y = fp8_linear(x, codes, scales, b, activation=activation, preact=z,
-                       residual=None if residual is None else residual.detach())
+        r = None if residual is None else residual.detach()
+        if x_codes is None and ctx.needs_input_grad[1]:
+            q, s, held = fp8_quantize_checkpoint(x)
+            x_codes, x_scales = held.codes, held.scales
+            y = fp8_gemm(q, s, codes, scales, b, activation=activation, preact=z, residual=r).reshape(*x.shape[:-1], n)
+        else:
+            y = fp8_linear(x, codes, scales, b, activation=activation, preact=z, residual=r)
         if z is not None and n % 16 == 0:
             z, z_scales, _ = ck.checkpoint_pack(z)
+        if not ctx.needs_input_grad[1]:
+            x_codes = x_scales = None
         ctx.save_for_backward(x_codes, x_scales, codes_t, scales_t, z, z_scales)
         ctx.activation = activation
         ctx.shapes = (x.shape, x.dtype, weight.dtype, None if bias is None else bias.dtype,
@@ -285,7 +303,7 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
     All three products run on the matrix cores from 8-bit operands: the input's gradient from the
     quantized gradient of the output, the weight's (at the values of) the 8-bit checkpoint of x, which
     is all that is kept of it: ``checkpoint`` shares one (of :func:`layernorm_train`,
-    :func:`rmsnorm_train` or :func:`checkpoint_pack`), None packs it here.  ``activation`` and
+    :func:`rmsnorm_train` or :func:`checkpoint_pack`), None packs it here, with x's codes.  ``activation`` and
     ``residual`` (bf16, gets its gradient too) as for :func:`nvfp4_linear_train`, the activation's
     gradient at z in 8 bits.
 
@@ -301,16 +319,16 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
     if weight.shape[0] % 16:
         raise ValueError(f"fp8_linear_train needs out_features divisible by 16, got {weight.shape[0]}")
     _require_device(x.device, weight=weight, bias=bias, residual=residual)
-    held = ck.checkpoint_pack(x.detach()) if checkpoint is None else checkpoint
-    if not isinstance(held, ck.Checkpoint):
+    if checkpoint is None:
+        return _FP8Fn.apply(x, weight, bias, None, None, activation, residual)
+    if not isinstance(checkpoint, ck.Checkpoint):
         raise TypeError("checkpoint must be None or a Checkpoint")
-    codes, scales, rows, k = ck._saved("checkpoint", held)
+    codes, scales, rows, k = ck._saved("checkpoint", checkpoint)
     _require_device(x.device, checkpoint=codes)
-    if held.rotation_group or k != x.shape[-1] or rows * k != x.numel():
-        raise ValueError(f"checkpoint holds {list(held.codes.shape)} under rotation group {held.rotation_group}; the "
-                         f"linear's input is {list(x.shape)} without a rotation")
-    return _FP8Fn.apply(x, weight, bias, codes.reshape(rows, k), scales.reshape(rows, scales.shape[-1]), activation,
-                        residual)
+    if checkpoint.rotation_group or k != x.shape[-1] or rows * k != x.numel():
+        raise ValueError(f"checkpoint holds {list(checkpoint.codes.shape)} under rotation group "
+                         f"{checkpoint.rotation_group}; the linear's input is {list(x.shape)} without a rotation")
+    return _FP8Fn.apply(x, weight, bias, codes, scales, activation, residual)
 
 
 class FP8Linear:

@@ -80,6 +80,15 @@ def test_fp8_quantize_refusals():
     assert a(t=P) == NVFP4_ERR_WORKSPACE and a(t=P, ws=P, n=need - 1) == NVFP4_ERR_WORKSPACE
     assert a(rows=0, x=None, c=None, s=None) == 0
 
+    def q(x=P, rows=4, k=64, c=P, s=P, kc=P, ks=P):
+        return L.nvfp4_fp8_quantize_checkpoint(x, rows, k, c, s, kc, ks, None)
+
+    for bad in ({"k": 24}, {"k": MAX + 16}, {"rows": -1}):
+        assert q(**bad) == NVFP4_ERR_SHAPE, bad
+    for bad in ({"x": None}, {"c": None}, {"s": None}, {"kc": None}, {"ks": None}, {"x": ODD}, {"c": ODD}, {"s": ODD1}, {"kc": ODD}):
+        assert q(**bad) == NVFP4_ERR_ARG, bad
+    assert q(rows=0, x=None, c=None, s=None, kc=None, ks=None) == 0
+
     def w(x=P, d=0, n=32, k=64, c=P, s=P, ct=None, st=None):
         return L.nvfp4_fp8_quantize_weight(x, d, n, k, c, s, ct, st, None)
 

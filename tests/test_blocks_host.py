@@ -37,6 +37,7 @@ def _calls():
         "fp8_gemm": (["xs", "codes", "scales", "bias", "residual", "out", "preact", "ws"],
                      lambda t: fp8.fp8_gemm(t["xc"], t["xs"], t["codes"], t["scales"], t["bias"], **e(t))),
         "fp8_quantize_swiglu": (["up"], lambda t: fp8.fp8_quantize_swiglu(t["x"], t["up"])),
+        "fp8_quantize_checkpoint": ([], lambda t: fp8.fp8_quantize_checkpoint(t["x"])),
         "fp8_dequantize": (["scales"], lambda t: fp8.fp8_dequantize(t["codes"], t["scales"])),
         "layernorm": (["lw", "lb", "h"], lambda t: layer_norm.layernorm(t["x"], t["lw"], t["lb"], 1e-6, t["h"])),
         "layernorm_checkpoint": (["lw", "lb", "h"], lambda t: layer_norm.layernorm_checkpoint(t["x"], t["lw"], t["lb"], 1e-6, t["h"])),

@@ -105,6 +105,21 @@ def test_activation_codes(m, k):
         assert v.dtype == dt and torch.equal(v.cpu(), want)
 
 
+@pytest.mark.parametrize("m,k", CODE_SHAPES)
+def test_codes_with_the_checkpoint(m, k):
+    x = _rows(m, k, 5).to(BF).to(DEV)
+    x[-1, ::7] = float("nan")
+    x[-1, 3] = float("inf")
+    codes, scales, ck = nv().fp8_quantize_checkpoint(x)
+    want = nv().checkpoint_pack(x)
+    assert torch.equal(ck.codes, want.codes) and torch.equal(ck.scales, want.scales) and ck.rotation_group == 0
+    for got, ref in zip((codes, scales), nv().fp8_quantize_activation(x)):
+        assert torch.equal(got, ref)
+    assert nv().fp8_quantize_checkpoint(x.view(m, 1, k))[2].scales.shape == (m, 1, (k + 31) // 32)
+    codes, scales, ck = nv().fp8_quantize_checkpoint(x[:0])
+    assert codes.shape == (0, k) and ck.codes.shape == (0, k) and scales.shape[1] == 0
+
+
 @pytest.mark.parametrize("m,k", [(1, 16), (5, 144), (67, 1040), (3, 25600)])
 def test_swiglu_codes(m, k):
     g, u = (workloads.draw("normal", (m, k), 210 + i, m).to(DEV) for i in range(2))
