@@ -98,7 +98,8 @@ struct Geo {
   static constexpr int kCopyA = kBM / 8 / kWaves, kCopyB = kBN / 8 / kWaves;   // copy instructions of a wave
   static constexpr int kEpiRow = 16 * kTN + 4;                                  // words per staged output row
   static constexpr int kEpiWave = 32 * kEpiRow * 4;
-  static_assert(kTN == 4, "a wave's 64 columns: eight lanes a row in the epilogue, one weight scale");
+  static constexpr int kEpiLanes = 2 * kTN, kEpiRows = 64 / kEpiLanes;          // of a row, and rows, at a time
+  static_assert(kTN == 2 || kTN == 4, "whole rows of lanes in the epilogue, one weight scale a wave");
   static_assert(kTM == 4 || kTM == 8, "pairs of tiles in the epilogue; the block's last two after a whole number of pairs");
   static_assert(kWaves > kBM / 64, "a wave for the weight's scales");
   static_assert(kOffSB + 512 <= kOffA, "room for the other waves' copies of nothing");
@@ -108,7 +109,11 @@ struct Geo {
 };
 using Large = Geo<2, 4, 8, 4, 2>;   // 256 x 256, one workgroup of eight waves per compute unit
 using Small = Geo<2, 2, 4, 4, 2>;   // 128 x 128, two workgroups of four
-using Deep = Geo<2, 2, 4, 4, 4>;    // the same, one workgroup with three blocks of K in flight
+// 128 x 128, one workgroup with three blocks of K in flight.  Eight waves of 64 x 32: two on a SIMD hide
+// each other's waits, for half as many LDS reads again (777 x 1040 -> 1001 with the quantizer 21.2 us in
+// four waves of 64 x 64, 18.2 so; 512 x 5120 -> 5120 35.8 and 33.2; 4096 x 5120 -> 1024 44.3 and 43.2).
+// Where workgroups share a compute unit it gains nothing (2048 x 1024 -> 4096 21.1 and 21.7).
+using Deep = Geo<2, 4, 4, 2, 4>;
 
 // Tile index -> (tile row, tile column): bands of kGroupM tile rows, column-major inside a band,
 // so that the tiles resident on one XCD share operand panels in its L2.
@@ -310,7 +315,8 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
   // (777 x 1040 -> 1001: 21.0 -> 20.3 us, with a residual 22.9 -> 21.5; 4091 x 1024 -> 4096 with gelu
   // 38.7 -> 37.6).
   float* stg = reinterpret_cast<float*>(lds + wave * G::kEpiWave);
-  const int ecol = 8 * (lane & 7);
+  constexpr int kRows = G::kEpiRows, kPasses = 32 / kRows;
+  const int ecol = 8 * (lane % G::kEpiLanes), erow = lane / G::kEpiLanes;
   auto stage16 = [&](const float4v (&v)[kTN], int h) {
 #pragma unroll
     for (int j = 0; j < kTN; ++j)
@@ -341,8 +347,8 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     for (int i = 0; i < kTM / 2; ++i) {
       stage_rows(i);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = 8 * p + (lane >> 3);
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = kRows * p + erow;
         const float4v* f = reinterpret_cast<const float4v*>(stg + r * G::kEpiRow + ecol);
         float4v* d = reinterpret_cast<float4v*>(dst + (wm * 16 * kTM + 32 * i + r) * G::kBN + wn * 16 * kTN + ecol);
         d[0] = f[0];
@@ -359,16 +365,16 @@ __global__ void __launch_bounds__(G::kThreads, 2) gemm_fp8_kernel(
     for (int h = 0; h < 8; ++h) bv[h] = bias != nullptr && col + h < n ? bf16_to_f32(bias[col + h]) : 0.0f;
 #pragma unroll 1
     for (int i = 0; i < kTM / 2; ++i) {
-      const int64_t r0 = row0 + wm * 16 * kTM + 32 * i + (lane >> 3);
-      uint4 res[4];
+      const int64_t r0 = row0 + wm * 16 * kTM + 32 * i + erow;
+      uint4 res[kPasses];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        res[p] = whole && r0 + 8 * p < m ? residual8(ep, (r0 + 8 * p) * n + col) : make_uint4(0, 0, 0, 0);
+      for (int p = 0; p < kPasses; ++p)
+        res[p] = whole && r0 + kRows * p < m ? residual8(ep, (r0 + kRows * p) * n + col) : make_uint4(0, 0, 0, 0);
       stage_rows(i);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int64_t row = r0 + 8 * p;
-        const float* f = stg + (8 * p + (lane >> 3)) * G::kEpiRow + ecol;
+      for (int p = 0; p < kPasses; ++p) {
+        const int64_t row = r0 + kRows * p;
+        const float* f = stg + (kRows * p + erow) * G::kEpiRow + ecol;
         const float4v f0 = *reinterpret_cast<const float4v*>(f), f1 = *reinterpret_cast<const float4v*>(f + 4);
         const int64_t idx = row * n + col;
         if (row < m && whole) {
@@ -618,10 +624,10 @@ struct Plan {
 // Time in us as measured over shapes from 48 x 1024 -> 4096 to 4096 x 8192 -> 5120 (within 15 % of
 // most): a round of tiles takes its prologue and epilogue, and its blocks of K, 1.45 us of a Large
 // tile, 1.05 of two Small ones on a compute unit and 0.6 of a Deep one; a split adds a launch and
-// 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Deep tiles whole 31.0 us, in
-// two splits 27.6, in six 37.1, in Large ones split eight ways 37.7; 2048 x 1024 -> 1024 whole 11.9,
+// 0.45 us per MB of partials written and read.  (2048 x 5120 -> 1024 in Deep tiles whole 29.2 us, in
+// two splits 27.8, in six 37.1, in Large ones split eight ways 37.7; 2048 x 1024 -> 1024 whole 10.8,
 // in two splits 21.2; 4096 x 5120 -> 5120 in Large ones 107, in Small 118; 4096 x 5120 -> 1024, one
-// tile a compute unit, with one block of K in flight 40.1, with three 31.8.)
+// tile a compute unit, with one block of K in flight 40.1, with three 31.0.)
 constexpr double kLargeRound = 6.0, kSmallRound = 4.9, kLargeBlock = 1.45, kSmallBlock = 1.05, kDeepBlock = 0.6;
 // The cheapest number of splits of `units` tiles of this size, at most one round of them.
 void plan_rest(Plan& p, int64_t units, int64_t kb, int64_t cus, bool large, int sub, double before) {
