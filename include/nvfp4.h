@@ -479,8 +479,9 @@ int nvfp4_quantize_layernorm(const void* x_dev, int x_dtype, const void* residua
  *     grad_r = s (g - mean(g) - n mean(g n)) + grad_residual,
  *     grad_w = sum over rows of grad_y n,   grad_b = sum over rows of grad_y.
  * grad_w_dev, grad_b_dev: fp32 [k], both or neither (then no workspace).  The row partials are
- * added in a fixed order: results repeat bit for bit.  Other arguments and the range of rows as
- * for nvfp4_rmsnorm_backward.
+ * added in a fixed order: results repeat bit for bit.  Other arguments as for
+ * nvfp4_rmsnorm_backward.  Rows may have any magnitude whose reciprocal is a normal fp32 number, as
+ * long as grad_y * weight of every value stays below 1e36.
  */
 size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t k);
 int nvfp4_layernorm_backward(const void* grad_y_dev, const void* r_dev, int r_dtype, const void* weight_dev,

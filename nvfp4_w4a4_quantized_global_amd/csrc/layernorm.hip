@@ -340,9 +340,10 @@ __global__ void __launch_bounds__(kNormQThreads) layernorm_quantize_kernel(const
 // Gradient.  With n = (r - mu) s and g = gy w:
 //   grad_r = s (g - mean(g) - n mean(g n)) + grad_residual,
 //   grad_w = sum over rows of gy n,   grad_b = sum over rows of gy
-// (the rounding of y taken as the identity).  One reduction gives all four row sums: those of
-// the pivot's distances d = r - p in fp64, and sum(g), sum(g d) from a lane's 16 products in
-// fp32, added in fp64: mean(g n) = s (sum(g d) - (mu - p) sum(g)) / K.
+// (the rounding of y taken as the identity).  One reduction gives all four row sums, in fp64: those
+// of the pivot's distances d = r - p and of d^2, and sum(g), sum(g d) of the products g rounded to
+// fp32: mean(g n) = s (sum(g d) - (mu - p) sum(g)) / K.  g d leaves fp32's range long before the
+// gradient does: |d| may be twice the largest |r|, and meets the gradients beside small r too.
 //
 // Each workgroup walks its rows with its lanes' 16 columns of grad_w and grad_b in registers and
 // writes one partial row of both; layernorm_weight_grad_kernel adds the partials in a fixed order.
@@ -384,18 +385,15 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
       p = stream_value<kSF32, 0>(a.r, nullptr, row * k);
       gy.load(a.gy, off);
       if constexpr (kRes) gres.load(a.grad_residual, off);
-      float sg = 0.0f, sgd = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const double d = (double)rr.get(i) - (double)p;
+        const double d = (double)rr.get(i) - (double)p, g = (double)(gy.get(i) * w.get(i));
         sum[0] += d;
         sum[1] = fma(d, d, sum[1]);
-        const float g = gy.get(i) * w.get(i);
-        sg += g;
-        sgd = fmaf(g, rr.get(i) - p, sgd);
+        sum[2] += g;
+        sum[3] = fma(g, d, sum[3]);
+        by_four(i);
       }
-      sum[2] = (double)sg;
-      sum[3] = (double)sgd;
     }
     const int lanes = a.lanes < 64 ? a.lanes : 64;
 #pragma unroll
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(1024) layernorm_backward_kernel(const NormBack
     double mu;
     const float s = row_statistics(sum[0], sum[1], p, k, a.eps, mu);
     const float f1 = (float)(sum[2] * inv_k);
-    const float f2 = s * (float)((sum[3] - (mu - (double)p) * sum[2]) * inv_k);
+    const float f2 = (float)((double)s * ((sum[3] - (mu - (double)p) * sum[2]) * inv_k));
     forget(rr);
 #pragma unroll
     for (int h = 0; h < 16; h += 8) {
