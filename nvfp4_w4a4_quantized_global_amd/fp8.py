@@ -48,6 +48,15 @@ def _bias(bias: torch.Tensor | None, n: int) -> None:
             raise ValueError(f"bias must have {n} elements, got {bias.numel()}")
 
 
+def _apart(workspace: torch.Tensor, need: int, *others: torch.Tensor | None) -> None:
+    """The ``need`` bytes of a caller's workspace that a call writes (the quantized input, partial
+    sums) and reads again share no memory with its operands and outputs."""
+    p = workspace.data_ptr()
+    for t in others if need else ():
+        if t is not None and p < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < p + need:
+            raise ValueError("workspace must not overlap the call's operands or outputs")
+
+
 def fp8_gemm_workspace_bytes(m: int, k: int, n: int) -> int:
     """Workspace fp8_gemm can use to split tiles along K (current device)."""
     return int(lib().nvfp4_fp8_gemm_workspace_bytes(m, k, n))
@@ -160,13 +169,16 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
     _operands(x_codes, x_scales=x_scales, codes=codes, scales=scales, bias=bias)
     dev = x_codes.device
     act = _activation_code(activation)
-    residual = _epilogue_tensors(m, n, dev, residual, preact, out, x_codes, x_scales, codes, scales)
+    inputs = (x_codes, x_scales, codes, scales) if bias is None else (x_codes, x_scales, codes, scales, bias)
+    residual = _epilogue_tensors(m, n, dev, residual, preact, out, *inputs)
     given = out
     if out is None:
         out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
+    need = fp8_gemm_workspace_bytes(m, k, n)
     if workspace is not None:
         _given_workspace(workspace, dev)
-    need = fp8_gemm_workspace_bytes(m, k, n)
+        if workspace.numel() >= need:
+            _apart(workspace, need, *inputs, residual, given, preact)
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     check(lib().nvfp4_fp8_gemm(_ptr(x_codes), _ptr(x_scales), m, k, _ptr(codes), _ptr(scales), n, _ptr(bias), act,
@@ -187,14 +199,15 @@ def _linear(x, x2, up, m, k, codes, scales, bias, workspace, out, activation, re
     dev = x.device
     act = _activation_code(activation)
     given = out
+    inputs = (x2, codes, scales, *(t for t in (up, bias) if t is not None))
     if residual is not None or preact is not None or given is not None:
-        inputs = (x2, codes, scales) if up is None else (x2, up, codes, scales)
         residual = _epilogue_tensors(m, n, dev, residual, preact, given, *inputs)
     if out is None:
         out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
     need = lib().nvfp4_fp8_linear_workspace_bytes(m, k, n)
     if workspace is not None:
         _given_workspace(workspace, dev)
+        _apart(workspace, need, *inputs, residual, given, preact)
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     check(lib().nvfp4_fp8_linear(_ptr(x2), _ptr(up), m, k, _ptr(codes), _ptr(scales), _ptr(bias), n, act, _ptr(residual),
