@@ -261,7 +261,7 @@ class _FP8Fn(torch.autograd.Function):
             codes, scales = fp8_quantize_weight(w)
         b = None if bias is None else bias.detach().to(torch.bfloat16).contiguous()
         z = z_scales = None
-        if activation is not None:
+        if activation is not None and any(ctx.needs_input_grad[:3]):
             z = torch.empty(x.numel() // x.shape[-1], n, dtype=torch.bfloat16, device=x.device)
         r = None if residual is None else residual.detach()
         if x_codes is None and ctx.needs_input_grad[1]:
@@ -292,7 +292,7 @@ class _FP8Fn(torch.autograd.Function):
             # of it would be kept as the gradient, and added to in place
             grad_r = grad_y if grad_y.shape == r_shape else grad_y.reshape(r_shape).clone()
         g = grad_y.reshape(-1, grad_y.shape[-1])
-        if ctx.activation is not None:
+        if z is not None:
             g = ck.activation_backward(g, z if z_scales is None else ck.Checkpoint(z, z_scales), ctx.activation)
         grad_x = grad_w = grad_b = None
         if need_x or need_b:
@@ -332,15 +332,20 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
     if weight.shape[0] % 16:
         raise ValueError(f"fp8_linear_train needs out_features divisible by 16, got {weight.shape[0]}")
     _require_device(x.device, weight=weight, bias=bias, residual=residual)
-    if checkpoint is None:
-        return _FP8Fn.apply(x, weight, bias, None, None, activation, residual)
-    if not isinstance(checkpoint, ck.Checkpoint):
-        raise TypeError("checkpoint must be None or a Checkpoint")
-    codes, scales, rows, k = ck._saved("checkpoint", checkpoint)
-    _require_device(x.device, checkpoint=codes)
-    if checkpoint.rotation_group or k != x.shape[-1] or rows * k != x.numel():
-        raise ValueError(f"checkpoint holds {list(checkpoint.codes.shape)} under rotation group "
-                         f"{checkpoint.rotation_group}; the linear's input is {list(x.shape)} without a rotation")
+    codes = scales = None
+    if checkpoint is not None:
+        if not isinstance(checkpoint, ck.Checkpoint):
+            raise TypeError("checkpoint must be None or a Checkpoint")
+        codes, scales, rows, k = ck._saved("checkpoint", checkpoint)
+        _require_device(x.device, checkpoint=codes)
+        if checkpoint.rotation_group or k != x.shape[-1] or rows * k != x.numel():
+            raise ValueError(f"checkpoint holds {list(checkpoint.codes.shape)} under rotation group "
+                             f"{checkpoint.rotation_group}; the linear's input is {list(x.shape)} without a rotation")
+    if not torch.is_grad_enabled():
+        # an autograd function is told of leaves that require gradients here too, and would keep for them
+        # what no backward pass will read
+        layer = FP8Linear.from_weight(weight, bias)
+        return layer(x, activation, residual)
     return _FP8Fn.apply(x, weight, bias, codes, scales, activation, residual)
 
 
