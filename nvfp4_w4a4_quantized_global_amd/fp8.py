@@ -270,7 +270,7 @@ class _FP8Fn(torch.autograd.Function):
             y = fp8_gemm(q, s, codes, scales, b, activation=activation, preact=z, residual=r).reshape(*x.shape[:-1], n)
         else:
             y = fp8_linear(x, codes, scales, b, activation=activation, preact=z, residual=r)
-        if z is not None and n % 16 == 0:
+        if z is not None:
             z, z_scales, _ = ck.checkpoint_pack(z)
         if not ctx.needs_input_grad[1]:
             x_codes = x_scales = None
@@ -293,7 +293,7 @@ class _FP8Fn(torch.autograd.Function):
             grad_r = grad_y if grad_y.shape == r_shape else grad_y.reshape(r_shape).clone()
         g = grad_y.reshape(-1, grad_y.shape[-1])
         if z is not None:
-            g = ck.activation_backward(g, z if z_scales is None else ck.Checkpoint(z, z_scales), ctx.activation)
+            g = ck.activation_backward(g, ck.Checkpoint(z, z_scales), ctx.activation)
         grad_x = grad_w = grad_b = None
         if need_x or need_b:
             g_codes, g_scales, *total = fp8_quantize_activation(g, column_sum=need_b)
