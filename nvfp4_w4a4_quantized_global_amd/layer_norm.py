@@ -102,13 +102,8 @@ def fp8_quantize_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-
     return (codes, scales) if residual is None else (codes, scales, r)
 
 
-@_on_device
-def layernorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
-                       grad_residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """Gradient of the norm at r (x, or the sum layernorm returned): (grad_r in r's dtype, the
-    gradient of x and of the residual alike; grad_weight and grad_bias fp32 [K]).
-    ``grad_residual``: the gradient that reaches r along the residual stream, of r's dtype, added
-    to grad_r."""
+def _layernorm_backward(grad_y, r, weight, eps, grad_residual, parameters: bool):
+    """layernorm_backward; without ``parameters`` grad_weight and grad_bias are None."""
     gy, *gm = _rows("grad_y", grad_y)
     r2, rows, k = _rows("r", r, None)
     _require_device(gy.device, r=r, grad_residual=grad_residual)
@@ -122,14 +117,26 @@ def layernorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tens
             raise ValueError(f"grad_residual and r must have the same shape, got {list(grad_residual.shape)} and "
                              f"{list(r.shape)}")
     grad_r = torch.empty_like(r2)
-    grad_w = torch.empty(k, dtype=torch.float32, device=r2.device)
-    grad_b = torch.empty_like(grad_w)
-    need = lib().nvfp4_layernorm_backward_workspace_bytes(rows, k)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=r2.device)
+    grad_w = grad_b = ws = None
+    if parameters:
+        grad_w = torch.empty(k, dtype=torch.float32, device=r2.device)
+        grad_b = torch.empty_like(grad_w)
+        need = lib().nvfp4_layernorm_backward_workspace_bytes(rows, k)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=r2.device)
     check(lib().nvfp4_layernorm_backward(_ptr(gy), _ptr(r2), DTYPE_CODES[r2.dtype], _ptr(w), DTYPE_CODES[w.dtype],
                                          _ptr(gr), rows, k, float(eps), _ptr(grad_r), _ptr(grad_w), _ptr(grad_b),
-                                         _ptr(ws), ws.numel(), _stream(r2.device)))
+                                         _ptr(ws), 0 if ws is None else ws.numel(), _stream(r2.device)))
     return grad_r, grad_w, grad_b
+
+
+@_on_device
+def layernorm_backward(grad_y: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                       grad_residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradient of the norm at r (x, or the sum layernorm returned): (grad_r in r's dtype, the
+    gradient of x and of the residual alike; grad_weight and grad_bias fp32 [K]).
+    ``grad_residual``: the gradient that reaches r along the residual stream, of r's dtype, added
+    to grad_r."""
+    return _layernorm_backward(grad_y, r, weight, eps, grad_residual, True)
 
 
 class _LayerNormFn(torch.autograd.Function):
@@ -158,13 +165,15 @@ class _LayerNormFn(torch.autograd.Function):
             # only the residual stream was used
             gx = grad_r
         else:
-            gx, gw, gb = layernorm_backward(grad_y, r, weight, ctx.eps, grad_r)
-            gw = gw.to(wd)
-            gb = None if bd is None else gb.to(bd)
+            need_w, need_b = ctx.needs_input_grad[1:3]
+            gx, gw, gb = _gradients_on_device(grad_y, r, weight, ctx.eps, grad_r, need_w or need_b)
+            gw = gw.to(wd) if need_w else None
+            gb = gb.to(bd) if need_b else None
         return (None if gx is None else gx.to(xd), gw, gb, gx if ctx.has_residual else None, None, None)
 
 
 _layernorm_on_device = _on_device(_layernorm)
+_gradients_on_device = _on_device(_layernorm_backward)
 
 
 def layernorm_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-6,

@@ -76,3 +76,20 @@ def test_a_gradient_behind_the_activation_keeps_it(rec, need):
     assert "nvfp4_checkpoint_pack" in _names(rec)
     transposed = _args(rec, "nvfp4_fp8_quantize_weight")[-3]
     assert (transposed is not None) == (need == "x")
+
+
+@pytest.mark.parametrize("weight,bias", [(False, False), (False, True), (True, False)])
+def test_a_frozen_norm_takes_no_parameter_gradients(rec, monkeypatch, weight, bias):
+    """A norm whose weight and bias are frozen asks the library for the stream's gradient alone."""
+    x, w, b = _leaf(M, K, grad=True), _leaf(K, grad=weight), _leaf(K, grad=bias)
+    r = _leaf(M, K)
+    ctx = type("Ctx", (), dict(saved_tensors=(r, w), dtypes=(BF, BF, BF), eps=1e-6, has_residual=False,
+                               needs_input_grad=(True, weight, bias, False, False, False)))()
+    gx, gw, gb, *rest = layer_norm._LayerNormFn.backward(ctx, on_gpu(torch.ones(M, K, dtype=BF)), None, None, None)
+    args = _args(rec, "nvfp4_layernorm_backward")
+    grads, workspace = args[10:12], args[12:14]
+    if weight or bias:
+        assert None not in grads and workspace[1] > 0
+    else:
+        assert grads == (None, None) and workspace == (None, 0)
+    assert (gw is None) == (not weight) and (gb is None) == (not bias) and gx.shape == x.shape and rest == [None] * 3

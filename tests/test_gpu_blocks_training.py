@@ -85,3 +85,24 @@ def test_each_gradient_alone(act, launches):
         want = {0: ["nvfp4_fp8_quantize_activation", "nvfp4_fp8_gemm"], 1: ["nvfp4_weight_grad"],
                 2: ["nvfp4_fp8_quantize_activation"], 3: []}[i]
         assert backward == ([] if act is None or i == 3 else ["nvfp4_activation_backward"]) + want
+
+
+@pytest.mark.parametrize("k", [48, 1040, 5120])
+@pytest.mark.parametrize("stream", [None, BF, F])
+def test_a_norm_with_frozen_parameters(k, stream):
+    m = 37
+    x = workloads.draw("normal_outliers", (m, k), 340, m).to(DEV)
+    w, b = ((1 + 0.1 * workloads.draw("normal", (k,), 341, i).float()).to(DEV) for i in range(2))
+    res = None if stream is None else workloads.draw("t3", (m, k), 342, m).to(DEV).to(stream)
+    gy = workloads.draw("normal", (m, k), 343, m).to(DEV)
+
+    def grads(*need):
+        t = [leaf.detach().clone().requires_grad_(i in need) for i, leaf in enumerate((x, w, b))]
+        out = nv().layernorm_train(*t, 1e-6, res)
+        y, extra = (out, ()) if res is None else (out[0], (out[1],))
+        return torch.autograd.grad((y, *extra), [t[i] for i in need], (gy, *(torch.ones_like(e) for e in extra)))
+
+    every = grads(0, 1, 2)
+    for need in ((0,), (1,), (2,), (0, 1), (0, 2), (1, 2)):
+        for i, got in zip(need, grads(*need)):
+            assert got.dtype == every[i].dtype and torch.equal(got, every[i])
