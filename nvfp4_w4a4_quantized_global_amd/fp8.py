@@ -156,8 +156,9 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
              preact: torch.Tensor | None = None) -> torch.Tensor:
     """The product of an activation's codes [M, K] and a weight's [N, K]: bf16(act(z) + residual)
     from z = product + bias, in fp32 with that one rounding; [M, N].  (The matrix cores add eight
-    products at a time, cut below 2^-13 of the largest: about 1e-4 of an output.)  ``out``,
-    ``activation``, ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
+    products at a time, cut below 2^-13 of the largest: about 1e-4 of an output.)  The product
+    of two blocks' scales must be an fp32 number (their largest magnitudes multiply to 6.8e43 at
+    most): the output is infinite or NaN otherwise.  ``out``, ``activation``, ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
     fp8_gemm_workspace_bytes is allocated here if not given."""
     _require_cuda("x_codes", x_codes, torch.uint8, 2)
     m, k = x_codes.shape
