@@ -246,8 +246,8 @@ def fp8_linear_swiglu(gate: torch.Tensor, up: torch.Tensor, codes: torch.Tensor,
 class _FP8Fn(torch.autograd.Function):
     """Forward: the master weight's codes, made afresh (it changes every step), and fp8_linear.
     Backward, quantization taken as the identity: the gradient g before the activation is quantized
-    to blocks along N and multiplied by the transposed weight codes (grad_x); grad_W = g^T x from the
-    input's 8-bit checkpoint (:func:`weight_grad`); grad_b = sum of g over rows, taken in the pass
+    to blocks along N and multiplied by the transposed weight codes (grad_x); grad_W = g^T x in bf16,
+    g not quantized, x the values of its 8-bit checkpoint (:func:`weight_grad`); grad_b = sum of g over rows, taken in the pass
     that quantizes it.  The residual's gradient is grad_y."""
 
     @staticmethod
@@ -314,10 +314,12 @@ def fp8_linear_train(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor |
     """Differentiable :func:`fp8_linear` on a full-precision master weight [out, in] (``out`` and
     ``in`` multiples of 16), its 8-bit codes made at every call; ``x`` is cast to bf16.
 
-    All three products run on the matrix cores from 8-bit operands: the input's gradient from the
-    quantized gradient of the output, the weight's (at the values of) the 8-bit checkpoint of x, which
-    is all that is kept of it: ``checkpoint`` shares one (of :func:`layernorm_train`,
-    :func:`rmsnorm_train` or :func:`checkpoint_pack`), None packs it here, with x's codes.  ``activation`` and
+    The output and the input's gradient are products of 8-bit blocks (of the weight with x, and with
+    the output's gradient, quantized); the weight's gradient is a bf16 product of the output's
+    gradient, not quantized, with the values of x's 8-bit checkpoint (:func:`weight_grad`), which is
+    all that is kept of x: ``checkpoint`` shares one (of :func:`layernorm_train`,
+    :func:`rmsnorm_train` or :func:`checkpoint_pack`), None packs it here, with x's codes.  Without
+    gradients (``torch.no_grad``) it is :func:`fp8_linear`, and keeps nothing.  ``activation`` and
     ``residual`` (bf16, gets its gradient too) as for :func:`nvfp4_linear_train`, the activation's
     gradient at z in 8 bits.
 
