@@ -532,12 +532,19 @@ hipError_t launch_layernorm(NormForward a, bool mean, hipStream_t s) {
   const RowShape shape = row_shape(a.k);
   a.lanes = shape.lanes;
   const int64_t per = shape.threads / shape.lanes;
-  // Workgroups of more than four waves walk down the rows with the weight and bias in registers, two
-  // for each compute unit (of 16 waves, which those of five leave room in); others take their rows at
-  // once, the rest by the row loop.  To 8-bit codes, 4096 x 5120 with 512 workgroups 41.2 us, 768 47.3,
-  // 4096 48.8; 4096 x 4096 (four waves) 512 33.8, 4096 31.8; 2000 x 2064 512 15.4, 2000 13.2.
-  const bool walks = shape.lanes > 256;
-  int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, walks ? 512 : 1 << 20);
+  // Workgroups of more than four waves walk down the rows with the weight and bias in registers; others
+  // take their rows at once, the rest by the row loop.  Two walkers for each compute unit, which has room
+  // for 16 waves of the layer norm's; four of the RMS norm's, which has for 28, with up to eight waves and
+  // nothing in fp32 to read (above, or with it, traffic is the bound either way).  Layer norm, bf16 stream
+  // with a residual, to bf16, with 512 / 768 / 1024 workgroups and one for every row: 600 x 5120 10.3 / - / - /
+  // 11.1 us, 768 11.4 / - / - / 12.3, 1000 13.6 / 15.5 / - / 17.5, 2048 21.9 / 23.6 / 27.0 / 27.1, 4096 37.3 / 43.3 /
+  // 46.0 / 47.1; to 8-bit codes 600 10.2 and 10.7, 1000 14.9 and 18.0, 4096 40.2 / 46.8 / 49.8 / 47.9; 1000 x 16384
+  // 35.1 and 40.4; 4096 x 4096 (four waves) 33.8 and, one for every row, 31.8.  RMS norm to 8-bit codes, 512 /
+  // 768 / 1024 / all: 1000 x 5120 13.3 / 12.4 / - / 12.4, 4096 35.6 / 33.0 / 33.1 / 34.3, 4096 x 8192 50.7 / 50.2 / 50.7 /
+  // 50.2, x 16384 96.5 / 97.7 / 99.2 / 108.6; with an fp32 residual 4096 x 5120 51.5 / 52.0 / 52.4 / 53.6.
+  const bool f32 = a.x_f32 || (a.residual != nullptr && a.stream_f32);
+  const int64_t walkers = !mean && !f32 && shape.lanes <= 512 ? 1024 : 512;
+  int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, shape.lanes > 256 ? walkers : 1 << 20);
   if (a.mode == kNormDynamic) {
     // one row needs no second pass: its workgroup knows the whole abs-max
     a.mode = a.rows == 1 ? kNormOneRow : kNormStats;
