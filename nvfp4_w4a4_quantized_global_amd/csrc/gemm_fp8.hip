@@ -450,10 +450,20 @@ constexpr int kWaves = 8;
 constexpr int kFusedRows = 4;
 constexpr int kFusedLds = 60 * 1024;
 
-// Blocks of K in flight per wave.  Measured with the first figure 3, 4 and 6 (and the others in
-// proportion): one row, 5120 -> 25600 26.7, 28.3, 30.9 us; 16 rows, 25600 -> 5120 39.6, 41.2, 41.8;
-// 64 rows, 25600 -> 5120 with one block in flight 89, with two 73.
-constexpr int skinny_depth(int ta, int tb) { return ta + tb <= 2 ? 3 : ta + tb <= 3 || ta + tb == 6 ? 2 : 1; }
+// Blocks of K in flight per wave; eight waves a compute unit hide most of a load by themselves, and more
+// registers each only get in their way.  Given codes: one, but two for 64 rows by two tiles of weight
+// rows, whose eight MFMAs a block leave the loads behind.  Where the rows are quantized in front of the
+// loop the first blocks arrive meanwhile: about three tiles' worth.  us with one / two / three in flight:
+//   codes, 1 x 1 tiles (16 x 5120 -> 4096) 8.5 / 9.1 / 9.3, 1 x 2 (16 x 25600 -> 5120) 33.1 / 34.9 / 36.8, 1 x 4 (16 x 1024
+//   -> 25600) 10.7 / 13.6 / 16.4, 2 x 1 (32 x 5120 -> 1024) 8.9 / 9.5 / 9.8, 2 x 2 (32 x 5120 -> 5120) 12.8 / 14.0 / 14.1,
+//   2 x 4 (32 x 5120 -> 25600) 39.9 / 42.4 / 69.6, 4 x 1 (64 x 1024 -> 4096) 6.0 / 7.2 / 8.6, 4 x 2 (64 x 5120 -> 5120)
+//   20.9 / 19.9 / 35.8, (64 x 5120 -> 8192) 22.8 / 21.8 / 38.4, but (64 x 1024 -> 8192) 7.2 / 8.6 / 17.9;
+//   one row quantized in the kernel, 1 x 1 (5120 -> 4096) 7.9 / 7.6 / 7.3, 1 x 2 (5120 -> 8192) 11.0 / 10.5 / 10.5,
+//   1 x 4 (5120 -> 25600) 26.1 / 27.8 / 30.0.
+constexpr int skinny_depth(int ta, int tb, bool fused) {
+  if (fused) return tb == 1 ? 3 : tb == 2 ? 2 : 1;
+  return ta == 4 && tb == 2 ? 2 : 1;
+}
 
 template <int kTA, int kTB, bool kFused>
 __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_fp8_skinny_kernel(
     int64_t k, const uint8_t* __restrict__ w_codes, const float* __restrict__ w_scales, int64_t n, int nrows,
     const uint16_t* __restrict__ bias, uint16_t* out, const Epilogue ep) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int kDepth = skinny_depth(kTA, kTB);   // blocks in flight
+  constexpr int kDepth = skinny_depth(kTA, kTB, kFused);
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * nrows;
