@@ -16,8 +16,8 @@
 // power-of-two group of lanes or a workgroup of its own; one read, one write.
 //
 // All of it is bound by HBM traffic.  4096 x 5120 with a bf16 residual and fp32 weights, each call
-// on other tensors (a 1 GiB copy reaches 5.06 TB/s): bf16 y and r 36.9 us, 4.55 TB/s; 8-bit codes and
-// r 40.9 us, 3.6 TB/s (RMS norm 36.1); with the checkpoint 43.9 us, 4.3 TB/s.  One row: 4.3 us,
+// on other tensors (a 1 GiB copy reaches 5.06 TB/s): bf16 y and r 37.3 us, 4.5 TB/s; 8-bit codes and
+// r 40.2 us, 3.7 TB/s (RMS norm 33.1); with the checkpoint 43.9 us, 4.3 TB/s.  One row: 4.3 us,
 // a launch and its one read.
 // (Neighbouring rows kept on one XCD, so that the block-major scales of 16 rows meet in its L2, give
 // 2 % on 4096 x 5120 to 8-bit codes and take 9 % at 16384 x 1024: rows go out in launch order.)
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kNormQThreads) layernorm_quantize_kernel(const
 // Each workgroup walks its rows with its lanes' 16 columns of grad_w and grad_b in registers and
 // writes one partial row of both; layernorm_weight_grad_kernel adds the partials in a fixed order.
 //
-// 16384 x 1024 in bf16 26.8 us (5.0 TB/s), 4091 x 5120 with an fp32 stream 61.4 us (4.8 TB/s), and
-// 5.2 us for the partials' sums.  Shuffles through LDS in place of lane moves: 61 and 142 us.
+// 16384 x 1024 in bf16 28.2 us (4.8 TB/s), 4091 x 5120 with an fp32 stream 64.8 us (4.5 TB/s), and
+// 4.0 and 5.5 us for the partials' sums.  Shuffles through LDS in place of lane moves: 61 and 142 us.
 // (Eight values a lane, in half the registers, take twice the waves per row and as many sums for
 // half the work: with shuffles still, 16384 x 1024 61 us against 45, 4091 x 5120 in fp32 93 against 75.)
 template <bool kSF32, bool kWF32, bool kRes>

@@ -156,10 +156,12 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor,
              preact: torch.Tensor | None = None) -> torch.Tensor:
     """The product of an activation's codes [M, K] and a weight's [N, K]: bf16(act(z) + residual)
     from z = product + bias, in fp32 with that one rounding; [M, N].  (The matrix cores add eight
-    products at a time, cut below 2^-13 of the largest: about 1e-4 of an output.)  The product
-    of two blocks' scales must be an fp32 number (their largest magnitudes multiply to 6.8e43 at
-    most): the output is infinite or NaN otherwise.  ``out``, ``activation``, ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
-    fp8_gemm_workspace_bytes is allocated here if not given."""
+    products at a time, cut below 2^-13 of the largest: 1.4e-5 of the outputs' norm on normal
+    values.)  The product of two blocks' scales must be an fp32 number (their largest magnitudes
+    multiply to 6.8e43 at most): the output is infinite or NaN otherwise.  ``out``, ``activation``,
+    ``residual`` and ``preact`` as for :func:`nvfp4_linear`; the workspace of
+    fp8_gemm_workspace_bytes is allocated here if not given.  Outputs may not overlap what the call
+    reads, nor a given workspace either."""
     _require_cuda("x_codes", x_codes, torch.uint8, 2)
     m, k = x_codes.shape
     _scales("x_scales", x_scales, (_blocks(k), m))
@@ -247,8 +249,8 @@ class _FP8Fn(torch.autograd.Function):
     """Forward: the master weight's codes, made afresh (it changes every step), and fp8_linear.
     Backward, quantization taken as the identity: the gradient g before the activation is quantized
     to blocks along N and multiplied by the transposed weight codes (grad_x); grad_W = g^T x in bf16,
-    g not quantized, x the values of its 8-bit checkpoint (:func:`weight_grad`); grad_b = sum of g over rows, taken in the pass
-    that quantizes it.  The residual's gradient is grad_y."""
+    g not quantized, x the values of its 8-bit checkpoint (:func:`weight_grad`); grad_b = sum of g
+    over rows, taken in the pass that quantizes it.  The residual's gradient is grad_y."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, x_codes, x_scales, activation, residual):
