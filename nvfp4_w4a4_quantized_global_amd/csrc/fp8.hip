@@ -2,9 +2,9 @@
 // weights in tiles of 128 x 128 (with their transposed copy for the input's gradient), and back.
 // All of it is bound by HBM traffic (a 1 GiB copy: 5.06 TB/s): 4096 x 5120 from bf16 11.4 us
 // (5.5 TB/s, from the last-level cache in part), with column sums 13.3 + 3.9, with the checkpoint
-// 15.1 to 17.6 (4.8 to 5.6; in two calls 27); the SwiGLU product of 4096 x 25600 139 us (131 to 152; 3.8; fewer
-// and longer workgroups are slower); a weight 25600 x 5120 from fp32 123 us (5.3), with the transposed copy
-// 150 (5.3), that from bf16 104 (5.0); back to bf16 70 us (5.6).
+// 15.1 to 17.6 (4.8 to 5.6; in two calls 27); the SwiGLU product of 4096 x 25600 139 us (131 to 152; 3.8
+// TB/s; fewer and longer workgroups are slower); a weight 25600 x 5120 from fp32 123 us (5.3), with the
+// transposed copy 150 (5.3), that from bf16 104 (5.0); back to bf16 70 us (5.6).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

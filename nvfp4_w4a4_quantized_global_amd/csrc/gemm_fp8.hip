@@ -138,9 +138,9 @@ __device__ __forceinline__ void sub_tile_coords(int u, int tile0, int tiles_m, i
 }
 
 // 8192 x 8192 -> 8192 460 us, 2.39 PFLOP/s, and 352 on zeros, where the clock does not fall (428 to 464 us
-// by box).  A library product of the same codes with one scale a tensor takes 348 (3.16 PFLOP/s; 299 on
-// zeros): power costs both about as much, and the rest is this loop's, which keeps the matrix cores busy
-// 53 to 64 % of the cycles.  4096 x 5120 -> 25600 500 us, 37 of them the quarter tiles'; 4091 x 1024 -> 4096
+// by box).  A library product of the same codes with one scale a tensor takes 348 (3.16 PFLOP/s), and 299
+// on zeros: half of the difference is this loop's cycles, of which the matrix cores are busy in 53 to
+// 64 %, the other half its power.  4096 x 5120 -> 25600 500 us, 37 of them the quarter tiles'; 4091 x 1024 -> 4096
 // with gelu 32.0 us, of which 12 are the loop over K, and the rest the output's 33.5 MB and the
 // activation, which nothing overlaps in a launch of one round.
 //
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(256) gemm_fp8_reduce(const float* __restrict__
 // A workgroup owns `nrows` weight rows (a multiple of 4), up to kTB MFMA tiles of 16: an equal
 // share for every compute unit, so that none streams twice what another does.  Its waves take the
 // blocks of K in turn, so that together they read runs of kWaves * 128 bytes of each row; each
-// multiplies its blocks with kTA tiles of 16 activation rows, several blocks' loads in flight, and
+// multiplies its blocks with kTA tiles of 16 activation rows, the next blocks' loads in flight, and
 // the waves' sums meet in LDS.  kFused (one activation tile): x is bf16 (or gate, with up), and
 // each wave first quantizes its own blocks of the m rows into LDS.
 // Bound by the weight's stream: one row 5120 -> 25600 25.3 us (5.2 TB/s), 25600 -> 5120 28.4 us (4.6);
@@ -456,11 +456,12 @@ constexpr int kFusedLds = 60 * 1024;
 // registers each only get in their way.  Given codes: one, but two for 64 rows by two tiles of weight
 // rows, whose eight MFMAs a block leave the loads behind.  Where the rows are quantized in front of the
 // loop the first blocks arrive meanwhile: about three tiles' worth.  us with one / two / three in flight:
-//   codes, 1 x 1 tiles (16 x 5120 -> 4096) 8.5 / 9.1 / 9.3, 1 x 2 (16 x 25600 -> 5120) 33.1 / 34.9 / 36.8, 1 x 4 (16 x 1024
-//   -> 25600) 10.7 / 13.6 / 16.4, 2 x 1 (32 x 5120 -> 1024) 8.9 / 9.5 / 9.8, 2 x 2 (32 x 5120 -> 5120) 12.8 / 14.0 / 14.1,
-//   2 x 4 (32 x 5120 -> 25600) 39.9 / 42.4 / 69.6, 4 x 1 (64 x 1024 -> 4096) 6.0 / 7.2 / 8.6, 4 x 2 (64 x 5120 -> 5120)
-//   20.9 / 19.9 / 35.8, (64 x 5120 -> 8192) 22.8 / 21.8 / 38.4, but (64 x 1024 -> 8192) 7.2 / 8.6 / 17.9;
-//   one row quantized in the kernel, 1 x 1 (5120 -> 4096) 7.9 / 7.6 / 7.3, 1 x 2 (5120 -> 8192) 11.0 / 10.5 / 10.5,
+//   codes: 1 x 1 tiles (16 x 5120 -> 4096) 8.5 / 9.1 / 9.3, 1 x 2 (16 x 25600 -> 5120) 33.1 / 34.9 / 36.8,
+//   1 x 4 (16 x 1024 -> 25600) 10.7 / 13.6 / 16.4, 2 x 1 (32 x 5120 -> 1024) 8.9 / 9.5 / 9.8,
+//   2 x 2 (32 x 5120 -> 5120) 12.8 / 14.0 / 14.1, 2 x 4 (32 x 5120 -> 25600) 39.9 / 42.4 / 69.6,
+//   4 x 1 (64 x 1024 -> 4096) 6.0 / 7.2 / 8.6, 4 x 2 (64 x 5120 -> 5120) 20.9 / 19.9 / 35.8,
+//   (64 x 5120 -> 8192) 22.8 / 21.8 / 38.4, but (64 x 1024 -> 8192) 7.2 / 8.6 / 17.9;
+//   one row quantized here: 1 x 1 (5120 -> 4096) 7.9 / 7.6 / 7.3, 1 x 2 (5120 -> 8192) 11.0 / 10.5 / 10.5,
 //   1 x 4 (5120 -> 25600) 26.1 / 27.8 / 30.0.
 constexpr int skinny_depth(int ta, int tb, bool fused) {
   if (fused) return tb == 1 ? 3 : tb == 2 ? 2 : 1;

@@ -107,3 +107,20 @@ def test_repeats_bit_for_bit_at_the_extremes():
     gy, w = workloads.draw("normal", (m, k), 321, 1).to(DEV), torch.ones(k, device=DEV)
     a, b = (nv().layernorm_backward(gy, r.to(DEV), w, 0.0) for _ in range(2))
     assert all(torch.equal(x, y) and x.isfinite().all() for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("k", [48, 1040, 16384])
+@pytest.mark.parametrize("at", [0, -1])
+def test_the_largest_gradients(k, at):
+    """|grad_y w| up to 1e36, with the signs of the row and half its spread in one value: n mean(g n) is then
+    as large as it gets, sqrt(k) / 2 times the gradient."""
+    m = 3
+    r = torch.sign(workloads.draw("normal", (m, k), 330, k).float() + 1e-3)
+    r[:, at] = k ** 0.5
+    r *= torch.tensor([1e3, 1e10, 1e30])[:, None]
+    gy = (9.8e35 * torch.sign(r - r.mean(-1, keepdim=True))).to(BF)
+    w = torch.ones(k)
+    assert float(gy.float().abs().max()) < 1e36
+    got = nv().layernorm_backward(gy.to(DEV), r.to(DEV), w.to(DEV), 1e-6)
+    assert got[0].isfinite().all()
+    _check(got, gy, r, w, 1e-6, None)
